@@ -409,3 +409,9 @@ def paro_linear_batch(calls, out_dtype=None, outs=None, ws=None):
         _check(_lib.paro_linear_batch(n, arr, _ydt(ys[0]), _ptr(ws), ws.numel() if ws is not None else 0,
                                       _stream_ptr(device)), "paro_linear_batch")
     return ys
+
+
+# The 8-bit path (include/paro_w8a8.h), beside the W4A16 one.
+from .w8a8 import (BF16, EXPORTS_W8A8, paro_dequantize_q8, paro_pack_weights_q8, paro_quantize_q8,  # noqa: E402,F401
+                   paro_rmsnorm, paro_rmsnorm_q8, paro_w8a8_gated_linear, paro_w8a8_gated_workspace_bytes,
+                   paro_w8a8_linear, paro_w8a8_workspace_bytes)

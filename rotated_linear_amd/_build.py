@@ -26,9 +26,10 @@ COMMON = [
 ]
 # per-file extras: the build-time pack must round every float64 product and sum on its own
 # the GEMM keeps its accumulators in architectural registers (the per-group rescale multiplies them)
-EXTRA = {"pack.hip": ["-ffp-contract=off"], "gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+EXTRA = {"pack.hip": ["-ffp-contract=off"], "q8_pack.hip": ["-ffp-contract=off"], "gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "skinny.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
-SOURCES = ["paro_api.cpp", "schedule.cpp", "pack.hip", "rotate.hip", "decode.hip", "gemm.hip", "skinny.hip", "noalloc.hip"]
+SOURCES = ["paro_api.cpp", "schedule.cpp", "pack.hip", "rotate.hip", "decode.hip", "gemm.hip", "skinny.hip", "noalloc.hip",
+           "q8_api.cpp", "q8_rows.hip", "q8_rotate.hip", "q8_pack.hip", "w8a8.hip"]
 
 
 def _hipcc() -> str:

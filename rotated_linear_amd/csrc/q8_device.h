@@ -1,0 +1,74 @@
+// Device helpers of the 8-bit path: 16-bit element conversions, the row quantiser's last step and
+// the gated activation.
+#pragma once
+
+#include "q8_internal.h"
+
+namespace paro {
+
+// Element types of rows (DT: PARO_F16, PARO_BF16, PARO_F32): float32 values to and from storage.
+template <int DT>
+__device__ inline float from_bits16(uint32_t h) {  // the element in the low 16 bits of h
+  if constexpr (DT == PARO_F16) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(h)));
+  } else {
+    return __builtin_bit_cast(float, h << 16);
+  }
+}
+template <int DT>
+__device__ inline uint32_t to_bits16(float v) {  // rounded to nearest, ties to even
+  if constexpr (DT == PARO_F16) {
+    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+  } else {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+  }
+}
+template <int DT>
+__device__ inline void unpack8(const u32x4& w, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = from_bits16<DT>(w[i] & 0xFFFFu);
+    f[2 * i + 1] = DT == PARO_F16 ? from_bits16<DT>(w[i] >> 16) : __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
+  }
+}
+template <int DT>
+__device__ inline u32x4 pack8(const float (&f)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = to_bits16<DT>(f[2 * i]) | (to_bits16<DT>(f[2 * i + 1]) << 16);
+  return w;
+}
+
+// |v| as an ordered integer: larger for larger magnitudes, an infinity above every number and a
+// NaN above that, so a maximum over a row keeps both.
+__device__ inline uint32_t abs_order(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }
+constexpr uint32_t kAbsInf = 0x7F800000u;
+
+// The row quantiser's scale and code step from the row's largest magnitude (as abs_order): codes
+// are rint(v * step). A row with an infinity or a NaN: scale NaN and `bad` (codes 0).
+struct RowQuant {
+  float scale, step;
+  bool bad;
+};
+__device__ inline RowQuant row_quant(uint32_t top) {
+  RowQuant r;
+  r.bad = top >= kAbsInf;
+  const float c = fmaxf(__builtin_bit_cast(float, top), kQ8MinTop);
+  r.scale = r.bad ? __builtin_nanf("") : c / kQ8Max;
+  r.step = kQ8Max / c;
+  return r;
+}
+// Four codes as one word (|v * step| <= 127 (1 + 2^-23): rint never passes 127).
+__device__ inline uint32_t codes4(const float (&v)[4], float step) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= (uint32_t(int(__builtin_rintf(v[i] * step))) & 0xFFu) << (8 * i);
+  return w;
+}
+
+// silu(g) u = g u / (1 + exp(-g)); exp(-g) past float32 gives an infinity and the quotient -0.
+__device__ inline float silu_mul(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896f)) * u;
+}
+
+}  // namespace paro

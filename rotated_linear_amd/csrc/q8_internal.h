@@ -1,0 +1,51 @@
+// Internal declarations of the 8-bit path (include/paro_w8a8.h).
+#pragma once
+
+#include "paro_internal.h"
+#include "paro_w8a8.h"
+
+namespace paro {
+
+constexpr float kQ8Max = 127.0f;
+// Smallest row maximum a scale is made from (2^-100): 127 / it and the scale stay normal float32.
+constexpr float kQ8MinTop = 0x1p-100f;
+
+// Rows of 16-bit elements, read as the library's own vector types.
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+using i32x4 = int __attribute__((ext_vector_type(4)));
+using i32x16 = int __attribute__((ext_vector_type(16)));
+
+struct NormArgs {
+  int M, D, dtype;
+  const void* x;
+  const void* residual;  // nullptr: none
+  const void* gamma;
+  float eps;
+  void* residual_out;
+  void* y;       // 16-bit output, or
+  int8_t* q;     // codes and
+  float* scales; // scales
+};
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st);
+hipError_t launch_quantize_q8(int M, int D, int dtype, const void* x, int8_t* q, float* scales, hipStream_t st);
+hipError_t launch_dequantize_q8(int M, int D, const int8_t* q, const float* scales, void* x, int dtype, hipStream_t st);
+// The row quantiser behind the transform R.
+hipError_t launch_rotate_q8(const DevRot& R, int M, int dtype, const void* x, int8_t* q, float* scales, hipStream_t st);
+// R.K == 0 and R.s == nullptr: no transform.
+hipError_t launch_pack_q8(const DevRot& R, int N, int dtype, const void* W, int8_t* q, float* scales, hipStream_t st);
+
+// One 8-bit product: y [M][N], or with `gated` y [M][N] = silu(gate) * up from weights [2N][D].
+struct W8A8Call {
+  int M, D, N;
+  bool gated;
+  const int8_t* x;
+  const float* xs;
+  const int8_t* w;
+  const float* ws;
+  void* y;
+  int ydtype;
+};
+size_t w8a8_workspace_bytes(int M, int D, int N, bool gated);
+hipError_t launch_w8a8(const W8A8Call& c, void* work, hipStream_t st);
+
+}  // namespace paro

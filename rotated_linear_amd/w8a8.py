@@ -1,0 +1,243 @@
+"""Python binding of the 8-bit path (include/paro_w8a8.h): residual RMS norm, row quantisation,
+8-bit weights and the W8A8 products. Argument marshalling only, as in the package; the names mirror
+the C ABI. Decode-sized calls take a few microseconds on the GPU, so the checks that pass take one
+comparison each and only a failing one goes through the package's checkers for its message.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import F16, F32, GROUP, MAX_D, ParoError, _check, _i, _lib, _on_gpu, _sz, _vp, _want, _want_ws, paro_rotation
+
+BF16 = 2
+_DTYPE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+_ROWS = (torch.float16, torch.bfloat16)
+
+_rot_p = ctypes.POINTER(paro_rotation)
+_f = ctypes.c_float
+_SIGNATURES = {
+    "paro_rmsnorm_q8": (_i, [_i, _i, _i, _vp, _vp, _vp, _f, _vp, _vp, _vp, _vp]),
+    "paro_rmsnorm": (_i, [_i, _i, _i, _vp, _vp, _vp, _f, _vp, _vp, _vp]),
+    "paro_quantize_q8": (_i, [_rot_p, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "paro_dequantize_q8": (_i, [_i, _i, _vp, _vp, _vp, _i, _vp]),
+    "paro_pack_weights_q8": (_i, [_rot_p, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "paro_w8a8_workspace_bytes": (_sz, [_i, _i, _i]),
+    "paro_w8a8_linear": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
+    "paro_w8a8_gated_workspace_bytes": (_sz, [_i, _i, _i]),
+    "paro_w8a8_gated_linear": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
+}
+for _name, (_res, _args) in _SIGNATURES.items():
+    getattr(_lib, _name).restype = _res
+    getattr(_lib, _name).argtypes = _args
+EXPORTS_W8A8 = tuple(_SIGNATURES)
+
+
+def _ok(t, dtype, shape, name):
+    """A tensor argument of this dtype and shape, contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        _want(t, dtype, shape, name)
+
+
+def _rows(t, name):
+    """A 2-d tensor of float16 or bfloat16 rows: its sizes."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _ROWS:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.shape
+
+
+def _channels(D):
+    if D % GROUP or not GROUP <= D <= MAX_D:
+        raise ParoError(2, "D")
+
+
+def _device(**named):
+    """The one GPU that every given tensor is on."""
+    dev = None
+    for t in named.values():
+        if t is not None:
+            if dev is None:
+                dev = t.device
+            if t.device != dev or not t.is_cuda:
+                return _on_gpu(named)
+    return dev
+
+
+def _call(fn, what, dev, *args):
+    """fn(*args, current stream of dev), with dev current; raises ParoError on an error status."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st:
+        _check(st, what)
+
+
+def _q8_out(out, M, D, names=("q", "scales")):
+    """Check a given (codes, scales) pair of outputs."""
+    if out is None:
+        return None, None
+    q, sc = out
+    _ok(q, torch.int8, (M, D), names[0])
+    _ok(sc, torch.float32, (M,), names[1])
+    return q, sc
+
+
+def _norm(x, gamma, residual, residual_out):
+    """Check a norm's operands: (M, D)."""
+    M, D = _rows(x, "x")
+    _channels(D)
+    _ok(gamma, x.dtype, (D,), "gamma")
+    if residual is not None:
+        _ok(residual, x.dtype, (M, D), "residual")
+        if residual_out is not None:
+            _ok(residual_out, x.dtype, (M, D), "residual_out")
+    elif residual_out is not None:
+        raise ValueError("residual_out without residual")
+    return M, D
+
+
+def _p(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def paro_rmsnorm_q8(x, gamma, eps=1e-6, residual=None, out=None, residual_out=None):
+    """h = x + residual (rounded to x's type), then the RMS norm of h times gamma in 8 bits:
+    (q int8 [M][D], scales float32 [M], h). x, residual float16 or bfloat16 [M][D], gamma [D] of
+    that type. ``out``: an optional (q, scales) pair to write; ``residual_out``: where h goes (it
+    may be ``residual`` itself). Without ``residual``, h is None."""
+    M, D = _norm(x, gamma, residual, residual_out)
+    q, sc = _q8_out(out, M, D)
+    dev = _device(x=x, gamma=gamma, residual=residual, residual_out=residual_out, q=q, scales=sc)
+    if q is None:
+        q = torch.empty((M, D), dtype=torch.int8, device=dev)
+        sc = torch.empty(M, dtype=torch.float32, device=dev)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    _call(_lib.paro_rmsnorm_q8, "paro_rmsnorm_q8", dev, M, D, _DTYPE[x.dtype], x.data_ptr(), _p(residual),
+          gamma.data_ptr(), eps, _p(residual_out), q.data_ptr(), sc.data_ptr())
+    return q, sc, residual_out
+
+
+def paro_rmsnorm(x, gamma, eps=1e-6, residual=None, out=None, residual_out=None):
+    """The same norm with its rows in x's type, as paro_rotate and the W4A16 linears read them:
+    (y [M][D], h). ``out``: an optional tensor for y."""
+    M, D = _norm(x, gamma, residual, residual_out)
+    if out is not None:
+        _ok(out, x.dtype, (M, D), "out")
+    dev = _device(x=x, gamma=gamma, residual=residual, residual_out=residual_out, out=out)
+    y = torch.empty_like(x) if out is None else out
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(residual)
+    _call(_lib.paro_rmsnorm, "paro_rmsnorm", dev, M, D, _DTYPE[x.dtype], x.data_ptr(), _p(residual), gamma.data_ptr(),
+          eps, _p(residual_out), y.data_ptr())
+    return y, residual_out
+
+
+def _quantize(fn, name, what, x, rot, out, out_names):
+    M, D = _rows(x, what)
+    _channels(D)
+    if rot is not None and rot.D != D:
+        raise ValueError(f"{what} has {D} channels, the transform {rot.D}")
+    q, sc = _q8_out(out, M, D, out_names)
+    dev = _device(**{what: x, out_names[0]: q, out_names[1]: sc, "transform": None if rot is None else rot.desc})
+    if q is None:
+        q = torch.empty((M, D), dtype=torch.int8, device=dev)
+        sc = torch.empty(M, dtype=torch.float32, device=dev)
+    _call(fn, name, dev, None if rot is None else rot.ptr, M, D, _DTYPE[x.dtype], x.data_ptr(), q.data_ptr(),
+          sc.data_ptr())
+    return q, sc
+
+
+def paro_quantize_q8(x, rot=None, out=None):
+    """Rows of x (float16 or bfloat16 [M][D]) in 8 bits: (q int8 [M][D], scales float32 [M]). With
+    ``rot`` (a Rotation) the rows are transformed first, as paro_rotate does, in float32."""
+    return _quantize(_lib.paro_quantize_q8, "paro_quantize_q8", "x", x, rot, out, ("q", "scales"))
+
+
+def paro_pack_weights_q8(W, rot=None, out=None):
+    """Weights W (float16 or bfloat16 [N][D]) in 8 bits for the W8A8 linears: (qweight int8 [N][D],
+    scales float32 [N]). With ``rot`` its transform is folded in first (build time, float64)."""
+    return _quantize(_lib.paro_pack_weights_q8, "paro_pack_weights_q8", "W", W, rot, out, ("qweight", "scales"))
+
+
+def paro_dequantize_q8(q, scales, out_dtype=torch.float16, out=None):
+    """The rows that 8-bit codes stand for: q * scales in float16, bfloat16 or float32."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 2:
+        raise ValueError("q must be a torch.Tensor with two dimensions")
+    M, D = q.shape
+    _ok(q, torch.int8, (M, D), "q")
+    _ok(scales, torch.float32, (M,), "scales")
+    _channels(D)
+    if out is not None:
+        out_dtype = out.dtype
+        _ok(out, out_dtype, (M, D), "out")
+    if out_dtype not in _DTYPE:
+        raise TypeError(f"the output must be float16, bfloat16 or float32, got {out_dtype}")
+    dev = _device(q=q, scales=scales, out=out)
+    x = torch.empty((M, D), dtype=out_dtype, device=dev) if out is None else out
+    _call(_lib.paro_dequantize_q8, "paro_dequantize_q8", dev, M, D, q.data_ptr(), scales.data_ptr(), x.data_ptr(),
+          _DTYPE[out_dtype])
+    return x
+
+
+def paro_w8a8_workspace_bytes(M: int, D: int, N: int) -> int:
+    return _lib.paro_w8a8_workspace_bytes(M, D, N)
+
+
+def paro_w8a8_gated_workspace_bytes(M: int, D: int, F: int) -> int:
+    return _lib.paro_w8a8_gated_workspace_bytes(M, D, F)
+
+
+def _linear(fn, name, need_fn, gated, x, x_scales, qweight, w_scales, out_dtype, out, ws):
+    for t, what in ((x, "x"), (qweight, "qweight")):
+        if not isinstance(t, torch.Tensor) or t.dim() != 2:
+            raise ValueError(f"{what} must be a torch.Tensor with two dimensions")
+    (M, D), rows = x.shape, qweight.shape[0]
+    _ok(x, torch.int8, (M, D), "x")
+    _ok(qweight, torch.int8, (rows, D), "qweight")
+    _ok(x_scales, torch.float32, (M,), "x_scales")
+    _ok(w_scales, torch.float32, (rows,), "w_scales")
+    _channels(D)
+    if gated and rows % 2:
+        raise ValueError(f"qweight must hold as many gate rows as up rows, got {rows} rows")
+    N = rows // 2 if gated else rows
+    dtype = out_dtype or (out.dtype if out is not None else torch.float16)
+    if dtype not in _DTYPE:
+        raise TypeError(f"the output must be float16, bfloat16 or float32, got {dtype}")
+    if out is not None:
+        _ok(out, dtype, (M, N), "out")
+    _want_ws(ws)
+    dev = _device(x=x, x_scales=x_scales, qweight=qweight, w_scales=w_scales, out=out, ws=ws)
+    y = torch.empty((M, N), dtype=dtype, device=dev) if out is None else out
+    if ws is None:
+        need = need_fn(M, D, N)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call(fn, name, dev, M, D, N, x.data_ptr(), x_scales.data_ptr(), qweight.data_ptr(), w_scales.data_ptr(),
+          y.data_ptr(), _DTYPE[dtype], _p(ws), 0 if ws is None else ws.numel())
+    return y
+
+
+def paro_w8a8_linear(x, x_scales, qweight, w_scales, out_dtype=None, out=None, ws=None):
+    """y = x . qweight^T with x_scales per row and w_scales per column: x int8 [M][D], x_scales
+    float32 [M], qweight int8 [N][D], w_scales float32 [N]; y float16 (default), bfloat16 or
+    float32 [M][N]. ``ws``: an optional workspace of paro_w8a8_workspace_bytes(M, D, N) bytes."""
+    return _linear(_lib.paro_w8a8_linear, "paro_w8a8_linear", _lib.paro_w8a8_workspace_bytes, False, x, x_scales,
+                   qweight, w_scales, out_dtype, out, ws)
+
+
+def paro_w8a8_gated_linear(x, x_scales, qweight, w_scales, out_dtype=None, out=None, ws=None):
+    """silu(gate) * up of one gated feed-forward block: qweight int8 [2F][D] holds the gate rows,
+    then the up rows; y [M][F]. The rest as in paro_w8a8_linear."""
+    return _linear(_lib.paro_w8a8_gated_linear, "paro_w8a8_gated_linear", _lib.paro_w8a8_gated_workspace_bytes, True,
+                   x, x_scales, qweight, w_scales, out_dtype, out, ws)
