@@ -39,7 +39,8 @@ __global__ __launch_bounds__(64) void w8a8_tile_kernel(const W8A8Call c) {
 
 size_t w8a8_workspace_bytes(int, int, int, bool) { return 0; }
 
-hipError_t launch_w8a8(const W8A8Call& c, void*, hipStream_t st) {
+hipError_t launch_w8a8(const W8A8Call& c, void* work, hipStream_t st) {
+  if (c.M > 64) return launch_w8a8_gemm(c, static_cast<int*>(work), st);
   const dim3 grid((c.N + 15) / 16, (c.M + 15) / 16);
   if (c.gated)
     hipLaunchKernelGGL((w8a8_tile_kernel<true>), grid, dim3(64), 0, st, c);
