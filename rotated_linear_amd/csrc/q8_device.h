@@ -66,9 +66,20 @@ __device__ inline uint32_t codes4(const float (&v)[4], float step) {
   return w;
 }
 
+// One output of an 8-bit product before its last rounding: sum * xs * ws, two float32 roundings.
+// Opaque to the compiler, which otherwise folds the last product into the conversion to float16
+// in some kernels and not in others: every kernel gives the same bits.
+__device__ inline float scaled(int sum, float xs, float ws) {
+  float v = float(sum) * xs * ws;
+  asm("" : "+v"(v));
+  return v;
+}
+
 // silu(g) u = g u / (1 + exp(-g)); exp(-g) past float32 gives an infinity and the quotient -0.
 __device__ inline float silu_mul(float g, float u) {
-  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896f)) * u;
+  float v = g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896f)) * u;
+  asm("" : "+v"(v));
+  return v;
 }
 
 }  // namespace paro

@@ -46,7 +46,8 @@ struct W8A8Call {
   int ydtype;
 };
 size_t w8a8_workspace_bytes(int M, int D, int N, bool gated);
-// part: the workspace
+// The tiled product (any number of rows); part: the workspace.
+size_t w8a8_gemm_workspace_bytes(int M, int D, int N, bool gated);
 hipError_t launch_w8a8_gemm(const W8A8Call& c, int* part, hipStream_t st);
 hipError_t launch_w8a8(const W8A8Call& c, void* work, hipStream_t st);
 

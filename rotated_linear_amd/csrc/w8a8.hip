@@ -25,8 +25,8 @@ __global__ __launch_bounds__(64) void w8a8_tile_kernel(const W8A8Call c) {
   for (int i = 0; i < 4; ++i) {
     const int n = n0 + (lane >> 4) * 4 + i;
     if (n >= c.N) continue;
-    float v = float(acc[i]) * c.xs[m] * c.ws[n];
-    if constexpr (GATED) v = silu_mul(v, float(acc2[i]) * c.xs[m] * c.ws[c.N + n]);
+    float v = scaled(acc[i], c.xs[m], c.ws[n]);
+    if constexpr (GATED) v = silu_mul(v, scaled(acc2[i], c.xs[m], c.ws[c.N + n]));
     const size_t at = size_t(m) * c.N + n;
     if (c.ydtype == PARO_F32)
       static_cast<float*>(c.y)[at] = v;
@@ -37,7 +37,9 @@ __global__ __launch_bounds__(64) void w8a8_tile_kernel(const W8A8Call c) {
 
 }  // namespace
 
-size_t w8a8_workspace_bytes(int, int, int, bool) { return 0; }
+size_t w8a8_workspace_bytes(int M, int D, int N, bool gated) {
+  return M > 64 ? w8a8_gemm_workspace_bytes(M, D, N, gated) : 0;
+}
 
 hipError_t launch_w8a8(const W8A8Call& c, void* work, hipStream_t st) {
   if (c.M > 64) return launch_w8a8_gemm(c, static_cast<int*>(work), st);

@@ -1,8 +1,8 @@
 // The 8-bit products for more rows than the streaming kernel takes: tiled matrix-core GEMM.
 #include <algorithm>
+#include <cmath>
 
 #include "q8_device.h"
-#include "w8a8_common.h"
 
 namespace paro {
 namespace {
@@ -10,8 +10,8 @@ namespace {
 constexpr int kCUs = 256;
 constexpr int kXcds = 8;
 
-// One 16-byte load per lane straight into LDS: lane l's bytes land at lds + 16 l. The compiler does
-// not see the load, so the kernel waits for it itself (stage_wait); it has no output register.
+// 16 (4) bytes per lane straight into LDS: lane l's land at lds + 16 l (4 l). The compiler does not
+// see these loads, so the kernel waits for them itself (stage_wait); they have no output register.
 __device__ inline void dma16(uint32_t lds, uint32_t voff, const void* base) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -21,40 +21,187 @@ __device__ inline void dma16(uint32_t lds, uint32_t voff, const void* base) {
       : "s"(lds), "v"(voff), "s"(base)
       : "memory", "m0");
 }
-// All but the N youngest of this wave's loads have landed and its LDS reads are done; then the
-// workgroup's waves meet.
+__device__ inline void dma4(uint32_t lds, uint32_t voff, const void* base) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %1, %2"
+      :
+      : "s"(lds), "v"(voff), "s"(base)
+      : "memory", "m0");
+}
+// All but the N youngest of this wave's memory operations are done and so are its LDS reads; then
+// the workgroup's waves meet.
 template <int N>
 __device__ inline void stage_wait() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
+// The lane index, made opaque where it is used: addresses formed from it once per tile are not
+// hoisted out of the tile loop and kept live (or spilled) across the products.
+__device__ inline int fresh_lane() {
+  int t = int(threadIdx.x);
+  asm volatile("" : "+v"(t));
+  return t & 63;
+}
+
 struct GemmArgs {
   W8A8Call c;
-  int* part;     // split partial sums [S][M][rows], or nullptr
+  int* part;  // split partial sums [S][M][rows of w], or nullptr
   int tiles_m, tiles_n, splits, steps_per_split;
 };
 
 template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_;
-  static constexpr int NT = WM * WN * 64;
-  static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;  // 32 x 32 fragments of a wave
+  static constexpr int NW = WM * WN, NT = NW * 64;
+  static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;  // 16 x 16 fragments of a wave
   static constexpr int ROWS = BM + BN;
   static constexpr int STAGE = ROWS * BK;
-  static constexpr int RPI = 1024 / BK;                // tile rows of one wave-wide load
-  static constexpr int LOADS = ROWS / RPI / (WM * WN); // a wave's loads per stage
-  static_assert(ROWS % (RPI * WM * WN) == 0, "loads divide over the waves");
-  static constexpr int LDS = STAGE * S;
+  static constexpr int RPI = 1024 / BK;           // tile rows of one wave-wide load
+  static constexpr int LOADS = ROWS / RPI / NW;   // a wave's loads per stage
+  static_assert(ROWS % (RPI * NW) == 0 && ROWS % 64 == 0 && BM % (RPI * 1) == 0, "loads divide over the waves");
+  static_assert(FM % 2 == 0 && FN == 4 && BK == 128, "32-row pieces of y; 32 gate and 32 up rows a wave; fragment sets take turns");
+  // Results leave through LDS 32 rows x 64 bytes at a time, rows 80 bytes apart.
+  static constexpr int EP = 80;
+  static constexpr int OUT = STAGE * S;           // LDS: the stages, each wave's results, the scales
+  static constexpr int SCALES = OUT + NW * 32 * EP;
+  static constexpr int LDS = SCALES + ROWS * 4;
 };
 
-// 16-byte slot of a tile row's chunk c: rows of BK bytes, the chunk index mixed with the row so
-// that 16 consecutive rows' chunk c lie in 16 distinct slots modulo 256 bytes.
+// Byte offset of chunk c (16 bytes) of a tile row in a stage: rows of BK bytes, the chunk index
+// mixed with the row so that 16 consecutive rows' chunk c lie in 16 distinct slots modulo 256 bytes.
 template <int BK>
 __device__ inline uint32_t swz(uint32_t row, uint32_t c) {
   if constexpr (BK == 64)
     return row * 64 + ((c ^ ((row >> 2) & 3)) << 4);
   else
     return row * 128 + ((c ^ ((row >> 1) & 7)) << 4);
+}
+
+// Where a tile lies.
+struct Place {
+  int m0, n0;  // first row and column of y
+  int split, t0, steps;
+};
+
+// Tile number `tile` (of tiles_m * tiles_n * splits): splits innermost, then groups of 4 tile rows
+// walked column by column, so that tiles worked on at the same time share rows of x and of w.
+template <class T, bool GATED>
+__device__ inline Place place(const GemmArgs& a, int tile) {
+  Place p;
+  p.split = tile % a.splits;
+  tile /= a.splits;
+  constexpr int GM = 4;
+  const int group = tile / (GM * a.tiles_n);
+  const int gsz = min(GM, a.tiles_m - group * GM);
+  const int in = tile - group * GM * a.tiles_n;
+  p.m0 = (group * GM + in % gsz) * T::BM;
+  p.n0 = (in / gsz) * (GATED ? T::BN / 2 : T::BN);
+  p.t0 = p.split * a.steps_per_split;
+  p.steps = min(a.steps_per_split, a.c.D / T::BK - p.t0);
+  return p;
+}
+
+// Four values in type DT at an address in LDS.
+template <int DT>
+__device__ inline void put4(char* at, const float (&v)[4]) {
+  if constexpr (DT == PARO_F32) {
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = __builtin_bit_cast(uint32_t, v[e]);
+    *reinterpret_cast<u32x4*>(at) = w;
+  } else {
+    using u32x2 = uint32_t __attribute__((ext_vector_type(2)));
+    *reinterpret_cast<u32x2*>(at) =
+        u32x2{to_bits16<DT>(v[0]) | (to_bits16<DT>(v[1]) << 16), to_bits16<DT>(v[2]) | (to_bits16<DT>(v[3]) << 16)};
+  }
+}
+
+// Store one 32-row piece (64 bytes a row) that the wave has put into buf: 16 bytes a lane, four
+// lanes a row. dst: column 0 of the piece in row 0; rows ld bytes apart; `rows` rows and `cols`
+// elements of EB bytes exist.
+template <int EB, int EP>
+__device__ inline void store_piece(const char* buf, char* dst, size_t ld, int rows, int cols, bool whole, int lane) {
+  if (whole) {
+#pragma unroll
+    for (int r0 = 0; r0 < 32; r0 += 16) {
+      const int r = r0 + (lane >> 2), b = lane & 3;
+      const u32x4 w = *reinterpret_cast<const u32x4*>(buf + r * EP + b * 16);
+      if (r < rows && b * (16 / EB) < cols) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(dst + r * ld + b * 16));
+    }
+  } else {
+    constexpr int E = 64 / EB;  // elements of a piece's row
+    const int b = lane % E;
+    for (int r = lane / E; r < 32; r += EB)
+      if (r < rows && b < cols) {
+        if constexpr (EB == 4)
+          *reinterpret_cast<uint32_t*>(dst + r * ld + b * 4) = *reinterpret_cast<const uint32_t*>(buf + r * EP + b * 4);
+        else
+          *reinterpret_cast<uint16_t*>(dst + r * ld + b * 2) = *reinterpret_cast<const uint16_t*>(buf + r * EP + b * 2);
+      }
+  }
+}
+
+// A wave's results: scaled (and gated) rows of y in type DT, or (PART) the int32 sums themselves.
+// A lane's column of a fragment is a row of y, its rows are columns of y, four at a time.
+template <class T, bool GATED, int DT, bool PART>
+__device__ inline void store_tile(const GemmArgs& a, const Place& p, const i32x4 (&acc)[T::FM][T::FN], char* smem,
+                                  int wave) {
+  const W8A8Call& c = a.c;
+  const int lane = fresh_lane();
+  constexpr int EB = DT == PARO_F32 ? 4 : 2;
+  constexpr bool G = GATED && !PART;
+  constexpr int CF = 4 / EB;  // column fragments of a piece
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  char* const buf = smem + T::OUT + wave * 32 * T::EP;
+  const float* const sc = reinterpret_cast<const float*>(smem + T::SCALES);
+  const size_t ldc = PART ? size_t(c.N) * (GATED ? 2 : 1) : size_t(c.N);  // columns of the output
+  char* const out = PART ? reinterpret_cast<char*>(a.part) + size_t(p.split) * c.M * ldc * 4 : static_cast<char*>(c.y);
+  const bool whole = c.N % (16 / EB) == 0;  // pieces start at multiples of 16 bytes and end with a row
+#pragma unroll
+  for (int i = 0; i < T::FM; i += 2) {
+    const int mf = (wm * T::FM + i) * 16;
+    const float xs[2] = {sc[mf + (lane & 15)], sc[mf + 16 + (lane & 15)]};
+#pragma unroll
+    for (int y = 0; y < (G ? T::FN / 2 : T::FN); y += CF) {  // column fragments of the output
+#pragma unroll
+      for (int k = 0; k < CF; ++k) {
+        // the fragment of w (32 gate rows, then their 32 up rows: the up fragment is two further on)
+        const int j = G ? ((y + k) >> 1) * 4 + ((y + k) & 1) : y + k;
+        const float* const wsc = sc + T::BM + (wn * T::FN + j) * 16 + 4 * (lane >> 4);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          char* const at = buf + (u * 16 + (lane & 15)) * T::EP + (16 * k + 4 * (lane >> 4)) * EB;
+          if constexpr (PART) {
+            *reinterpret_cast<i32x4*>(at) = acc[i + u][j];
+          } else {
+            float v[4];
+            const float4 w4 = *reinterpret_cast<const float4*>(wsc);
+            const float w0[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i + u][j][e], xs[u], w0[e]);
+            if constexpr (G) {
+              const float4 u4 = *reinterpret_cast<const float4*>(wsc + 32);
+              const float u0[4] = {u4.x, u4.y, u4.z, u4.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], scaled(acc[i + u][j + 2][e], xs[u], u0[e]));
+            }
+            put4<DT>(at, v);
+          }
+        }
+      }
+      // one wave's LDS accesses are carried out in order; the compiler keeps them in order too
+      asm volatile("" ::: "memory");
+      // the piece's first column: of y (n), and in the output (the sums of a gated pair keep w's rows)
+      const int r = (wn * T::FN + y) * 16;  // row of w in the tile (not gated output)
+      const int n = p.n0 + (G ? wn * T::FN * 8 + y * 16 : GATED ? (r >> 6) * 32 + (r & 31) : r);
+      const size_t col = n + (PART && GATED && ((r >> 5) & 1) ? size_t(c.N) : 0);
+      store_piece<EB, T::EP>(buf, out + (size_t(p.m0 + mf) * ldc + col) * EB, ldc * EB, c.M - p.m0 - mf, c.N - n, whole,
+                             lane);
+      asm volatile("" ::: "memory");
+    }
+  }
 }
 
 template <class T, bool GATED>
@@ -65,176 +212,296 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / T::WN, wn = wave % T::WN;
 
-  // XCD-aware order: workgroups go round the XCDs, each XCD takes a contiguous range of tiles.
+  // Workgroups go round the XCDs; each XCD takes a contiguous range of tiles, its workgroups one
+  // tile after another.
   const int total = a.tiles_m * a.tiles_n * a.splits;
   const int per = total / kXcds, rem = total % kXcds;
-  const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
-  int tile = xcd * per + min(xcd, rem) + idx;
-  const int split = tile % a.splits;
-  tile /= a.splits;
-  // within a range: columns of GM tile rows
-  constexpr int GM = 4;
-  const int group = tile / (GM * a.tiles_n);
-  const int gm0 = group * GM, gsz = min(GM, a.tiles_m - gm0);
-  const int in = tile - group * GM * a.tiles_n;
-  const int tm = gm0 + in % gsz, tn = in / gsz;
+  const int xcd = blockIdx.x % kXcds;
+  const int stride = (gridDim.x - xcd + kXcds - 1) / kXcds;  // workgroups on this XCD
+  const int first = xcd * per + min(xcd, rem), end = first + per + (xcd < rem ? 1 : 0);
+  int tile = first + blockIdx.x / kXcds;
+  if (tile >= end) return;
 
-  const int m0 = tm * T::BM;
-  // columns of y per tile: a gated tile's rows of w alternate, 32 gate rows then their 32 up rows
-  constexpr int YN = GATED ? T::BN / 2 : T::BN;
-  const int n0 = tn * YN;
-
-  // this lane's source offsets (x rows first, then w rows), rows past the end clamped to the last
+  // The loads run S stages ahead of the products and pass from one tile to the next without a
+  // break: `ahead` is the tile they are in, step `at` of it.
+  int ahead = tile, at = 0;
+  Place q = place<T, GATED>(a, ahead);
   uint32_t voff[T::LOADS];
   const char* src[T::LOADS];
-  const int8_t* xb = c.x + size_t(m0) * c.D;
-  const int8_t* wb = c.w + size_t(n0) * c.D;
+  auto aim = [&]() {
+    const int lane = fresh_lane();
+    // this lane's source offsets in tile q; rows past the end are the last row again
+    const char* const xb = reinterpret_cast<const char*>(c.x) + size_t(q.m0) * c.D + size_t(q.t0) * T::BK;
+    const char* const wb = reinterpret_cast<const char*>(c.w) + size_t(q.n0) * c.D + size_t(q.t0) * T::BK;
 #pragma unroll
-  for (int i = 0; i < T::LOADS; ++i) {
-    const int r0 = (wave * T::LOADS + i) * T::RPI;  // first tile row of the load
-    const int lr = lane / (T::BK / 16);
-    const int row = r0 + lr;
-    const uint32_t slot = (lane % (T::BK / 16)) * 16;
-    const uint32_t ch = (swz<T::BK>(row, 0) - row * T::BK) ^ slot;  // the chunk that this slot holds
-    if (r0 < T::BM) {
-      src[i] = reinterpret_cast<const char*>(xb);
-      voff[i] = uint32_t(min(row, c.M - 1 - m0)) * uint32_t(c.D) + ch;
-    } else {
-      const int br = row - T::BM, b0 = r0 - T::BM;
-      if constexpr (GATED) {
-        const bool up = (b0 >> 5) & 1;
-        src[i] = reinterpret_cast<const char*>(wb) + (up ? size_t(c.N) * c.D : 0);
-        voff[i] = uint32_t(min((br >> 6) * 32 + (br & 31), c.N - 1 - n0)) * uint32_t(c.D) + ch;
+    for (int i = 0; i < T::LOADS; ++i) {
+      const int r0 = (wave * T::LOADS + i) * T::RPI;  // first tile row of the load
+      const int row = r0 + lane / (T::BK / 16);
+      const uint32_t slot = (lane % (T::BK / 16)) * 16;
+      const uint32_t ch = (swz<T::BK>(row, 0) - row * T::BK) ^ slot;  // the chunk that this slot holds
+      if (r0 < T::BM) {
+        src[i] = xb;
+        voff[i] = uint32_t(min(row, c.M - 1 - q.m0)) * uint32_t(c.D) + ch;
       } else {
-        src[i] = reinterpret_cast<const char*>(wb);
-        voff[i] = uint32_t(min(br, c.N - 1 - n0)) * uint32_t(c.D) + ch;
+        const int b = row - T::BM;
+        const bool up = GATED && (((r0 - T::BM) >> 5) & 1);
+        src[i] = wb + (up ? size_t(c.N) * c.D : 0);
+        voff[i] = uint32_t(min(GATED ? (b >> 6) * 32 + (b & 31) : b, c.N - 1 - q.n0)) * uint32_t(c.D) + ch;
       }
     }
-  }
-  const int steps_all = c.D / T::BK;
-  const int t0 = split * a.steps_per_split;
-  const int steps = min(a.steps_per_split, steps_all - t0);
+  };
+  aim();
   const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)smem));
-  auto issue = [&](int t) {  // stage t into buffer t % S (past the end: the last stage again, never read)
-    const int kt = (t0 + min(t, steps - 1)) * T::BK;
-    const uint32_t dst = lds0 + uint32_t(t % T::S) * T::STAGE + uint32_t(wave * T::LOADS) * 1024;
+  const uint32_t ldsw = __builtin_amdgcn_readfirstlane(lds0 + uint32_t(wave * T::LOADS) * 1024);
+  auto issue = [&](uint32_t buf) {  // the next stage into buffer `buf`; after the last tile its last stage again
+    if (at == q.steps) {
+      if (ahead + stride < end) {
+        ahead += stride;
+        at = 0;
+        q = place<T, GATED>(a, ahead);
+        aim();
+      } else {
+        at = q.steps - 1;
+      }
+    }
 #pragma unroll
-    for (int i = 0; i < T::LOADS; ++i)
-      dma16(__builtin_amdgcn_readfirstlane(dst + i * 1024), voff[i], src[i] + kt);
+    for (int i = 0; i < T::LOADS; ++i) dma16(ldsw + buf * T::STAGE + i * 1024, voff[i], src[i] + size_t(at) * T::BK);
+    ++at;
+  };
+  // The scales of a tile (x rows, then w rows) into LDS: the waves take 64 each.
+  auto load_scales = [&](const Place& p) {
+    const int lane = fresh_lane();
+#pragma unroll
+    for (int r0 = 0; r0 < T::ROWS; r0 += 64 * T::NW) {
+      const int rw = r0 + wave * 64;
+      if (rw >= T::ROWS) break;
+      const uint32_t dst = lds0 + T::SCALES + rw * 4;
+      if (rw < T::BM) {
+        dma4(dst, uint32_t(min(rw + lane, c.M - 1 - p.m0)) * 4, c.xs + p.m0);
+      } else {
+        const int b = rw - T::BM + lane;
+        const uint32_t o = GATED ? min((b >> 6) * 32 + (b & 31), c.N - 1 - p.n0) + ((b >> 5) & 1 ? uint32_t(c.N) : 0)
+                                 : min(b, c.N - 1 - p.n0);
+        dma4(dst, o * 4, c.ws + p.n0);
+      }
+    }
   };
 
-  i32x16 acc[T::FM][T::FN];
+  constexpr int SUB = T::BK / 64;
+  // Half a wave's rows of x at a time: while one half's products run, the other half's fragments
+  // (and, before a new 64-channel step, its fragments of w) are read.
+  constexpr int HM = T::FM / 2;
+  i32x4 fx[2][HM], fw[2][T::FN];
+  auto read_x = [&](uint32_t buf, int sub, int half) {
+    const char* const st = smem + buf * T::STAGE;
 #pragma unroll
-  for (int i = 0; i < T::FM; ++i)
-#pragma unroll
-    for (int j = 0; j < T::FN; ++j) acc[i][j] = i32x16{};
-
-  constexpr int SUB = T::BK / 32;
-  i32x4 fx[2][T::FM], fw[2][T::FN];
-  auto read = [&](int t, int sub, int set) {
-    const char* st = smem + (t % T::S) * T::STAGE;
-    const uint32_t ch = sub * 2 + (lane >> 5);
-#pragma unroll
-    for (int i = 0; i < T::FM; ++i)
-      fx[set][i] = *reinterpret_cast<const i32x4*>(st + swz<T::BK>((wm * T::FM + i) * 32 + (lane & 31), ch));
-#pragma unroll
-    for (int j = 0; j < T::FN; ++j)
-      fw[set][j] = *reinterpret_cast<const i32x4*>(st + T::BM * T::BK + swz<T::BK>((wn * T::FN + j) * 32 + (lane & 31), ch));
+    for (int i = 0; i < HM; ++i)
+      fx[half][i] = *reinterpret_cast<const i32x4*>(st + swz<T::BK>((wm * T::FM + half * HM + i) * 16 + (lane & 15), sub * 4 + (lane >> 4)));
   };
-  auto mma = [&](int set) {
+  auto read_w = [&](uint32_t buf, int sub) {
+    const char* const st = smem + buf * T::STAGE + T::BM * T::BK;
 #pragma unroll
     for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-      for (int i = 0; i < T::FM; ++i)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[set][j], fx[set][i], acc[i][j], 0, 0, 0);
+      fw[sub & 1][j] = *reinterpret_cast<const i32x4*>(st + swz<T::BK>((wn * T::FN + j) * 16 + (lane & 15), sub * 4 + (lane >> 4)));
   };
 
 #pragma unroll
   for (int s = 0; s < T::S; ++s) issue(s);
   stage_wait<(T::S - 1) * T::LOADS>();
-  read(0, 0, 0);
-  for (int t = 0; t < steps; ++t) {
+  read_w(0, 0);
+  read_x(0, 0, 0);
+  uint32_t buf = 0;
+  for (; tile < end; tile += stride) {
+    const Place p = place<T, GATED>(a, tile);
+    i32x4 acc[T::FM][T::FN];
 #pragma unroll
-    for (int sub = 0; sub < SUB; ++sub) {
-      if (sub + 1 < SUB) {
-        read(t, sub + 1, (sub + 1) & 1);
-      } else {
-        // every wave has read stage t: its buffer takes stage t + S, and stage t + 1 is in LDS
-        stage_wait<(T::S - 2) * T::LOADS>();
-        issue(t + T::S);
-        read(t + 1, 0, 0);
-      }
-      mma(sub & 1);
-    }
-  }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the loads past the end
-
-  // y[m][n]: lane's column of a fragment is m, its rows n come four at a time
-  const int mrow = m0 + wm * T::FM * 32 + (lane & 31);
+    for (int i = 0; i < T::FM; ++i)
 #pragma unroll
-  for (int i = 0; i < T::FM; ++i) {
-    const int m = mrow + i * 32;
-    if (m >= c.M) continue;
-    if (a.part) {
-      const size_t rows = size_t(c.N) * (GATED ? 2 : 1);
-      int* p = a.part + (size_t(split) * c.M + m) * rows;
+      for (int j = 0; j < T::FN; ++j) acc[i][j] = i32x4{};
+    for (int t = 0; t < p.steps; ++t) {
+      const uint32_t nbuf = buf + 1 == T::S ? 0 : buf + 1;
 #pragma unroll
-      for (int j = 0; j < T::FN; ++j) {
-        const int fj = wn * T::FN + j;
-        const int nb = GATED ? n0 + (fj >> 1) * 32 : n0 + fj * 32;
-        const size_t base = GATED && (fj & 1) ? size_t(c.N) : 0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int n = nb + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
-          if (n < c.N) p[base + n] = acc[i][j][e];
+      for (int h = 0; h < 2 * SUB; ++h) {
+        const int sub = h / 2, half = h & 1;
+        if (half == 0) {
+          read_x(buf, sub, 1);
+        } else if (sub + 1 < SUB) {
+          read_w(buf, sub + 1);
+          read_x(buf, sub + 1, 0);
+        } else {
+          // every wave has read this stage: its buffer takes the stage S further on, and the next
+          // stage is in LDS
+          stage_wait<(T::S - 2) * T::LOADS>();
+          issue(buf);
+          if (t == 0) load_scales(p);  // every wave has stored the last tile
+          read_w(nbuf, 0);
+          read_x(nbuf, 0, 0);
         }
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+          for (int i = 0; i < HM; ++i)
+            acc[half * HM + i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[sub & 1][j], fx[half][i], acc[half * HM + i][j], 0, 0, 0);
+        // a fragment read, then its share of the products, in turn
+        constexpr int kShare = HM * T::FN / (HM + T::FN);
+#pragma unroll
+        for (int r = 0; r < T::FN + HM; ++r) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x008, kShare > 0 ? kShare : 1, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      continue;
+      asm volatile("" ::: "memory");  // the next stage's first reads stay in this iteration
+      buf = nbuf;
+    }
+    // with S steps or more the scales' loads were waited for at a later stage's barrier
+    if (p.steps < T::S) stage_wait<0>();
+    if (a.part)
+      store_tile<T, GATED, PARO_F32, true>(a, p, acc, smem, wave);
+    else if (c.ydtype == PARO_F32)
+      store_tile<T, GATED, PARO_F32, false>(a, p, acc, smem, wave);
+    else if (c.ydtype == PARO_F16)
+      store_tile<T, GATED, PARO_F16, false>(a, p, acc, smem, wave);
+    else
+      store_tile<T, GATED, PARO_BF16, false>(a, p, acc, smem, wave);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads past the last stage land before the LDS is given up
+}
+
+// y from the S partial sums of a split reduction: a thread takes V columns of a row (their sums of
+// every split in flight together), the integer sums are exact in any order.
+template <int V, bool GATED, int DT>
+__global__ __launch_bounds__(256) void reduce_kernel(const W8A8Call c, const int* part, int splits) {
+  using IV = int __attribute__((ext_vector_type(V)));
+  const size_t rows = size_t(c.N) * (GATED ? 2 : 1), plane = size_t(c.M) * rows;
+  const size_t per_row = c.N / V, total = per_row * c.M;
+  for (size_t t = size_t(blockIdx.x) * 256 + threadIdx.x; t < total; t += size_t(gridDim.x) * 256) {
+    const size_t m = t / per_row;
+    const int n = int(t - m * per_row) * V;
+    const int* const p = part + m * rows + n;
+    IV g = IV(0), u = IV(0);
+#pragma unroll 4
+    for (int s = 0; s < splits; ++s) {
+      g += *reinterpret_cast<const IV*>(p + s * plane);
+      if constexpr (GATED) u += *reinterpret_cast<const IV*>(p + s * plane + c.N);
     }
     const float xs = c.xs[m];
+    float v[V];
 #pragma unroll
-    for (int j = 0; j < T::FN; j += GATED ? 2 : 1) {
-      const int fj = wn * T::FN + j;
-      const int nb = GATED ? n0 + (fj >> 1) * 32 : n0 + fj * 32;
-#pragma unroll
-      for (int e4 = 0; e4 < 4; ++e4) {
-        const int n = nb + 8 * e4 + 4 * (lane >> 5);
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int nc = min(n + e, c.N - 1);
-          v[e] = float(acc[i][j][e4 * 4 + e]) * xs * c.ws[nc];
-          if constexpr (GATED) v[e] = silu_mul(v[e], float(acc[i][j + 1][e4 * 4 + e]) * xs * c.ws[size_t(c.N) + nc]);
-        }
-        store4(c, m, n, v);
-      }
+    for (int e = 0; e < V; ++e) {
+      v[e] = scaled(g[e], xs, c.ws[n + e]);
+      if constexpr (GATED) v[e] = silu_mul(v[e], scaled(u[e], xs, c.ws[size_t(c.N) + n + e]));
+    }
+    if constexpr (V == 4) {
+      put4<DT>(static_cast<char*>(c.y) + (m * c.N + n) * (DT == PARO_F32 ? 4 : 2), v);
+    } else if constexpr (DT == PARO_F32) {
+      static_cast<float*>(c.y)[m * c.N + n] = v[0];
+    } else {
+      static_cast<uint16_t*>(c.y)[m * c.N + n] = uint16_t(to_bits16<DT>(v[0]));
     }
   }
+}
+
+template <bool GATED>
+hipError_t launch_reduce(const W8A8Call& c, const int* part, int splits, hipStream_t st) {
+  const bool four = c.N % 4 == 0;
+  const size_t total = size_t(c.M) * (c.N / (four ? 4 : 1));
+  const dim3 grid(unsigned(std::min<size_t>((total + 255) / 256, 8192)));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, c, part, splits);
+    return hipGetLastError();
+  };
+  if (c.ydtype == PARO_F32) return go(four ? reduce_kernel<4, GATED, PARO_F32> : reduce_kernel<1, GATED, PARO_F32>);
+  if (c.ydtype == PARO_F16) return go(four ? reduce_kernel<4, GATED, PARO_F16> : reduce_kernel<1, GATED, PARO_F16>);
+  return go(four ? reduce_kernel<4, GATED, PARO_BF16> : reduce_kernel<1, GATED, PARO_BF16>);
 }
 
 template <class T, bool GATED>
 hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st) {
   GemmArgs a;
   a.c = c;
-  a.part = splits > 1 ? part : nullptr;
   a.tiles_m = (c.M + T::BM - 1) / T::BM;
   const int yn = GATED ? T::BN / 2 : T::BN;
   a.tiles_n = (c.N + yn - 1) / yn;
-  a.splits = splits;
   const int steps = c.D / T::BK;
   a.steps_per_split = (steps + splits - 1) / splits;
+  a.splits = (steps + a.steps_per_split - 1) / a.steps_per_split;  // every split has steps
+  a.part = a.splits > 1 ? part : nullptr;
   const void* fn = reinterpret_cast<const void*>(&w8a8_gemm_kernel<T, GATED>);
   if (hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS)) return e;
-  hipLaunchKernelGGL((w8a8_gemm_kernel<T, GATED>), dim3(a.tiles_m * a.tiles_n * splits), dim3(T::NT), T::LDS, st, a);
-  return hipGetLastError();
+  const long total = long(a.tiles_m) * a.tiles_n * a.splits;
+  const long resident = long(kCUs) * std::max(1, int(160 * 1024 / T::LDS));
+  hipLaunchKernelGGL((w8a8_gemm_kernel<T, GATED>), dim3(unsigned(std::min(total, resident))), dim3(T::NT), T::LDS, st, a);
+  if (hipError_t e = hipGetLastError()) return e;
+  return a.part ? launch_reduce<GATED>(c, part, a.splits, st) : hipSuccess;
 }
 
-using T256 = Tile<256, 256, 2, 2, 64, 4>;
+// The three tilings: 256 x 256 with 8 waves; 128 x 128 with 4 waves, two workgroups on a CU; the
+// same with four stages in LDS, one workgroup on a CU.
+using T256 = Tile<256, 256, 2, 4, 128, 2>;
+using T128 = Tile<128, 128, 2, 2, 128, 2>;
+using T128Deep = Tile<128, 128, 2, 2, 128, 4>;
+
+struct Plan {
+  int tile;  // 0: T256, 1: T128, 2: T128Deep
+  int splits;
+};
+
+// Partial sums of a split reduction at most (a split past it would cost more than it gives).
+constexpr size_t kMaxPartBytes = size_t(128) << 20;
+
+// The tiling and split with the least estimated time, from rates measured on MI355X (microseconds;
+// x in 8 bits, random codes, D = 128..16384): a call costs about 6 (T256: 9) before its first step
+// of 128 channels; a step of a 128 x 128 tile takes 0.46 on its own CU (T128Deep; 0.52 with two
+// stages) and 0.97 for two on one CU (T128); a step of a 256 x 256 tile 1.15 on a quiet chip and
+// 1.6 when every CU runs one (the power limit then sets the clock). A split adds a launch and the
+// partial sums' way out and back (about 3 TB/s).
+Plan plan_gemm_w8a8(int M, int D, int N, bool gated) {
+  const double rows = double(N) * (gated ? 2 : 1);
+  const int steps = D / 128;
+  Plan best{1, 1};
+  double best_us = 1e30;
+  for (int tile = 0; tile < 3; ++tile) {
+    const int b = tile == 0 ? 256 : 128;
+    const double tiles = double((M + b - 1) / b) * double((size_t(N) * (gated ? 2 : 1) + b - 1) / b);
+    for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
+      if (s > 1 && (s > steps || double(s) * M * rows * 4 > double(kMaxPartBytes))) break;
+      const int per = (steps + s - 1) / s;
+      const double units = tiles * ((steps + per - 1) / per);
+      double us;
+      if (tile == 0)
+        us = 9 + std::ceil(units / kCUs) * (per * (1.15 + 0.45 * std::min(1.0, units / kCUs)) + 1);
+      else if (tile == 1)
+        us = 6 + (units <= kCUs ? per * 0.52 : std::ceil(units / (2 * kCUs)) * (per * 0.97 + 1));
+      else
+        us = 6 + std::ceil(units / kCUs) * (per * 0.46 + 1.5);
+      if (s > 1) us += 4 + 2.0 * s * M * rows * 4 / 3e6;
+      if (us < best_us) {
+        best_us = us;
+        best = Plan{tile, s};
+      }
+    }
+  }
+  return best;
+}
+
+template <bool GATED>
+hipError_t launch_plan(const W8A8Call& c, int* part, hipStream_t st) {
+  const Plan p = plan_gemm_w8a8(c.M, c.D, c.N, GATED);
+  if (p.tile == 0) return launch_tile<T256, GATED>(c, part, p.splits, st);
+  if (p.tile == 1) return launch_tile<T128, GATED>(c, part, p.splits, st);
+  return launch_tile<T128Deep, GATED>(c, part, p.splits, st);
+}
 
 }  // namespace
 
+size_t w8a8_gemm_workspace_bytes(int M, int D, int N, bool gated) {
+  const int s = plan_gemm_w8a8(M, D, N, gated).splits;
+  return s > 1 ? align256(size_t(s) * M * N * (gated ? 2 : 1) * 4) : 0;
+}
+
 hipError_t launch_w8a8_gemm(const W8A8Call& c, int* part, hipStream_t st) {
-  return c.gated ? launch_tile<T256, true>(c, part, 1, st) : launch_tile<T256, false>(c, part, 1, st);
+  return c.gated ? launch_plan<true>(c, part, st) : launch_plan<false>(c, part, st);
 }
 
 }  // namespace paro
