@@ -38,6 +38,10 @@ size_t dtype_bytes(int t) { return t == PARO_F32 ? 4 : 2; }
 paro_status from_hip(hipError_t e) { return e == hipSuccess ? PARO_OK : PARO_EHIP; }
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
+size_t w8a8_workspace_bytes(int M, int D, int N, bool gated) {
+  return w8a8_stream_takes(M, D, N, gated) ? 0 : w8a8_gemm_workspace_bytes(M, D, N, gated);
+}
+
 // The transform of a call (r may be NULL); *out is filled either way.
 paro_status check_rot(const paro_rotation* r, int D, DevRot* out, Span* desc) {
   *out = DevRot{0, D, nullptr, nullptr, nullptr};
@@ -82,7 +86,9 @@ paro_status linear(int M, int D, int N, bool gated, const int8_t* x, const float
   const Span outs[] = {{y, size_t(M) * N * dtype_bytes(ydtype)}, {need ? ws : nullptr, need}};
   const Span ins[] = {{x, size_t(M) * D}, {xs, size_t(M) * 4}, {w, rows * D}, {wsc, rows * 4}};
   if (any_overlap(outs, ins)) return PARO_EINVAL;
-  return from_hip(launch_w8a8(W8A8Call{M, D, N, gated, x, xs, w, wsc, y, ydtype}, ws, as_stream(stream)));
+  const W8A8Call c{M, D, N, gated, x, xs, w, wsc, y, ydtype};
+  return from_hip(w8a8_stream_takes(M, D, N, gated) ? launch_w8a8_stream(c, as_stream(stream))
+                                                    : launch_w8a8_gemm(c, static_cast<int*>(ws), as_stream(stream)));
 }
 
 }  // namespace

@@ -45,10 +45,11 @@ struct W8A8Call {
   void* y;
   int ydtype;
 };
-size_t w8a8_workspace_bytes(int M, int D, int N, bool gated);
-// The tiled product (any number of rows); part: the workspace.
+// A few rows: the weights streamed into registers, no workspace.
+bool w8a8_stream_takes(int M, int D, int N, bool gated);
+hipError_t launch_w8a8_stream(const W8A8Call& c, hipStream_t st);
+// Any number of rows: the tiled product; part: its workspace.
 size_t w8a8_gemm_workspace_bytes(int M, int D, int N, bool gated);
 hipError_t launch_w8a8_gemm(const W8A8Call& c, int* part, hipStream_t st);
-hipError_t launch_w8a8(const W8A8Call& c, void* work, hipStream_t st);
 
 }  // namespace paro

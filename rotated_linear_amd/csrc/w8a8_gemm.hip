@@ -60,24 +60,22 @@ struct Tile {
   static constexpr int STAGE = ROWS * BK;
   static constexpr int RPI = 1024 / BK;           // tile rows of one wave-wide load
   static constexpr int LOADS = ROWS / RPI / NW;   // a wave's loads per stage
-  static_assert(ROWS % (RPI * NW) == 0 && ROWS % 64 == 0 && BM % (RPI * 1) == 0, "loads divide over the waves");
-  static_assert(FM % 2 == 0 && FN == 4 && BK == 128, "32-row pieces of y; 32 gate and 32 up rows a wave; fragment sets take turns");
-  // Results leave through LDS 32 rows x 64 bytes at a time, rows 80 bytes apart.
+  static_assert(BK == 128 && ROWS % (RPI * NW) == 0 && BM % RPI == 0, "loads divide over the waves");
+  static_assert(FN % 2 == 0 && (FM == 1 || FM % 2 == 0), "16 gate and 16 up rows in turn; x fragments in halves");
+  // Results leave through LDS in pieces of PR rows, up to 64 bytes of a row at a time, rows 80 bytes
+  // apart.
+  static constexpr int PR = FM == 1 ? 16 : 32;
   static constexpr int EP = 80;
   static constexpr int OUT = STAGE * S;           // LDS: the stages, each wave's results, the scales
-  static constexpr int SCALES = OUT + NW * 32 * EP;
-  static constexpr int LDS = SCALES + ROWS * 4;
+  static constexpr int SCALES = OUT + NW * PR * EP;
+  static constexpr int XS = BM < 64 ? 64 : BM;    // scales of x rows (64 at least: they come 64 a load)
+  static constexpr int LDS = SCALES + (XS + BN) * 4;
+  static_assert(XS % 64 == 0 && BN % 64 == 0 && LDS <= 160 * 1024, "scales 64 a load; one CU's LDS");
 };
 
-// Byte offset of chunk c (16 bytes) of a tile row in a stage: rows of BK bytes, the chunk index
+// Byte offset of chunk c (16 bytes) of a tile row in a stage: rows of 128 bytes, the chunk index
 // mixed with the row so that 16 consecutive rows' chunk c lie in 16 distinct slots modulo 256 bytes.
-template <int BK>
-__device__ inline uint32_t swz(uint32_t row, uint32_t c) {
-  if constexpr (BK == 64)
-    return row * 64 + ((c ^ ((row >> 2) & 3)) << 4);
-  else
-    return row * 128 + ((c ^ ((row >> 1) & 7)) << 4);
-}
+__device__ inline uint32_t swz(uint32_t row, uint32_t c) { return row * 128 + ((c ^ ((row >> 1) & 7)) << 4); }
 
 // Where a tile lies.
 struct Place {
@@ -118,22 +116,24 @@ __device__ inline void put4(char* at, const float (&v)[4]) {
   }
 }
 
-// Store one 32-row piece (64 bytes a row) that the wave has put into buf: 16 bytes a lane, four
-// lanes a row. dst: column 0 of the piece in row 0; rows ld bytes apart; `rows` rows and `cols`
-// elements of EB bytes exist.
-template <int EB, int EP>
+// Store one piece that the wave has put into buf: PR rows of PB bytes, 16 bytes a lane. dst: the
+// piece's first element; rows ld bytes apart; `rows` rows and `cols` elements of EB bytes exist.
+template <int EB, int EP, int PB, int PR>
 __device__ inline void store_piece(const char* buf, char* dst, size_t ld, int rows, int cols, bool whole, int lane) {
   if (whole) {
+    constexpr int L = PB / 16;  // lanes of a row
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 16) {
-      const int r = r0 + (lane >> 2), b = lane & 3;
-      const u32x4 w = *reinterpret_cast<const u32x4*>(buf + r * EP + b * 16);
-      if (r < rows && b * (16 / EB) < cols) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(dst + r * ld + b * 16));
+    for (int r0 = 0; r0 < PR; r0 += 64 / L) {
+      const int r = r0 + lane / L, b = lane % L;
+      if (r < min(rows, PR) && b * (16 / EB) < cols) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(buf + r * EP + b * 16);
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(dst + r * ld + b * 16));
+      }
     }
   } else {
-    constexpr int E = 64 / EB;  // elements of a piece's row
+    constexpr int E = PB / EB;  // elements of a piece's row
     const int b = lane % E;
-    for (int r = lane / E; r < 32; r += EB)
+    for (int r = lane / E; r < PR; r += 64 / E)
       if (r < rows && b < cols) {
         if constexpr (EB == 4)
           *reinterpret_cast<uint32_t*>(dst + r * ld + b * 4) = *reinterpret_cast<const uint32_t*>(buf + r * EP + b * 4);
@@ -152,26 +152,29 @@ __device__ inline void store_tile(const GemmArgs& a, const Place& p, const i32x4
   const int lane = fresh_lane();
   constexpr int EB = DT == PARO_F32 ? 4 : 2;
   constexpr bool G = GATED && !PART;
-  constexpr int CF = 4 / EB;  // column fragments of a piece
+  constexpr int YF = G ? T::FN / 2 : T::FN;    // the wave's column fragments of the output,
+  constexpr int CF = YF < 4 / EB ? YF : 4 / EB;  // and a piece's
+  constexpr int RF = T::PR / 16;               // row fragments of a piece
   const int wm = wave / T::WN, wn = wave % T::WN;
-  char* const buf = smem + T::OUT + wave * 32 * T::EP;
+  char* const buf = smem + T::OUT + wave * T::PR * T::EP;
   const float* const sc = reinterpret_cast<const float*>(smem + T::SCALES);
   const size_t ldc = PART ? size_t(c.N) * (GATED ? 2 : 1) : size_t(c.N);  // columns of the output
   char* const out = PART ? reinterpret_cast<char*>(a.part) + size_t(p.split) * c.M * ldc * 4 : static_cast<char*>(c.y);
   const bool whole = c.N % (16 / EB) == 0;  // pieces start at multiples of 16 bytes and end with a row
 #pragma unroll
-  for (int i = 0; i < T::FM; i += 2) {
+  for (int i = 0; i < T::FM; i += RF) {
     const int mf = (wm * T::FM + i) * 16;
-    const float xs[2] = {sc[mf + (lane & 15)], sc[mf + 16 + (lane & 15)]};
+    float xs[RF];
 #pragma unroll
-    for (int y = 0; y < (G ? T::FN / 2 : T::FN); y += CF) {  // column fragments of the output
+    for (int u = 0; u < RF; ++u) xs[u] = sc[mf + u * 16 + (lane & 15)];
+#pragma unroll
+    for (int y = 0; y < YF; y += CF) {
 #pragma unroll
       for (int k = 0; k < CF; ++k) {
-        // the fragment of w (32 gate rows, then their 32 up rows: the up fragment is two further on)
-        const int j = G ? ((y + k) >> 1) * 4 + ((y + k) & 1) : y + k;
-        const float* const wsc = sc + T::BM + (wn * T::FN + j) * 16 + 4 * (lane >> 4);
+        const int j = G ? 2 * (y + k) : y + k;  // the fragment of w (gate fragments and their up fragments in turn)
+        const float* const wsc = sc + T::XS + (wn * T::FN + j) * 16 + 4 * (lane >> 4);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < RF; ++u) {
           char* const at = buf + (u * 16 + (lane & 15)) * T::EP + (16 * k + 4 * (lane >> 4)) * EB;
           if constexpr (PART) {
             *reinterpret_cast<i32x4*>(at) = acc[i + u][j];
@@ -182,10 +185,10 @@ __device__ inline void store_tile(const GemmArgs& a, const Place& p, const i32x4
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = scaled(acc[i + u][j][e], xs[u], w0[e]);
             if constexpr (G) {
-              const float4 u4 = *reinterpret_cast<const float4*>(wsc + 32);
+              const float4 u4 = *reinterpret_cast<const float4*>(wsc + 16);
               const float u0[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], scaled(acc[i + u][j + 2][e], xs[u], u0[e]));
+              for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], scaled(acc[i + u][j + 1][e], xs[u], u0[e]));
             }
             put4<DT>(at, v);
           }
@@ -194,11 +197,11 @@ __device__ inline void store_tile(const GemmArgs& a, const Place& p, const i32x4
       // one wave's LDS accesses are carried out in order; the compiler keeps them in order too
       asm volatile("" ::: "memory");
       // the piece's first column: of y (n), and in the output (the sums of a gated pair keep w's rows)
-      const int r = (wn * T::FN + y) * 16;  // row of w in the tile (not gated output)
-      const int n = p.n0 + (G ? wn * T::FN * 8 + y * 16 : GATED ? (r >> 6) * 32 + (r & 31) : r);
-      const size_t col = n + (PART && GATED && ((r >> 5) & 1) ? size_t(c.N) : 0);
-      store_piece<EB, T::EP>(buf, out + (size_t(p.m0 + mf) * ldc + col) * EB, ldc * EB, c.M - p.m0 - mf, c.N - n, whole,
-                             lane);
+      const int r = wn * T::FN + y;  // fragment of w in the tile (not gated output)
+      const int n = p.n0 + (G ? wn * YF + y : GATED ? r >> 1 : r) * 16;
+      const size_t col = n + (PART && GATED && (r & 1) ? size_t(c.N) : 0);
+      store_piece<EB, T::EP, CF * 16 * EB, T::PR>(buf, out + (size_t(p.m0 + mf) * ldc + col) * EB, ldc * EB,
+                                                  c.M - p.m0 - mf, c.N - n, whole, lane);
       asm volatile("" ::: "memory");
     }
   }
@@ -238,15 +241,15 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
       const int r0 = (wave * T::LOADS + i) * T::RPI;  // first tile row of the load
       const int row = r0 + lane / (T::BK / 16);
       const uint32_t slot = (lane % (T::BK / 16)) * 16;
-      const uint32_t ch = (swz<T::BK>(row, 0) - row * T::BK) ^ slot;  // the chunk that this slot holds
+      const uint32_t ch = (swz(row, 0) - row * T::BK) ^ slot;  // the chunk that this slot holds
       if (r0 < T::BM) {
         src[i] = xb;
         voff[i] = uint32_t(min(row, c.M - 1 - q.m0)) * uint32_t(c.D) + ch;
       } else {
         const int b = row - T::BM;
-        const bool up = GATED && (((r0 - T::BM) >> 5) & 1);
+        const bool up = GATED && (((r0 - T::BM) >> 4) & 1);
         src[i] = wb + (up ? size_t(c.N) * c.D : 0);
-        voff[i] = uint32_t(min(GATED ? (b >> 6) * 32 + (b & 31) : b, c.N - 1 - q.n0)) * uint32_t(c.D) + ch;
+        voff[i] = uint32_t(min(GATED ? (b >> 5) * 16 + (b & 15) : b, c.N - 1 - q.n0)) * uint32_t(c.D) + ch;
       }
     }
   };
@@ -272,15 +275,15 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
   auto load_scales = [&](const Place& p) {
     const int lane = fresh_lane();
 #pragma unroll
-    for (int r0 = 0; r0 < T::ROWS; r0 += 64 * T::NW) {
+    for (int r0 = 0; r0 < T::XS + T::BN; r0 += 64 * T::NW) {
       const int rw = r0 + wave * 64;
-      if (rw >= T::ROWS) break;
+      if (rw >= T::XS + T::BN) break;
       const uint32_t dst = lds0 + T::SCALES + rw * 4;
-      if (rw < T::BM) {
+      if (rw < T::XS) {
         dma4(dst, uint32_t(min(rw + lane, c.M - 1 - p.m0)) * 4, c.xs + p.m0);
       } else {
-        const int b = rw - T::BM + lane;
-        const uint32_t o = GATED ? min((b >> 6) * 32 + (b & 31), c.N - 1 - p.n0) + ((b >> 5) & 1 ? uint32_t(c.N) : 0)
+        const int b = rw - T::XS + lane;
+        const uint32_t o = GATED ? min((b >> 5) * 16 + (b & 15), c.N - 1 - p.n0) + ((b >> 4) & 1 ? uint32_t(c.N) : 0)
                                  : min(b, c.N - 1 - p.n0);
         dma4(dst, o * 4, c.ws + p.n0);
       }
@@ -288,28 +291,29 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
   };
 
   constexpr int SUB = T::BK / 64;
-  // Half a wave's rows of x at a time: while one half's products run, the other half's fragments
-  // (and, before a new 64-channel step, its fragments of w) are read.
-  constexpr int HM = T::FM / 2;
+  // Half a wave's rows of x at a time (all of a single fragment): while one part's products run, the
+  // next part's fragments (and, before a new 64-channel step, its fragments of w) are read.
+  constexpr int NH = T::FM > 1 ? 2 : 1, HM = T::FM / NH;
   i32x4 fx[2][HM], fw[2][T::FN];
-  auto read_x = [&](uint32_t buf, int sub, int half) {
+  auto read_x = [&](uint32_t buf, int h) {  // part h of a stage
     const char* const st = smem + buf * T::STAGE;
 #pragma unroll
     for (int i = 0; i < HM; ++i)
-      fx[half][i] = *reinterpret_cast<const i32x4*>(st + swz<T::BK>((wm * T::FM + half * HM + i) * 16 + (lane & 15), sub * 4 + (lane >> 4)));
+      fx[h & 1][i] = *reinterpret_cast<const i32x4*>(
+          st + swz((wm * T::FM + h % NH * HM + i) * 16 + (lane & 15), h / NH * 4 + (lane >> 4)));
   };
   auto read_w = [&](uint32_t buf, int sub) {
     const char* const st = smem + buf * T::STAGE + T::BM * T::BK;
 #pragma unroll
     for (int j = 0; j < T::FN; ++j)
-      fw[sub & 1][j] = *reinterpret_cast<const i32x4*>(st + swz<T::BK>((wn * T::FN + j) * 16 + (lane & 15), sub * 4 + (lane >> 4)));
+      fw[sub & 1][j] = *reinterpret_cast<const i32x4*>(st + swz((wn * T::FN + j) * 16 + (lane & 15), sub * 4 + (lane >> 4)));
   };
 
 #pragma unroll
   for (int s = 0; s < T::S; ++s) issue(s);
   stage_wait<(T::S - 1) * T::LOADS>();
   read_w(0, 0);
-  read_x(0, 0, 0);
+  read_x(0, 0);
   uint32_t buf = 0;
   for (; tile < end; tile += stride) {
     const Place p = place<T, GATED>(a, tile);
@@ -321,13 +325,11 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
     for (int t = 0; t < p.steps; ++t) {
       const uint32_t nbuf = buf + 1 == T::S ? 0 : buf + 1;
 #pragma unroll
-      for (int h = 0; h < 2 * SUB; ++h) {
-        const int sub = h / 2, half = h & 1;
-        if (half == 0) {
-          read_x(buf, sub, 1);
-        } else if (sub + 1 < SUB) {
-          read_w(buf, sub + 1);
-          read_x(buf, sub + 1, 0);
+      for (int h = 0; h < NH * SUB; ++h) {
+        const int sub = h / NH;
+        if (h + 1 < NH * SUB) {
+          if ((h + 1) % NH == 0) read_w(buf, sub + 1);
+          read_x(buf, h + 1);
         } else {
           // every wave has read this stage: its buffer takes the stage S further on, and the next
           // stage is in LDS
@@ -335,13 +337,14 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
           issue(buf);
           if (t == 0) load_scales(p);  // every wave has stored the last tile
           read_w(nbuf, 0);
-          read_x(nbuf, 0, 0);
+          read_x(nbuf, 0);
         }
 #pragma unroll
         for (int j = 0; j < T::FN; ++j)
 #pragma unroll
           for (int i = 0; i < HM; ++i)
-            acc[half * HM + i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[sub & 1][j], fx[half][i], acc[half * HM + i][j], 0, 0, 0);
+            acc[h % NH * HM + i][j] =
+                __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[sub & 1][j], fx[h & 1][i], acc[h % NH * HM + i][j], 0, 0, 0);
         // a fragment read, then its share of the products, in turn
         constexpr int kShare = HM * T::FN / (HM + T::FN);
 #pragma unroll
@@ -436,49 +439,57 @@ hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st)
   return a.part ? launch_reduce<GATED>(c, part, a.splits, st) : hipSuccess;
 }
 
-// The three tilings: 256 x 256 with 8 waves; 128 x 128 with 4 waves, two workgroups on a CU; the
-// same with four stages in LDS, one workgroup on a CU.
-using T256 = Tile<256, 256, 2, 4, 128, 2>;
-using T128 = Tile<128, 128, 2, 2, 128, 2>;
-using T128Deep = Tile<128, 128, 2, 2, 128, 4>;
+// The tilings: waves side by side in rows and columns, stages in LDS, and workgroups on a CU (by LDS).
+using T256 = Tile<256, 256, 2, 4, 128, 2>;      // 8 waves, one workgroup
+using T128 = Tile<128, 128, 2, 2, 128, 2>;      // two workgroups
+using T128Deep = Tile<128, 128, 2, 2, 128, 4>;  // one
+using T128x64 = Tile<128, 64, 2, 2, 128, 3>;    // one, for units that should be many
+using T64 = Tile<64, 64, 1, 2, 128, 3>;         // two
+using T32 = Tile<32, 64, 1, 2, 128, 4>;         // two
+
+// Estimated time of a call in microseconds, from a fit to 700 measured combinations of shape, tiling
+// and split (MI355X, cold weights, M = 16..2048, D = 1536..14336, N = 1024..28672; 8 % rms off):
+// a launch, then the larger of the weights' way from HBM and the units a CU works through, per 128
+// channels of a unit (alone on a CU, and with `cap` units on it) plus its end; a split adds a launch
+// and its partial sums out and back. The tiling and split with the least estimate are within 1.5 % of
+// the fastest measured on average, 14 % at worst.
+struct TileCost {
+  int bm, bn, cap;
+  double alone, full, end;
+};
+constexpr TileCost kTiles[] = {{256, 256, 1, 1.30, 1.59, 3.1}, {128, 128, 2, 0.92, 1.34, 0.6}, {128, 128, 1, 0.59, 0.63, 1.8},
+                               {128, 64, 1, 0.44, 0.47, 0.7},  {64, 64, 2, 0.38, 0.57, 0.8},   {32, 64, 2, 0.26, 0.385, 0.6}};
+constexpr double kLaunchUs = 2.6, kSplitUs = 3.0, kHbmBytesPerUs = 4.2e6, kPartBytesPerUs = 4.7e6;
+
+// Partial sums of a split reduction at most (larger ones cost more than a split gives).
+constexpr double kMaxPartBytes = double(size_t(128) << 20);
 
 struct Plan {
-  int tile;  // 0: T256, 1: T128, 2: T128Deep
+  int tile;  // index in kTiles
   int splits;
 };
 
-// Partial sums of a split reduction at most (a split past it would cost more than it gives).
-constexpr size_t kMaxPartBytes = size_t(128) << 20;
-
-// The tiling and split with the least estimated time, from rates measured on MI355X (microseconds;
-// x in 8 bits, random codes, D = 128..16384): a call costs about 6 (T256: 9) before its first step
-// of 128 channels; a step of a 128 x 128 tile takes 0.46 on its own CU (T128Deep; 0.52 with two
-// stages) and 0.97 for two on one CU (T128); a step of a 256 x 256 tile 1.15 on a quiet chip and
-// 1.6 when every CU runs one (the power limit then sets the clock). A split adds a launch and the
-// partial sums' way out and back (about 3 TB/s).
 Plan plan_gemm_w8a8(int M, int D, int N, bool gated) {
   const double rows = double(N) * (gated ? 2 : 1);
   const int steps = D / 128;
   Plan best{1, 1};
   double best_us = 1e30;
-  for (int tile = 0; tile < 3; ++tile) {
-    const int b = tile == 0 ? 256 : 128;
-    const double tiles = double((M + b - 1) / b) * double((size_t(N) * (gated ? 2 : 1) + b - 1) / b);
+  for (int t = 0; t < int(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
+    const TileCost& k = kTiles[t];
+    const double tiles = std::ceil(double(M) / k.bm) * std::ceil(rows / k.bn);
     for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (s > 1 && (s > steps || double(s) * M * rows * 4 > double(kMaxPartBytes))) break;
+      const double part = double(s) * M * rows * 4;
+      if (s > 1 && (s > steps || part > kMaxPartBytes)) break;
       const int per = (steps + s - 1) / s;
-      const double units = tiles * ((steps + per - 1) / per);
-      double us;
-      if (tile == 0)
-        us = 9 + std::ceil(units / kCUs) * (per * (1.15 + 0.45 * std::min(1.0, units / kCUs)) + 1);
-      else if (tile == 1)
-        us = 6 + (units <= kCUs ? per * 0.52 : std::ceil(units / (2 * kCUs)) * (per * 0.97 + 1));
-      else
-        us = 6 + std::ceil(units / kCUs) * (per * 0.46 + 1.5);
-      if (s > 1) us += 4 + 2.0 * s * M * rows * 4 / 3e6;
+      const double on_cu = std::ceil(tiles * ((steps + per - 1) / per) / kCUs);  // units of the busiest CU
+      const double rounds = std::floor(on_cu / k.cap), rest = on_cu - rounds * k.cap;
+      double us = rounds * (per * k.full + k.end);
+      if (rest > 0) us += per * (k.cap == 1 ? k.alone : k.alone + (k.full - k.alone) * (rest - 1) / (k.cap - 1)) + k.end;
+      us = kLaunchUs + std::max(us, rows * D / kHbmBytesPerUs);
+      if (s > 1) us += kSplitUs + 2 * part / kPartBytesPerUs;
       if (us < best_us) {
         best_us = us;
-        best = Plan{tile, s};
+        best = Plan{t, s};
       }
     }
   }
@@ -488,9 +499,14 @@ Plan plan_gemm_w8a8(int M, int D, int N, bool gated) {
 template <bool GATED>
 hipError_t launch_plan(const W8A8Call& c, int* part, hipStream_t st) {
   const Plan p = plan_gemm_w8a8(c.M, c.D, c.N, GATED);
-  if (p.tile == 0) return launch_tile<T256, GATED>(c, part, p.splits, st);
-  if (p.tile == 1) return launch_tile<T128, GATED>(c, part, p.splits, st);
-  return launch_tile<T128Deep, GATED>(c, part, p.splits, st);
+  switch (p.tile) {
+    case 0: return launch_tile<T256, GATED>(c, part, p.splits, st);
+    case 1: return launch_tile<T128, GATED>(c, part, p.splits, st);
+    case 2: return launch_tile<T128Deep, GATED>(c, part, p.splits, st);
+    case 3: return launch_tile<T128x64, GATED>(c, part, p.splits, st);
+    case 4: return launch_tile<T64, GATED>(c, part, p.splits, st);
+    default: return launch_tile<T32, GATED>(c, part, p.splits, st);
+  }
 }
 
 }  // namespace
