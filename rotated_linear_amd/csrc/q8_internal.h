@@ -48,8 +48,13 @@ struct W8A8Call {
 // A few rows: the weights streamed into registers, no workspace.
 bool w8a8_stream_takes(int M, int D, int N, bool gated);
 hipError_t launch_w8a8_stream(const W8A8Call& c, hipStream_t st);
-// Any number of rows: the tiled product; part: its workspace.
-size_t w8a8_gemm_workspace_bytes(int M, int D, int N, bool gated);
-hipError_t launch_w8a8_gemm(const W8A8Call& c, int* part, hipStream_t st);
+// Any number of rows: the tiled product.
+struct GemmPlanQ8 {
+  int tile;           // which tiling
+  int splits;         // of the reduction over D
+  size_t part_bytes;  // workspace of the splits' partial sums (0: no split)
+};
+GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated);
+hipError_t launch_w8a8_gemm(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStream_t st);
 
 }  // namespace paro

@@ -464,15 +464,12 @@ constexpr double kLaunchUs = 2.6, kSplitUs = 3.0, kHbmBytesPerUs = 4.2e6, kPartB
 // Partial sums of a split reduction at most (larger ones cost more than a split gives).
 constexpr double kMaxPartBytes = double(size_t(128) << 20);
 
-struct Plan {
-  int tile;  // index in kTiles
-  int splits;
-};
+}  // namespace
 
-Plan plan_gemm_w8a8(int M, int D, int N, bool gated) {
+GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated) {
   const double rows = double(N) * (gated ? 2 : 1);
   const int steps = D / 128;
-  Plan best{1, 1};
+  GemmPlanQ8 best{1, 1, 0};
   double best_us = 1e30;
   for (int t = 0; t < int(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
     const TileCost& k = kTiles[t];
@@ -489,16 +486,17 @@ Plan plan_gemm_w8a8(int M, int D, int N, bool gated) {
       if (s > 1) us += kSplitUs + 2 * part / kPartBytesPerUs;
       if (us < best_us) {
         best_us = us;
-        best = Plan{t, s};
+        best = GemmPlanQ8{t, s, s > 1 ? align256(size_t(part)) : 0};
       }
     }
   }
   return best;
 }
 
+namespace {
+
 template <bool GATED>
-hipError_t launch_plan(const W8A8Call& c, int* part, hipStream_t st) {
-  const Plan p = plan_gemm_w8a8(c.M, c.D, c.N, GATED);
+hipError_t launch_plan(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStream_t st) {
   switch (p.tile) {
     case 0: return launch_tile<T256, GATED>(c, part, p.splits, st);
     case 1: return launch_tile<T128, GATED>(c, part, p.splits, st);
@@ -511,13 +509,8 @@ hipError_t launch_plan(const W8A8Call& c, int* part, hipStream_t st) {
 
 }  // namespace
 
-size_t w8a8_gemm_workspace_bytes(int M, int D, int N, bool gated) {
-  const int s = plan_gemm_w8a8(M, D, N, gated).splits;
-  return s > 1 ? align256(size_t(s) * M * N * (gated ? 2 : 1) * 4) : 0;
-}
-
-hipError_t launch_w8a8_gemm(const W8A8Call& c, int* part, hipStream_t st) {
-  return c.gated ? launch_plan<true>(c, part, st) : launch_plan<false>(c, part, st);
+hipError_t launch_w8a8_gemm(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStream_t st) {
+  return c.gated ? launch_plan<true>(c, p, part, st) : launch_plan<false>(c, p, part, st);
 }
 
 }  // namespace paro

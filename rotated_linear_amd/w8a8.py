@@ -34,10 +34,25 @@ for _name, (_res, _args) in _SIGNATURES.items():
 EXPORTS_W8A8 = tuple(_SIGNATURES)
 
 
-def _ok(t, dtype, shape, name):
-    """A tensor argument of this dtype and shape, contiguous."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
-        _want(t, dtype, shape, name)
+# The current stream's handle by device index (the lookup through a Stream object takes 2 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = torch.cuda.current_device
+
+
+def _fits(t, dtype, shape, index):
+    """Whether t is a contiguous tensor of this dtype and shape on GPU `index`."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index >= 0
+
+
+def _refuse(wants, named):
+    """Raise for the first operand that is not as wanted: (tensor, dtype, shape, name) of those given,
+    then where they live."""
+    for t, dtype, shape, name in wants:
+        if t is not None:
+            _want(t, dtype, shape, name)
+    _on_gpu(named)
+    raise ValueError("operands do not fit together")
 
 
 def _rows(t, name):
@@ -50,64 +65,42 @@ def _rows(t, name):
         raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.shape
-
-
-def _channels(D):
+    M, D = t.shape
     if D % GROUP or not GROUP <= D <= MAX_D:
         raise ParoError(2, "D")
+    return M, D
 
 
-def _device(**named):
-    """The one GPU that every given tensor is on."""
-    dev = None
-    for t in named.values():
-        if t is not None:
-            if dev is None:
-                dev = t.device
-            if t.device != dev or not t.is_cuda:
-                return _on_gpu(named)
-    return dev
-
-
-def _call(fn, what, dev, *args):
-    """fn(*args, current stream of dev), with dev current; raises ParoError on an error status."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream)
+def _call(fn, what, index, *args):
+    """fn(*args, current stream of GPU `index`), with that GPU current; raises on an error status."""
+    if _current_device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(dev):
-            st = fn(*args, stream)
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
     if st:
         _check(st, what)
 
 
-def _q8_out(out, M, D, names=("q", "scales")):
-    """Check a given (codes, scales) pair of outputs."""
-    if out is None:
-        return None, None
-    q, sc = out
-    _ok(q, torch.int8, (M, D), names[0])
-    _ok(sc, torch.float32, (M,), names[1])
-    return q, sc
-
-
-def _norm(x, gamma, residual, residual_out):
-    """Check a norm's operands: (M, D)."""
-    M, D = _rows(x, "x")
-    _channels(D)
-    _ok(gamma, x.dtype, (D,), "gamma")
-    if residual is not None:
-        _ok(residual, x.dtype, (M, D), "residual")
-        if residual_out is not None:
-            _ok(residual_out, x.dtype, (M, D), "residual_out")
-    elif residual_out is not None:
-        raise ValueError("residual_out without residual")
-    return M, D
-
-
 def _p(t):
     return 0 if t is None else t.data_ptr()
+
+
+def _norm(x, gamma, residual, residual_out, outs):
+    """Check a norm's operands and given outputs [(tensor, dtype, shape, name)]: (M, D, GPU)."""
+    M, D = _rows(x, "x")
+    if residual is None and residual_out is not None:
+        raise ValueError("residual_out without residual")
+    index, dtype, shape = x.get_device(), x.dtype, x.shape
+    wants = [(gamma, dtype, (D,), "gamma"), (residual, dtype, shape, "residual"),
+             (residual_out, dtype, shape, "residual_out"), *outs]
+    for t, dt, sh, _ in wants:
+        if t is not None and not (isinstance(t, torch.Tensor) and _fits(t, dt, sh, index)):
+            break
+    else:
+        if index >= 0:
+            return M, D, index
+    _refuse(wants, {"x": x, **{name: t for t, _, _, name in wants}})
 
 
 def paro_rmsnorm_q8(x, gamma, eps=1e-6, residual=None, out=None, residual_out=None):
@@ -115,15 +108,15 @@ def paro_rmsnorm_q8(x, gamma, eps=1e-6, residual=None, out=None, residual_out=No
     (q int8 [M][D], scales float32 [M], h). x, residual float16 or bfloat16 [M][D], gamma [D] of
     that type. ``out``: an optional (q, scales) pair to write; ``residual_out``: where h goes (it
     may be ``residual`` itself). Without ``residual``, h is None."""
-    M, D = _norm(x, gamma, residual, residual_out)
-    q, sc = _q8_out(out, M, D)
-    dev = _device(x=x, gamma=gamma, residual=residual, residual_out=residual_out, q=q, scales=sc)
+    q, sc = (None, None) if out is None else out
+    M, D, index = _norm(x, gamma, residual, residual_out,
+                        () if out is None else ((q, torch.int8, x.shape, "q"), (sc, torch.float32, x.shape[:1], "scales")))
     if q is None:
-        q = torch.empty((M, D), dtype=torch.int8, device=dev)
-        sc = torch.empty(M, dtype=torch.float32, device=dev)
+        q = torch.empty_like(x, dtype=torch.int8)
+        sc = x.new_empty(M, dtype=torch.float32)
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(residual)
-    _call(_lib.paro_rmsnorm_q8, "paro_rmsnorm_q8", dev, M, D, _DTYPE[x.dtype], x.data_ptr(), _p(residual),
+    _call(_lib.paro_rmsnorm_q8, "paro_rmsnorm_q8", index, M, D, _DTYPE[x.dtype], x.data_ptr(), _p(residual),
           gamma.data_ptr(), eps, _p(residual_out), q.data_ptr(), sc.data_ptr())
     return q, sc, residual_out
 
@@ -131,29 +124,32 @@ def paro_rmsnorm_q8(x, gamma, eps=1e-6, residual=None, out=None, residual_out=No
 def paro_rmsnorm(x, gamma, eps=1e-6, residual=None, out=None, residual_out=None):
     """The same norm with its rows in x's type, as paro_rotate and the W4A16 linears read them:
     (y [M][D], h). ``out``: an optional tensor for y."""
-    M, D = _norm(x, gamma, residual, residual_out)
-    if out is not None:
-        _ok(out, x.dtype, (M, D), "out")
-    dev = _device(x=x, gamma=gamma, residual=residual, residual_out=residual_out, out=out)
+    M, D, index = _norm(x, gamma, residual, residual_out, () if out is None else ((out, x.dtype, x.shape, "out"),))
     y = torch.empty_like(x) if out is None else out
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(residual)
-    _call(_lib.paro_rmsnorm, "paro_rmsnorm", dev, M, D, _DTYPE[x.dtype], x.data_ptr(), _p(residual), gamma.data_ptr(),
-          eps, _p(residual_out), y.data_ptr())
+    _call(_lib.paro_rmsnorm, "paro_rmsnorm", index, M, D, _DTYPE[x.dtype], x.data_ptr(), _p(residual),
+          gamma.data_ptr(), eps, _p(residual_out), y.data_ptr())
     return y, residual_out
 
 
 def _quantize(fn, name, what, x, rot, out, out_names):
     M, D = _rows(x, what)
-    _channels(D)
     if rot is not None and rot.D != D:
         raise ValueError(f"{what} has {D} channels, the transform {rot.D}")
-    q, sc = _q8_out(out, M, D, out_names)
-    dev = _device(**{what: x, out_names[0]: q, out_names[1]: sc, "transform": None if rot is None else rot.desc})
+    q, sc = (None, None) if out is None else out
+    index = x.get_device()
+    if index < 0 or (rot is not None and rot.desc.get_device() != index) or not (
+            out is None or (isinstance(q, torch.Tensor) and isinstance(sc, torch.Tensor)
+                            and _fits(q, torch.int8, x.shape, index) and _fits(sc, torch.float32, (M,), index))):
+        wants = () if out is None else ((q, torch.int8, (M, D), out_names[0]), (sc, torch.float32, (M,), out_names[1]))
+        for t, dtype, shape, n in wants:
+            _want(t, dtype, shape, n)
+        _refuse((), {what: x, out_names[0]: q, out_names[1]: sc, "transform": None if rot is None else rot.desc})
     if q is None:
-        q = torch.empty((M, D), dtype=torch.int8, device=dev)
-        sc = torch.empty(M, dtype=torch.float32, device=dev)
-    _call(fn, name, dev, None if rot is None else rot.ptr, M, D, _DTYPE[x.dtype], x.data_ptr(), q.data_ptr(),
+        q = torch.empty_like(x, dtype=torch.int8)
+        sc = x.new_empty(M, dtype=torch.float32)
+    _call(fn, name, index, None if rot is None else rot.ptr, M, D, _DTYPE[x.dtype], x.data_ptr(), q.data_ptr(),
           sc.data_ptr())
     return q, sc
 
@@ -175,17 +171,19 @@ def paro_dequantize_q8(q, scales, out_dtype=torch.float16, out=None):
     if not isinstance(q, torch.Tensor) or q.dim() != 2:
         raise ValueError("q must be a torch.Tensor with two dimensions")
     M, D = q.shape
-    _ok(q, torch.int8, (M, D), "q")
-    _ok(scales, torch.float32, (M,), "scales")
-    _channels(D)
     if out is not None:
         out_dtype = out.dtype
-        _ok(out, out_dtype, (M, D), "out")
     if out_dtype not in _DTYPE:
         raise TypeError(f"the output must be float16, bfloat16 or float32, got {out_dtype}")
-    dev = _device(q=q, scales=scales, out=out)
-    x = torch.empty((M, D), dtype=out_dtype, device=dev) if out is None else out
-    _call(_lib.paro_dequantize_q8, "paro_dequantize_q8", dev, M, D, q.data_ptr(), scales.data_ptr(), x.data_ptr(),
+    index = q.get_device()
+    if not (isinstance(scales, torch.Tensor) and _fits(q, torch.int8, (M, D), index)
+            and _fits(scales, torch.float32, (M,), index) and (out is None or _fits(out, out_dtype, (M, D), index))):
+        _refuse(((q, torch.int8, (M, D), "q"), (scales, torch.float32, (M,), "scales"), (out, out_dtype, (M, D), "out")),
+                {"q": q, "scales": scales, "out": out})
+    if D % GROUP or not GROUP <= D <= MAX_D:
+        raise ParoError(2, "D")
+    x = torch.empty_like(q, dtype=out_dtype) if out is None else out
+    _call(_lib.paro_dequantize_q8, "paro_dequantize_q8", index, M, D, q.data_ptr(), scales.data_ptr(), x.data_ptr(),
           _DTYPE[out_dtype])
     return x
 
@@ -203,28 +201,36 @@ def _linear(fn, name, need_fn, gated, x, x_scales, qweight, w_scales, out_dtype,
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise ValueError(f"{what} must be a torch.Tensor with two dimensions")
     (M, D), rows = x.shape, qweight.shape[0]
-    _ok(x, torch.int8, (M, D), "x")
-    _ok(qweight, torch.int8, (rows, D), "qweight")
-    _ok(x_scales, torch.float32, (M,), "x_scales")
-    _ok(w_scales, torch.float32, (rows,), "w_scales")
-    _channels(D)
     if gated and rows % 2:
         raise ValueError(f"qweight must hold as many gate rows as up rows, got {rows} rows")
     N = rows // 2 if gated else rows
     dtype = out_dtype or (out.dtype if out is not None else torch.float16)
-    if dtype not in _DTYPE:
-        raise TypeError(f"the output must be float16, bfloat16 or float32, got {dtype}")
-    if out is not None:
-        _ok(out, dtype, (M, N), "out")
-    _want_ws(ws)
-    dev = _device(x=x, x_scales=x_scales, qweight=qweight, w_scales=w_scales, out=out, ws=ws)
-    y = torch.empty((M, N), dtype=dtype, device=dev) if out is None else out
+    index = x.get_device()
+    if not (isinstance(x_scales, torch.Tensor) and isinstance(w_scales, torch.Tensor) and dtype in _DTYPE
+            and _fits(x, torch.int8, (M, D), index) and _fits(qweight, torch.int8, (rows, D), index)
+            and _fits(x_scales, torch.float32, (M,), index) and _fits(w_scales, torch.float32, (rows,), index)
+            and (out is None or _fits(out, dtype, (M, N), index))
+            and (ws is None or _fits(ws, torch.uint8, (ws.numel(),), index))):
+        for a in ((x, torch.int8, (M, D), "x"), (qweight, torch.int8, (rows, D), "qweight"),
+                  (x_scales, torch.float32, (M,), "x_scales"), (w_scales, torch.float32, (rows,), "w_scales")):
+            _want(*a)
+        if dtype not in _DTYPE:
+            raise TypeError(f"the output must be float16, bfloat16 or float32, got {dtype}")
+        _want_ws(ws)
+        _refuse(((out, dtype, (M, N), "out"),), {"x": x, "x_scales": x_scales, "qweight": qweight, "w_scales": w_scales,
+                                                "out": out, "ws": ws})
+    if D % GROUP or not GROUP <= D <= MAX_D:
+        raise ParoError(2, "D")
+    y = x.new_empty((M, N), dtype=dtype) if out is None else out
+    ws_bytes = 0
     if ws is None:
-        need = need_fn(M, D, N)
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call(fn, name, dev, M, D, N, x.data_ptr(), x_scales.data_ptr(), qweight.data_ptr(), w_scales.data_ptr(),
-          y.data_ptr(), _DTYPE[dtype], _p(ws), 0 if ws is None else ws.numel())
+        ws_bytes = need_fn(M, D, N)
+        if ws_bytes:
+            ws = x.new_empty(ws_bytes, dtype=torch.uint8)
+    else:
+        ws_bytes = ws.numel()
+    _call(fn, name, index, M, D, N, x.data_ptr(), x_scales.data_ptr(), qweight.data_ptr(), w_scales.data_ptr(),
+          y.data_ptr(), _DTYPE[dtype], _p(ws), ws_bytes)
     return y
 
 
