@@ -58,12 +58,17 @@ __device__ inline RowQuant row_quant(uint32_t top) {
   r.step = kQ8Max / c;
   return r;
 }
-// Four codes as one word (|v * step| <= 127 (1 + 2^-23): rint never passes 127).
-__device__ inline uint32_t codes4(const float (&v)[4], float step) {
-  uint32_t w = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w |= (uint32_t(int(__builtin_rintf(v[i] * step))) & 0xFFu) << (8 * i);
-  return w;
+// rint(v * step) in the low byte: adding 1.5 * 2^23 in the fused multiply-add leaves the nearest
+// whole number (ties to even, the product not rounded before) in the sum's low mantissa bits.
+// |v * step| <= 127 (1 + 2^-23), which never rounds past 127.
+__device__ inline uint32_t code_bits(float v, float step) {
+  return __builtin_bit_cast(uint32_t, __builtin_fmaf(v, step, 12582912.0f));
+}
+// Four codes as one word.
+__device__ inline uint32_t codes4(float a, float b, float c, float d, float step) {
+  const uint32_t ab = __builtin_amdgcn_perm(code_bits(b, step), code_bits(a, step), 0x0c0c0400u);
+  const uint32_t cd = __builtin_amdgcn_perm(code_bits(d, step), code_bits(c, step), 0x04000c0cu);
+  return ab | cd;
 }
 
 // One output of an 8-bit product before its last rounding: sum * xs * ws, two float32 roundings.

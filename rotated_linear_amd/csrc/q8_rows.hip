@@ -1,114 +1,201 @@
 // Row kernels of the 8-bit path: residual addition + RMS norm (8-bit or 16-bit output), the row
-// quantiser, and reading 8-bit rows back.
+// quantiser, and reading 8-bit rows back. All are bound by HBM: one pass over the row, which stays
+// in registers between its statistics and its output.
+#include <algorithm>
+
 #include "q8_device.h"
 
 namespace paro {
 namespace {
 
-constexpr int kRowThreads = 256;
+constexpr int kCUs = 256;
 
-// Maximum (as abs_order) and float64 sum over the workgroup.
-__device__ inline void block_reduce(uint32_t& top, double& sum) {
-  __shared__ uint32_t stop[kRowThreads / 64];
-  __shared__ double ssum[kRowThreads / 64];
-  for (int off = 32; off >= 1; off >>= 1) {
-    top = max(top, uint32_t(__shfl_xor(int(top), off)));
-    sum += __shfl_xor(sum, off);
-  }
-  if ((threadIdx.x & 63) == 0) {
-    stop[threadIdx.x >> 6] = top;
-    ssum[threadIdx.x >> 6] = sum;
-  }
-  __syncthreads();
-  top = stop[0];
-  sum = ssum[0];
-  for (int w = 1; w < kRowThreads / 64; ++w) {
-    top = max(top, stop[w]);
-    sum += ssum[w];
+// One step of a reduction over the wave's lanes by data-parallel moves (row shifts, then broadcasts):
+// lane 63 ends with the result. Lanes without a source keep `v` out of it (max with 0, plus 0).
+template <int CTRL, int ROWS>
+__device__ inline uint32_t dpp(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false));
+}
+template <int CTRL, int ROWS>
+__device__ inline void wave_step(uint32_t& top, double& sum, bool with_sum) {
+  top = max(top, dpp<CTRL, ROWS>(top));
+  if (with_sum) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, sum);
+    sum += __builtin_bit_cast(double, uint64_t(dpp<CTRL, ROWS>(uint32_t(b))) | uint64_t(dpp<CTRL, ROWS>(uint32_t(b >> 32))) << 32);
   }
 }
+__device__ inline void wave_reduce(uint32_t& top, double& sum, bool with_sum) {
+  wave_step<0x111, 0xF>(top, sum, with_sum);  // row_shr:1, 2, 4, 8
+  wave_step<0x112, 0xF>(top, sum, with_sum);
+  wave_step<0x114, 0xF>(top, sum, with_sum);
+  wave_step<0x118, 0xF>(top, sum, with_sum);
+  wave_step<0x142, 0xA>(top, sum, with_sum);  // row_bcast:15 into rows 1 and 3
+  wave_step<0x143, 0xC>(top, sum, with_sum);  // row_bcast:31 into rows 2 and 3
+}
 
-// One workgroup per row. NORM: the norm, else v = x.
-template <int DT, bool NORM, bool Q8>
-__global__ __launch_bounds__(kRowThreads) void rows_kernel(const NormArgs a) {
-  const size_t row = blockIdx.x;
+// A workgroup walks rows blockIdx.x, + gridDim.x, ...; a thread holds VPT chunks of 8 channels. The
+// next row is loaded before this row's statistics are complete. NORM: the norm, else v = x.
+//
+// With t = float32(h * gamma) and inv = float32(1 / sqrt(mean(h^2) + eps)), n = t * inv. Rounding is
+// monotonic, so the row's largest |n| is the largest |t| times inv: one reduction (the sum of squares
+// in float64 and the largest |t|) gives both the norm and the scale.
+template <int DT, bool NORM, bool Q8, int VPT>
+__global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
+  __shared__ uint32_t stop[2][16];
+  __shared__ double ssum[2][16];
+  const int tid = threadIdx.x, nt = blockDim.x, waves = nt / 64;
   const int chunks = a.D / 8;
-  const u32x4* x = reinterpret_cast<const u32x4*>(a.x) + row * chunks;
-  const u32x4* res = a.residual ? reinterpret_cast<const u32x4*>(a.residual) + row * chunks : nullptr;
-  u32x4* ro = a.residual_out ? reinterpret_cast<u32x4*>(a.residual_out) + row * chunks : nullptr;
-  const u32x4* gamma = reinterpret_cast<const u32x4*>(a.gamma);
-  // t = h * gamma in float32 (v = x without the norm)
-  auto load = [&](int c, float(&h)[8], float(&t)[8]) {
-    unpack8<DT>(x[c], h);
-    if constexpr (NORM) {
-      if (res) {
-        float r[8];
-        unpack8<DT>(res[c], r);
-        for (int i = 0; i < 8; ++i) h[i] = from_bits16<DT>(to_bits16<DT>(h[i] + r[i]));
+  const u32x4* const x = static_cast<const u32x4*>(a.x);
+  const u32x4* const res = static_cast<const u32x4*>(a.residual);
+  u32x4* const ro = static_cast<u32x4*>(a.residual_out);
+  u32x4 gw[VPT], xw[VPT], rw[VPT];
+  auto load = [&](size_t row) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = tid + i * nt;
+      if (c < chunks) {
+        xw[i] = x[row * chunks + c];
+        if (NORM && res) rw[i] = res[row * chunks + c];
       }
-      float g[8];
-      unpack8<DT>(gamma[c], g);
-      for (int i = 0; i < 8; ++i) t[i] = h[i] * g[i];
-    } else {
-      for (int i = 0; i < 8; ++i) t[i] = h[i];
     }
   };
-  uint32_t top = 0;
-  double sum = 0;
-  for (int c = threadIdx.x; c < chunks; c += kRowThreads) {
-    float h[8], t[8];
-    load(c, h, t);
-    for (int i = 0; i < 8; ++i) {
-      top = max(top, abs_order(t[i]));
-      if constexpr (NORM) sum += double(h[i]) * double(h[i]);
-    }
-  }
-  block_reduce(top, sum);
-  float inv = 1.0f;
+  size_t row = blockIdx.x;
+  load(row);
   if constexpr (NORM) {
-    inv = float(1.0 / sqrt(sum / a.D + double(a.eps)));
-    top = abs_order(__builtin_bit_cast(float, top) * inv);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+      if (tid + i * nt < chunks) gw[i] = static_cast<const u32x4*>(a.gamma)[tid + i * nt];
   }
-  const RowQuant rq = row_quant(top);
-  for (int c = threadIdx.x; c < chunks; c += kRowThreads) {
-    float h[8], t[8];
-    load(c, h, t);
-    for (int i = 0; i < 8; ++i) t[i] = t[i] * inv;
-    if (NORM && ro) ro[c] = pack8<DT>(h);
-    if constexpr (Q8) {
-      const float lo[4] = {t[0], t[1], t[2], t[3]}, hi[4] = {t[4], t[5], t[6], t[7]};
-      uint32_t* q = reinterpret_cast<uint32_t*>(a.q + row * a.D) + 2 * c;
-      q[0] = rq.bad ? 0u : codes4(lo, rq.step);
-      q[1] = rq.bad ? 0u : codes4(hi, rq.step);
-    } else {
-      reinterpret_cast<u32x4*>(a.y)[row * chunks + c] = pack8<DT>(t);
+  for (int parity = 0;; parity ^= 1) {
+    float t[VPT][8];
+    u32x4 hw[VPT];
+    uint32_t top = 0;
+    double sum = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const bool live = tid + i * nt < chunks;
+      float h[8];
+      unpack8<DT>(xw[i], h);
+      if constexpr (NORM) {
+        if (res) {
+          float r[8];
+          unpack8<DT>(rw[i], r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] += r[e];
+          hw[i] = pack8<DT>(h);
+          unpack8<DT>(hw[i], h);
+        }
+        float g[8];
+        unpack8<DT>(gw[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[i][e] = h[e] * g[e];
+        double s = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = __builtin_fma(double(h[e]), double(h[e]), s);
+        sum += live ? s : 0.0;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[i][e] = h[e];
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = max(m, abs_order(t[i][e]));
+      top = max(top, live ? m : 0u);
     }
+    const size_t next = row + gridDim.x;
+    if (next < size_t(a.M)) load(next);  // uniform
+    if (NORM && res) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (tid + i * nt < chunks) ro[row * chunks + tid + i * nt] = hw[i];
+    }
+    float inv = 1.0f;
+    RowQuant rq{};
+    if (NORM || Q8) {
+      wave_reduce(top, sum, NORM);
+      if ((tid & 63) == 63) {
+        stop[parity][tid >> 6] = top;
+        if constexpr (NORM) ssum[parity][tid >> 6] = sum;
+      }
+      __syncthreads();  // one per row: the other parity's slots are rewritten only after the next one
+      top = 0;
+      sum = 0;
+      for (int w = 0; w < waves; ++w) {
+        top = max(top, stop[parity][w]);
+        if constexpr (NORM) sum += ssum[parity][w];
+      }
+      if constexpr (NORM) {
+        inv = float(1.0 / __builtin_sqrt(sum / a.D + double(a.eps)));
+        top = abs_order(__builtin_bit_cast(float, top) * inv);
+      }
+      rq = row_quant(top);
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int c = tid + i * nt;
+      if (NORM) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[i][e] *= inv;
+      }
+      if (c < chunks) {
+        if constexpr (Q8) {
+          uint2 q = make_uint2(codes4(t[i][0], t[i][1], t[i][2], t[i][3], rq.step),
+                               codes4(t[i][4], t[i][5], t[i][6], t[i][7], rq.step));
+          if (rq.bad) q = make_uint2(0, 0);
+          reinterpret_cast<uint2*>(a.q)[row * chunks + c] = q;
+        } else {
+          static_cast<u32x4*>(a.y)[row * chunks + c] = pack8<DT>(t[i]);
+        }
+      }
+    }
+    if (Q8 && tid == 0) a.scales[row] = rq.scale;
+    if (next >= size_t(a.M)) break;
+    row = next;
   }
-  if (Q8 && threadIdx.x == 0) a.scales[row] = rq.scale;
 }
 
+// Threads take 16 codes each.
 template <int DT>
-__global__ __launch_bounds__(kRowThreads) void dequantize_kernel(int M, int D, const int8_t* q, const float* scales,
-                                                                 void* x) {
-  const size_t i = size_t(blockIdx.x) * kRowThreads + threadIdx.x;  // 8 codes each
-  if (i >= size_t(M) * (D / 8)) return;
-  const float s = scales[i / (D / 8)];
-  float f[8];
-  for (int k = 0; k < 8; ++k) f[k] = float(q[8 * i + k]) * s;
-  if constexpr (DT == PARO_F32) {
-    for (int k = 0; k < 8; ++k) reinterpret_cast<float*>(x)[8 * i + k] = f[k];
-  } else {
-    reinterpret_cast<u32x4*>(x)[i] = pack8<DT>(f);
+__global__ __launch_bounds__(256) void dequantize_kernel(size_t total, uint32_t per_row, const u32x4* q,
+                                                         const float* scales, u32x4* x) {
+  for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += size_t(gridDim.x) * 256) {
+    const float s = scales[total <= 0xFFFFFFFFu ? uint32_t(i) / per_row : i / per_row];
+    const u32x4 w = q[i];
+    float f[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) f[k] = float(int8_t(w[k / 4] >> (8 * (k % 4)))) * s;
+    if constexpr (DT == PARO_F32) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[4 * i + k] = u32x4{__builtin_bit_cast(uint32_t, f[4 * k]), __builtin_bit_cast(uint32_t, f[4 * k + 1]),
+                             __builtin_bit_cast(uint32_t, f[4 * k + 2]), __builtin_bit_cast(uint32_t, f[4 * k + 3])};
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float g[8] = {f[8 * k], f[8 * k + 1], f[8 * k + 2], f[8 * k + 3], f[8 * k + 4], f[8 * k + 5], f[8 * k + 6], f[8 * k + 7]};
+        x[2 * i + k] = pack8<DT>(g);
+      }
+    }
   }
+}
+
+template <int DT, bool NORM, bool Q8>
+hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
+  const int chunks = a.D / 8;
+  // few rows: as many threads as chunks (latency); many rows: two chunks a thread
+  const int vpt = chunks > 1024 || (a.M >= 512 && chunks > 64) ? 2 : 1;
+  const int nt = std::max(64, ((chunks + vpt - 1) / vpt + 63) / 64 * 64);
+  const unsigned grid = unsigned(std::min(a.M, kCUs * (2048 / nt)));
+  if (vpt == 2)
+    hipLaunchKernelGGL((rows_kernel<DT, NORM, Q8, 2>), dim3(grid), dim3(nt), 0, st, a);
+  else
+    hipLaunchKernelGGL((rows_kernel<DT, NORM, Q8, 1>), dim3(grid), dim3(nt), 0, st, a);
+  return hipGetLastError();
 }
 
 template <bool NORM, bool Q8>
 hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
-  if (a.dtype == PARO_F16)
-    hipLaunchKernelGGL((rows_kernel<PARO_F16, NORM, Q8>), dim3(a.M), dim3(kRowThreads), 0, st, a);
-  else
-    hipLaunchKernelGGL((rows_kernel<PARO_BF16, NORM, Q8>), dim3(a.M), dim3(kRowThreads), 0, st, a);
-  return hipGetLastError();
+  return a.dtype == PARO_F16 ? launch_rows<PARO_F16, NORM, Q8>(a, st) : launch_rows<PARO_BF16, NORM, Q8>(a, st);
 }
 
 }  // namespace
@@ -130,14 +217,14 @@ hipError_t launch_quantize_q8(int M, int D, int dtype, const void* x, int8_t* q,
 
 hipError_t launch_dequantize_q8(int M, int D, const int8_t* q, const float* scales, void* x, int dtype,
                                 hipStream_t st) {
-  const unsigned grid = unsigned((size_t(M) * (D / 8) + kRowThreads - 1) / kRowThreads);
-  if (dtype == PARO_F16)
-    hipLaunchKernelGGL((dequantize_kernel<PARO_F16>), dim3(grid), dim3(kRowThreads), 0, st, M, D, q, scales, x);
-  else if (dtype == PARO_BF16)
-    hipLaunchKernelGGL((dequantize_kernel<PARO_BF16>), dim3(grid), dim3(kRowThreads), 0, st, M, D, q, scales, x);
-  else
-    hipLaunchKernelGGL((dequantize_kernel<PARO_F32>), dim3(grid), dim3(kRowThreads), 0, st, M, D, q, scales, x);
-  return hipGetLastError();
+  const size_t total = size_t(M) * (D / 16);
+  const dim3 grid(unsigned(std::min<size_t>((total + 255) / 256, 1 << 16)));
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, total, uint32_t(D / 16), reinterpret_cast<const u32x4*>(q), scales,
+                       static_cast<u32x4*>(x));
+    return hipGetLastError();
+  };
+  return go(dtype == PARO_F16 ? dequantize_kernel<PARO_F16> : dtype == PARO_BF16 ? dequantize_kernel<PARO_BF16> : dequantize_kernel<PARO_F32>);
 }
 
 }  // namespace paro
