@@ -122,16 +122,27 @@ __global__ __launch_bounds__(NT) void rotate_q8_kernel(const RotQ8Args a) {
     asm volatile("" : "+s"(isb));
     using f32x2 = float __attribute__((ext_vector_type(2)));
     const gptr<const f32x2> isp = (gptr<const f32x2>)isb;
-    f32x2 is[PPT];
+    // 1/s of the pairs: kept from one read of the rows to the next, or (the widest 4-row blocks, whose
+    // registers are full) loaded for each
+    constexpr bool kHoldS = !(R == 4 && PPT > 4);
+    f32x2 held[kHoldS ? PPT : 1];
+    if constexpr (kHoldS) {
 #pragma unroll
-    for (int u = 0; u < PPT; ++u) is[u] = isp[min(to + u * NT, P - 1)];
+      for (int u = 0; u < PPT; ++u) held[u] = isp[min(to + u * NT, P - 1)];
+    }
     uint32_t top[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) top[r] = 0;
 #pragma unroll
     for (int u = 0; u < PPT; ++u) {
+      const int j = min(to + u * NT, P - 1);
+      f32x2 is;
+      if constexpr (kHoldS)
+        is = held[u];
+      else
+        is = isp[j];
       float va[R], vb[R];
-      scaled_pair(min(to + u * NT, P - 1), is[u].x, is[u].y, va, vb);
+      scaled_pair(j, is.x, is.y, va, vb);
 #pragma unroll
       for (int r = 0; r < R; ++r) top[r] = max(top[r], max(abs_order(va[r]), abs_order(vb[r])));
     }
@@ -152,8 +163,14 @@ __global__ __launch_bounds__(NT) void rotate_q8_kernel(const RotQ8Args a) {
     uint32_t ov[PPT][(R + 1) / 2];  // two codes a row, two rows a word
 #pragma unroll
     for (int u = 0; u < PPT; ++u) {
+      const int j = min(to + u * NT, P - 1);
+      f32x2 is;
+      if constexpr (kHoldS)
+        is = held[u];
+      else
+        is = isp[j];
       float va[R], vb[R];
-      scaled_pair(min(to + u * NT, P - 1), is[u].x, is[u].y, va, vb);
+      scaled_pair(j, is.x, is.y, va, vb);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         uint32_t w = __builtin_amdgcn_perm(code_bits(vb[r], rq[r].step), code_bits(va[r], rq[r].step), 0x0c0c0400u);
@@ -220,13 +237,14 @@ hipError_t launch_ppt(const RotQ8Args& a, hipStream_t st) {
   if (P <= 1536) return launch_exact<DT, 512, R, 3, (R == 4 ? 2 : 4)>(a, st);
   if (P <= 2048) return launch_exact<DT, 512, R, 4, (R == 1 ? 4 : 2)>(a, st);
   if (P <= 3072) return launch_exact<DT, 512, R, 6, (R == 1 ? 2 : 1)>(a, st);
-  if constexpr (R < 4) {
+  if constexpr (R == 4) {
+    return launch_exact<DT, 1024, R, 5, 1>(a, st);  // 4-row blocks go to 9216 channels
+  } else {
     if (P <= 4608) return launch_exact<DT, 1024, R, 5, (R == 1 ? 2 : 1)>(a, st);
     if (P <= 6144) return launch_exact<DT, 1024, R, 6, 1>(a, st);
     if (P <= 7168) return launch_exact<DT, 1024, R, 7, 1>(a, st);
     return launch_exact<DT, 512, R, 16, 1>(a, st);
   }
-  return hipErrorInvalidValue;  // 4-row blocks go to 6144 channels
 }
 
 template <int DT>
@@ -235,7 +253,7 @@ hipError_t launch_rows(const RotQ8Args& a, hipStream_t st) {
   const size_t row = size_t(a.D) * sizeof(float);
   const auto fits = [&](int r) { return r * row + 16 * r * sizeof(uint32_t) <= kLds; };
   if (a.M <= kCUs || !fits(2)) return launch_ppt<DT, 1>(a, st);
-  if (a.M <= 2 * kCUs || a.D > 6144) return launch_ppt<DT, 2>(a, st);
+  if (a.M <= 2 * kCUs || a.D > 9216) return launch_ppt<DT, 2>(a, st);
   return launch_ppt<DT, 4>(a, st);
 }
 
