@@ -75,7 +75,8 @@ hipError_t launch_pack_q8(const DevRot& R, int N, int dtype, const void* W, int8
                                      : reinterpret_cast<const void*>(&pack_q8_kernel<PARO_BF16>);
   if (lds + 64 > 64 * 1024)
     if (hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, int(lds))) return e;
-  const int nt = std::min(1024, std::max(64, (R.D / 2 / 4 + 63) / 64 * 64));
+  const int share = N <= 256 ? 1 : 4;  // pairs of a thread per stage
+  const int nt = std::min(1024, (R.D / 2 / share + 63) / 64 * 64);
   const dim3 grid(unsigned(std::min(N, 1 << 20)));
   if (dtype == PARO_F16)
     hipLaunchKernelGGL((pack_q8_kernel<PARO_F16>), grid, dim3(nt), lds, st, N, R.D, R.K, static_cast<const uint16_t*>(W), R.rec,
