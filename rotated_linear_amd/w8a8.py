@@ -12,6 +12,7 @@ import torch
 from . import F16, F32, GROUP, MAX_D, ParoError, _check, _i, _lib, _on_gpu, _sz, _vp, _want, _want_ws, paro_rotation
 
 BF16 = 2
+_EWORKSPACE = 5
 _DTYPE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 _ROWS = (torch.float16, torch.bfloat16)
 
@@ -71,15 +72,17 @@ def _rows(t, name):
     return M, D
 
 
-def _call(fn, what, index, *args):
-    """fn(*args, current stream of GPU `index`), with that GPU current; raises on an error status."""
+def _call(fn, what, index, *args, ask=None):
+    """fn(*args, current stream of GPU `index`), with that GPU current; raises on an error status,
+    except that status `ask` is returned."""
     if _current_device() == index:
         st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
             st = fn(*args, _raw_stream(index))
-    if st:
+    if st and st != ask:
         _check(st, what)
+    return st
 
 
 def _p(t):
@@ -207,8 +210,10 @@ def _linear(fn, name, need_fn, gated, x, x_scales, qweight, w_scales, out_dtype,
     dtype = out_dtype or (out.dtype if out is not None else torch.float16)
     index = x.get_device()
     if not (isinstance(x_scales, torch.Tensor) and isinstance(w_scales, torch.Tensor) and dtype in _DTYPE
-            and _fits(x, torch.int8, (M, D), index) and _fits(qweight, torch.int8, (rows, D), index)
-            and _fits(x_scales, torch.float32, (M,), index) and _fits(w_scales, torch.float32, (rows,), index)
+            and x.dtype is torch.int8 is qweight.dtype and x_scales.dtype is torch.float32 is w_scales.dtype
+            and qweight.shape[1] == D and x_scales.shape == (M,) and w_scales.shape == (rows,)
+            and x.is_contiguous() and qweight.is_contiguous() and x_scales.is_contiguous() and w_scales.is_contiguous()
+            and qweight.get_device() == x_scales.get_device() == w_scales.get_device() == index >= 0
             and (out is None or _fits(out, dtype, (M, N), index))
             and (ws is None or _fits(ws, torch.uint8, (ws.numel(),), index))):
         for a in ((x, torch.int8, (M, D), "x"), (qweight, torch.int8, (rows, D), "qweight"),
@@ -219,18 +224,13 @@ def _linear(fn, name, need_fn, gated, x, x_scales, qweight, w_scales, out_dtype,
         _want_ws(ws)
         _refuse(((out, dtype, (M, N), "out"),), {"x": x, "x_scales": x_scales, "qweight": qweight, "w_scales": w_scales,
                                                 "out": out, "ws": ws})
-    if D % GROUP or not GROUP <= D <= MAX_D:
-        raise ParoError(2, "D")
     y = x.new_empty((M, N), dtype=dtype) if out is None else out
-    ws_bytes = 0
-    if ws is None:
-        ws_bytes = need_fn(M, D, N)
-        if ws_bytes:
-            ws = x.new_empty(ws_bytes, dtype=torch.uint8)
-    else:
-        ws_bytes = ws.numel()
-    _call(fn, name, index, M, D, N, x.data_ptr(), x_scales.data_ptr(), qweight.data_ptr(), w_scales.data_ptr(),
-          y.data_ptr(), _DTYPE[dtype], _p(ws), ws_bytes)
+    args = (M, D, N, x.data_ptr(), x_scales.data_ptr(), qweight.data_ptr(), w_scales.data_ptr(), y.data_ptr(), _DTYPE[dtype])
+    if ws is not None:
+        _call(fn, name, index, *args, ws.data_ptr(), ws.numel())
+    elif _call(fn, name, index, *args, 0, 0, ask=_EWORKSPACE):  # the call wants a workspace: it has done nothing yet
+        ws = x.new_empty(need_fn(M, D, N), dtype=torch.uint8)
+        _call(fn, name, index, *args, ws.data_ptr(), ws.numel())
     return y
 
 
