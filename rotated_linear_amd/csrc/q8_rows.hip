@@ -154,27 +154,23 @@ __global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
   }
 }
 
-// Threads take 16 codes each.
+// Threads take 8 codes each: a wave reads and writes whole lines.
 template <int DT>
-__global__ __launch_bounds__(256) void dequantize_kernel(size_t total, uint32_t per_row, const u32x4* q,
+__global__ __launch_bounds__(256) void dequantize_kernel(size_t total, uint32_t per_row, const uint2* q,
                                                          const float* scales, u32x4* x) {
   for (size_t i = size_t(blockIdx.x) * 256 + threadIdx.x; i < total; i += size_t(gridDim.x) * 256) {
     const float s = scales[total <= 0xFFFFFFFFu ? uint32_t(i) / per_row : i / per_row];
-    const u32x4 w = q[i];
-    float f[16];
+    const uint2 w = q[i];
+    float f[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) f[k] = float(int8_t(w[k / 4] >> (8 * (k % 4)))) * s;
+    for (int k = 0; k < 8; ++k) f[k] = float(int8_t((k < 4 ? w.x : w.y) >> (8 * (k % 4)))) * s;
     if constexpr (DT == PARO_F32) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        x[4 * i + k] = u32x4{__builtin_bit_cast(uint32_t, f[4 * k]), __builtin_bit_cast(uint32_t, f[4 * k + 1]),
+      for (int k = 0; k < 2; ++k)
+        x[2 * i + k] = u32x4{__builtin_bit_cast(uint32_t, f[4 * k]), __builtin_bit_cast(uint32_t, f[4 * k + 1]),
                              __builtin_bit_cast(uint32_t, f[4 * k + 2]), __builtin_bit_cast(uint32_t, f[4 * k + 3])};
     } else {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float g[8] = {f[8 * k], f[8 * k + 1], f[8 * k + 2], f[8 * k + 3], f[8 * k + 4], f[8 * k + 5], f[8 * k + 6], f[8 * k + 7]};
-        x[2 * i + k] = pack8<DT>(g);
-      }
+      x[i] = pack8<DT>(f);
     }
   }
 }
@@ -217,10 +213,10 @@ hipError_t launch_quantize_q8(int M, int D, int dtype, const void* x, int8_t* q,
 
 hipError_t launch_dequantize_q8(int M, int D, const int8_t* q, const float* scales, void* x, int dtype,
                                 hipStream_t st) {
-  const size_t total = size_t(M) * (D / 16);
+  const size_t total = size_t(M) * (D / 8);
   const dim3 grid(unsigned(std::min<size_t>((total + 255) / 256, 1 << 16)));
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, total, uint32_t(D / 16), reinterpret_cast<const u32x4*>(q), scales,
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, total, uint32_t(D / 8), reinterpret_cast<const uint2*>(q), scales,
                        static_cast<u32x4*>(x));
     return hipGetLastError();
   };

@@ -443,23 +443,26 @@ hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st)
 using T256 = Tile<256, 256, 2, 4, 128, 2>;      // 8 waves, one workgroup
 using T128 = Tile<128, 128, 2, 2, 128, 2>;      // two workgroups
 using T128Deep = Tile<128, 128, 2, 2, 128, 4>;  // one
-using T128x64 = Tile<128, 64, 2, 2, 128, 3>;    // one, for units that should be many
+using T128x64 = Tile<128, 64, 2, 2, 128, 3>;    // one
+using T64x128 = Tile<64, 128, 1, 4, 128, 3>;    // one
 using T64 = Tile<64, 64, 1, 2, 128, 3>;         // two
 using T32 = Tile<32, 64, 1, 2, 128, 4>;         // two
 
-// Estimated time of a call in microseconds, from a fit to 700 measured combinations of shape, tiling
-// and split (MI355X, cold weights, M = 16..2048, D = 1536..14336, N = 1024..28672; 8 % rms off):
-// a launch, then the larger of the weights' way from HBM and the units a CU works through, per 128
-// channels of a unit (alone on a CU, and with `cap` units on it) plus its end; a split adds a launch
-// and its partial sums out and back. The tiling and split with the least estimate are within 1.5 % of
-// the fastest measured on average, 14 % at worst.
+// Estimated time of a call in microseconds, from a fit to 616 measured combinations of shape, tiling
+// and split (MI355X, cold weights, M = 16..2048, D = 1536..14336, N = 1024..28672; 7 % rms off): a
+// launch; the units that a CU works through, per 128 channels of a unit (alone on a CU, and with
+// `cap` units on it) plus its end; the weights' way from HBM; these two joined as the cube root of
+// the sum of their cubes, since they overlap but not wholly; and for a split a launch and the partial
+// sums out and back. The choice by it was 1.4 % slower than the fastest measured one on average, 14 %
+// at worst.
 struct TileCost {
   int bm, bn, cap;
   double alone, full, end;
 };
-constexpr TileCost kTiles[] = {{256, 256, 1, 1.30, 1.59, 3.1}, {128, 128, 2, 0.92, 1.34, 0.6}, {128, 128, 1, 0.59, 0.63, 1.8},
-                               {128, 64, 1, 0.44, 0.47, 0.7},  {64, 64, 2, 0.38, 0.57, 0.8},   {32, 64, 2, 0.26, 0.385, 0.6}};
-constexpr double kLaunchUs = 2.6, kSplitUs = 3.0, kHbmBytesPerUs = 4.2e6, kPartBytesPerUs = 4.7e6;
+constexpr TileCost kTiles[] = {{256, 256, 1, 1.29, 1.42, 3.15}, {128, 128, 2, 0.92, 1.31, 0.63}, {128, 128, 1, 0.59, 0.62, 1.69},
+                               {128, 64, 1, 0.434, 0.46, 0.68}, {64, 128, 1, 0.465, 0.487, 0.48}, {64, 64, 2, 0.374, 0.563, 0.79},
+                               {32, 64, 2, 0.253, 0.384, 0.54}};
+constexpr double kLaunchUs = 2.66, kSplitUs = 2.9, kHbmBytesPerUs = 5.13e6, kPartBytesPerUs = 4.67e6;
 
 // Partial sums of a split reduction at most (larger ones cost more than a split gives).
 constexpr double kMaxPartBytes = double(size_t(128) << 20);
@@ -482,7 +485,8 @@ GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated) {
       const double rounds = std::floor(on_cu / k.cap), rest = on_cu - rounds * k.cap;
       double us = rounds * (per * k.full + k.end);
       if (rest > 0) us += per * (k.cap == 1 ? k.alone : k.alone + (k.full - k.alone) * (rest - 1) / (k.cap - 1)) + k.end;
-      us = kLaunchUs + std::max(us, rows * D / kHbmBytesPerUs);
+      const double hbm = rows * D / kHbmBytesPerUs;
+      us = kLaunchUs + std::cbrt(us * us * us + hbm * hbm * hbm);
       if (s > 1) us += kSplitUs + 2 * part / kPartBytesPerUs;
       if (us < best_us) {
         best_us = us;
@@ -502,7 +506,8 @@ hipError_t launch_plan(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStr
     case 1: return launch_tile<T128, GATED>(c, part, p.splits, st);
     case 2: return launch_tile<T128Deep, GATED>(c, part, p.splits, st);
     case 3: return launch_tile<T128x64, GATED>(c, part, p.splits, st);
-    case 4: return launch_tile<T64, GATED>(c, part, p.splits, st);
+    case 4: return launch_tile<T64x128, GATED>(c, part, p.splits, st);
+    case 5: return launch_tile<T64, GATED>(c, part, p.splits, st);
     default: return launch_tile<T32, GATED>(c, part, p.splits, st);
   }
 }
