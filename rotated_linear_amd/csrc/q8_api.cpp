@@ -30,6 +30,9 @@ bool any_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
   return false;
 }
 
+// The byte offsets of a gated call's 2 F scales stay below 2^32.
+constexpr int kMaxGatedF = (1 << 29) - 1;
+
 bool good_ptr(const void* p) { return p && aligned16(p); }
 bool good_D(int D) { return D >= PARO_GROUP && D <= PARO_MAX_D && D % PARO_GROUP == 0; }
 bool row_dtype(int t) { return t == PARO_F16 || t == PARO_BF16; }
@@ -70,8 +73,7 @@ paro_status norm(int M, int D, int dtype, const void* x, const void* residual, c
 
 paro_status linear(int M, int D, int N, bool gated, const int8_t* x, const float* xs, const int8_t* w, const float* wsc,
                    void* y, int ydtype, void* ws, size_t ws_bytes, void* stream) {
-  // a gated call's 2 N weight rows are counted in int
-  if (M < 0 || N < 0 || (gated && N > (1 << 30) - 1) || !out_dtype(ydtype)) return PARO_EINVAL;
+  if (M < 0 || N < 0 || (gated && N > kMaxGatedF) || !out_dtype(ydtype)) return PARO_EINVAL;
   if (!good_D(D)) return PARO_ESHAPE;
   if (M == 0 || N == 0) return PARO_OK;
   if (!good_ptr(x) || !good_ptr(xs) || !good_ptr(w) || !good_ptr(wsc) || !good_ptr(y)) return PARO_EINVAL;
@@ -153,7 +155,7 @@ size_t paro_w8a8_workspace_bytes(int M, int D, int N) {
 }
 
 size_t paro_w8a8_gated_workspace_bytes(int M, int D, int F) {
-  if (M <= 0 || F <= 0 || F > (1 << 30) - 1 || !good_D(D) || w8a8_stream_takes(M, D, F, true)) return 0;
+  if (M <= 0 || F <= 0 || F > kMaxGatedF || !good_D(D) || w8a8_stream_takes(M, D, F, true)) return 0;
   return plan_gemm_w8a8(M, D, F, true).part_bytes;
 }
 

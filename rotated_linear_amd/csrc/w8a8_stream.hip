@@ -128,7 +128,10 @@ hipError_t launch_rows(const W8A8Call& c, hipStream_t st) {
 // 32 MB of weights the tiled kernel, which shares x through LDS, is faster there. Measured, cold
 // weights, M = 16: 4096 -> 4096 7.4 us here, 9.5 tiled; 14336 -> 4096 20.7 and 16.4; gated 4096 ->
 // 14336 31.4 and 28.1. Up to 8 rows the stream always wins (M = 8, 4096 -> 4096: 6.0 and 9.5).
+// (A grid of more than 2^32 threads cannot be launched: layers of more than 2^24 columns go to the
+// tiled kernel, whose grid does not grow with them.)
 bool w8a8_stream_takes(int M, int D, int N, bool gated) {
+  if (N > 1 << 24) return false;
   return M <= 8 || (M <= 16 && size_t(N) * (gated ? 2 : 1) * D <= size_t(32) << 20);
 }
 

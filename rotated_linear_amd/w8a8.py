@@ -57,7 +57,7 @@ def _refuse(wants, named):
 
 
 def _rows(t, name):
-    """A 2-d tensor of float16 or bfloat16 rows: its sizes."""
+    """Refuse anything but contiguous 2-d float16 or bfloat16 rows of channels the library takes."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _ROWS:
@@ -66,10 +66,8 @@ def _rows(t, name):
         raise ValueError(f"{name} must have two dimensions, got shape {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    M, D = t.shape
-    if D % GROUP or not GROUP <= D <= MAX_D:
+    if t.shape[1] % GROUP or not GROUP <= t.shape[1] <= MAX_D:
         raise ParoError(2, "D")
-    return M, D
 
 
 def _call(fn, what, index, *args, ask=None):
@@ -91,19 +89,23 @@ def _p(t):
 
 def _norm(x, gamma, residual, residual_out, outs):
     """Check a norm's operands and given outputs [(tensor, dtype, shape, name)]: (M, D, GPU)."""
-    M, D = _rows(x, "x")
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _ROWS or not x.is_contiguous():
+        _rows(x, "x")
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    M, D = shape
     if residual is None and residual_out is not None:
         raise ValueError("residual_out without residual")
-    index, dtype, shape = x.get_device(), x.dtype, x.shape
-    wants = [(gamma, dtype, (D,), "gamma"), (residual, dtype, shape, "residual"),
-             (residual_out, dtype, shape, "residual_out"), *outs]
-    for t, dt, sh, _ in wants:
-        if t is not None and not (isinstance(t, torch.Tensor) and _fits(t, dt, sh, index)):
-            break
-    else:
-        if index >= 0:
-            return M, D, index
-    _refuse(wants, {"x": x, **{name: t for t, _, _, name in wants}})
+    if (index < 0 or D % GROUP or not GROUP <= D <= MAX_D
+            or not isinstance(gamma, torch.Tensor) or not _fits(gamma, dtype, (D,), index)
+            or (residual is not None and not (isinstance(residual, torch.Tensor) and _fits(residual, dtype, shape, index)))
+            or (residual_out is not None and not (isinstance(residual_out, torch.Tensor)
+                                                  and _fits(residual_out, dtype, shape, index)))
+            or not all(isinstance(t, torch.Tensor) and _fits(t, dt, sh, index) for t, dt, sh, _ in outs)):
+        _rows(x, "x")
+        wants = [(gamma, dtype, (D,), "gamma"), (residual, dtype, shape, "residual"),
+                 (residual_out, dtype, shape, "residual_out"), *outs]
+        _refuse(wants, {"x": x, **{name: t for t, _, _, name in wants}})
+    return M, D, index
 
 
 def paro_rmsnorm_q8(x, gamma, eps=1e-6, residual=None, out=None, residual_out=None):
@@ -137,16 +139,18 @@ def paro_rmsnorm(x, gamma, eps=1e-6, residual=None, out=None, residual_out=None)
 
 
 def _quantize(fn, name, what, x, rot, out, out_names):
-    M, D = _rows(x, what)
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.dtype not in _ROWS or not x.is_contiguous():
+        _rows(x, what)
+    (M, D), index = x.shape, x.get_device()
     if rot is not None and rot.D != D:
         raise ValueError(f"{what} has {D} channels, the transform {rot.D}")
     q, sc = (None, None) if out is None else out
-    index = x.get_device()
-    if index < 0 or (rot is not None and rot.desc.get_device() != index) or not (
-            out is None or (isinstance(q, torch.Tensor) and isinstance(sc, torch.Tensor)
-                            and _fits(q, torch.int8, x.shape, index) and _fits(sc, torch.float32, (M,), index))):
-        wants = () if out is None else ((q, torch.int8, (M, D), out_names[0]), (sc, torch.float32, (M,), out_names[1]))
-        for t, dtype, shape, n in wants:
+    if (index < 0 or D % GROUP or not GROUP <= D <= MAX_D or (rot is not None and rot.desc.get_device() != index)
+            or (out is not None and not (isinstance(q, torch.Tensor) and isinstance(sc, torch.Tensor)
+                                         and _fits(q, torch.int8, x.shape, index) and _fits(sc, torch.float32, (M,), index)))):
+        _rows(x, what)
+        for t, dtype, shape, n in () if out is None else ((q, torch.int8, (M, D), out_names[0]),
+                                                          (sc, torch.float32, (M,), out_names[1])):
             _want(t, dtype, shape, n)
         _refuse((), {what: x, out_names[0]: q, out_names[1]: sc, "transform": None if rot is None else rot.desc})
     if q is None:

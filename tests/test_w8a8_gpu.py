@@ -332,6 +332,63 @@ def test_gated_linear(M, D, F):
     assert torch.equal(y, rl.paro_w8a8_gated_linear(*d, torch.float32))
 
 
+# Every tiling of the tiled kernel: one tile per workgroup and several, reductions whole and split,
+# ragged ends and rows of y at 16-byte boundaries.
+TILED = [(654, 384, 11023, False), (1606, 256, 15152, False), (138, 11904, 5769, False), (258, 384, 11466, True), (1158, 256, 9798, True),
+         (134, 12032, 2840, True), (129, 128, 12350, False), (514, 128, 13270, False), (514, 128, 13272, False), (68, 128, 8478, True),
+         (260, 128, 10981, True), (260, 128, 10984, True), (71, 9472, 8197, True), (129, 512, 13533, False), (2075, 13824, 65, False),
+         (2881, 9728, 70, False), (66, 640, 8975, True), (2713, 8064, 37, True), (2778, 9728, 34, True), (4409, 128, 391, False),
+         (3739, 256, 1032, False), (2831, 2688, 23, False), (4163, 128, 193, True), (2973, 256, 665, True), (2841, 6912, 17, True),
+         (69, 128, 11270, False), (270, 128, 11200, False), (33, 4224, 1481, False), (702, 5504, 134, False), (33, 128, 9174, True),
+         (130, 128, 8624, True), (33, 4224, 803, True), (1060, 4736, 33, True), (413, 128, 4667, False), (1160, 768, 3330, False),
+         (1067, 7808, 265, False), (278, 15488, 544, False), (820, 128, 1219, True), (1185, 768, 1666, True), (1303, 11008, 65, True),
+         (129, 384, 10994, False), (1034, 3200, 17, False), (65, 384, 9115, True), (34, 2688, 713, True)]
+
+
+@pytest.mark.parametrize("M,D,N,gated", TILED)
+def test_tiled_kernel(M, D, N, gated):
+    C.log(f"w8a8 tiled M={M} D={D} N={N} gated={gated}")
+    xq, xs, wq, ws = operands(54, M, D, N * (2 if gated else 1))
+    if gated:
+        ws = ws * np.float32(20)
+        ref, g, u = Q.gated(xq, xs, wq, ws)
+    else:
+        ref = Q.linear(xq, xs, wq, ws)
+    fn = rl.paro_w8a8_gated_linear if gated else rl.paro_w8a8_linear
+    need = (rl.paro_w8a8_gated_workspace_bytes if gated else rl.paro_w8a8_workspace_bytes)(M, D, N)
+    d = on_gpu(xq, xs, wq, ws)
+    work = torch.full((max(need, 16),), 0xA5, dtype=torch.uint8, device="cuda")
+    for dt in ("bf16", "f32"):
+        y, ok = guarded((M, N), DT[dt])
+        fn(*d, out=y, ws=work)
+        assert ok()
+        bound = gated_bound(ref, g, u, dt) if gated else linear_bound(ref, dt)
+        assert over(y.double().cpu().numpy() - ref, bound) <= 1, dt
+
+
+@pytest.mark.parametrize("D,N", [(256, 70), (1536, 256), (4096, 640), (8960, 136)])
+def test_rows_do_not_depend_on_the_other_rows(D, N):
+    """A row alone (streamed weights), in a short batch and in a long one (every kernel and split):
+    the same bits, for the linears, the gated ones and the row kernels."""
+    M = 600
+    xq, xs, wq, ws = on_gpu(*operands(55, M, D, N))
+    x, _ = rows(56, M, D, "f16")
+    g = torch.ones(D, dtype=torch.float16, device="cuda")
+    for dt in (torch.float16, torch.float32):
+        full = rl.paro_w8a8_linear(xq, xs, wq, ws, dt)
+        full_g = rl.paro_w8a8_gated_linear(xq, xs, wq, ws, dt)
+        for m in (1, 3, 7, 12, 16, 17, 40, 64, 65, 130, 300):
+            assert torch.equal(rl.paro_w8a8_linear(xq[:m], xs[:m], wq, ws, dt), full[:m]), (m, dt)
+            assert torch.equal(rl.paro_w8a8_gated_linear(xq[:m], xs[:m], wq, ws, dt), full_g[:m]), (m, dt)
+    q, s, h = rl.paro_rmsnorm_q8(x, g, residual=x)
+    p, t = rl.paro_quantize_q8(x)
+    for m in (1, 5, 100):
+        q1, s1, h1 = rl.paro_rmsnorm_q8(x[:m], g, residual=x[:m])
+        assert torch.equal(q1, q[:m]) and torch.equal(s1, s[:m]) and torch.equal(h1, h[:m])
+        p1, t1 = rl.paro_quantize_q8(x[:m])
+        assert torch.equal(p1, p[:m]) and torch.equal(t1, t[:m])
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_linear_extreme_sums(M):
     """All codes -128 or 127 at D = 16384: sums of +-2^28 are exact in float32."""
