@@ -29,9 +29,9 @@ COMMON = [
 EXTRA = {"pack.hip": ["-ffp-contract=off"], "q8_pack.hip": ["-ffp-contract=off"], "gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          "skinny.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
          # inline assembly names m0, a register the compiler keeps for itself
-         "w8a8_gemm.hip": ["-Wno-inline-asm"]}
+         "w8a8_column.hip": ["-Wno-inline-asm"], "w8a8_gemm.hip": ["-Wno-inline-asm"]}
 SOURCES = ["paro_api.cpp", "schedule.cpp", "pack.hip", "rotate.hip", "decode.hip", "gemm.hip", "skinny.hip", "noalloc.hip",
-           "q8_api.cpp", "q8_rows.hip", "q8_rotate.hip", "q8_pack.hip", "w8a8_stream.hip", "w8a8_gemm.hip"]
+           "q8_api.cpp", "q8_rows.hip", "q8_rotate.hip", "q8_pack.hip", "w8a8_stream.hip", "w8a8_column.hip", "w8a8_gemm.hip"]
 
 
 def _hipcc() -> str:

@@ -41,6 +41,18 @@ size_t dtype_bytes(int t) { return t == PARO_F32 ? 4 : 2; }
 paro_status from_hip(hipError_t e) { return e == hipSuccess ? PARO_OK : PARO_EHIP; }
 hipStream_t as_stream(void* s) { return static_cast<hipStream_t>(s); }
 
+// The kernel of an 8-bit product: a function of its shape only.
+enum class Kernel { kStream, kColumn, kTiled };
+struct Plan {
+  Kernel kernel;
+  GemmPlanQ8 tiled;
+};
+Plan plan(int M, int D, int N, bool gated) {
+  if (w8a8_stream_takes(M, N)) return Plan{Kernel::kStream, {}};
+  const GemmPlanQ8 t = plan_gemm_w8a8(M, D, N, gated);
+  return w8a8_column_us(M, D, N, gated) <= t.us ? Plan{Kernel::kColumn, {}} : Plan{Kernel::kTiled, t};
+}
+
 // The transform of a call (r may be NULL); *out is filled either way.
 paro_status check_rot(const paro_rotation* r, int D, DevRot* out, Span* desc) {
   *out = DevRot{0, D, nullptr, nullptr, nullptr};
@@ -78,17 +90,18 @@ paro_status linear(int M, int D, int N, bool gated, const int8_t* x, const float
   if (M == 0 || N == 0) return PARO_OK;
   if (!good_ptr(x) || !good_ptr(xs) || !good_ptr(w) || !good_ptr(wsc) || !good_ptr(y)) return PARO_EINVAL;
   const size_t rows = size_t(N) * (gated ? 2 : 1);
-  const bool stream_weights = w8a8_stream_takes(M, D, N, gated);
-  const GemmPlanQ8 plan = stream_weights ? GemmPlanQ8{0, 1, 0} : plan_gemm_w8a8(M, D, N, gated);
-  const size_t need = plan.part_bytes;
+  const Plan p = plan(M, D, N, gated);
+  const size_t need = p.tiled.part_bytes;
   if (need && (!ws || ws_bytes < need)) return PARO_EWORKSPACE;
   if (need && !aligned16(ws)) return PARO_EINVAL;
   const Span outs[] = {{y, size_t(M) * N * dtype_bytes(ydtype)}, {need ? ws : nullptr, need}};
   const Span ins[] = {{x, size_t(M) * D}, {xs, size_t(M) * 4}, {w, rows * D}, {wsc, rows * 4}};
   if (any_overlap(outs, ins)) return PARO_EINVAL;
   const W8A8Call c{M, D, N, gated, x, xs, w, wsc, y, ydtype};
-  return from_hip(stream_weights ? launch_w8a8_stream(c, as_stream(stream))
-                                 : launch_w8a8_gemm(c, plan, static_cast<int*>(ws), as_stream(stream)));
+  const hipStream_t st = as_stream(stream);
+  return from_hip(p.kernel == Kernel::kStream   ? launch_w8a8_stream(c, st)
+                  : p.kernel == Kernel::kColumn ? launch_w8a8_column(c, st)
+                                                : launch_w8a8_gemm(c, p.tiled, static_cast<int*>(ws), st));
 }
 
 }  // namespace
@@ -151,12 +164,11 @@ paro_status paro_pack_weights_q8(const paro_rotation* r, int N, int D, int dtype
 }
 
 size_t paro_w8a8_workspace_bytes(int M, int D, int N) {
-  return M > 0 && N > 0 && good_D(D) && !w8a8_stream_takes(M, D, N, false) ? plan_gemm_w8a8(M, D, N, false).part_bytes : 0;
+  return M > 0 && N > 0 && good_D(D) ? plan(M, D, N, false).tiled.part_bytes : 0;
 }
 
 size_t paro_w8a8_gated_workspace_bytes(int M, int D, int F) {
-  if (M <= 0 || F <= 0 || F > kMaxGatedF || !good_D(D) || w8a8_stream_takes(M, D, F, true)) return 0;
-  return plan_gemm_w8a8(M, D, F, true).part_bytes;
+  return M > 0 && F > 0 && F <= kMaxGatedF && good_D(D) ? plan(M, D, F, true).tiled.part_bytes : 0;
 }
 
 paro_status paro_w8a8_linear(int M, int D, int N, const int8_t* x, const float* xscales, const int8_t* qweight,

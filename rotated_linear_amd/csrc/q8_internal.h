@@ -45,14 +45,18 @@ struct W8A8Call {
   void* y;
   int ydtype;
 };
-// A few rows: the weights streamed into registers, no workspace.
-bool w8a8_stream_takes(int M, int D, int N, bool gated);
+// A row or two: the weights streamed into registers, no workspace.
+bool w8a8_stream_takes(int M, int N);
 hipError_t launch_w8a8_stream(const W8A8Call& c, hipStream_t st);
+// Up to 64 rows: 16 columns a workgroup, no workspace. Its estimated time (1e30: not taken).
+double w8a8_column_us(int M, int D, int N, bool gated);
+hipError_t launch_w8a8_column(const W8A8Call& c, hipStream_t st);
 // Any number of rows: the tiled product.
 struct GemmPlanQ8 {
   int tile;           // which tiling
   int splits;         // of the reduction over D
   size_t part_bytes;  // workspace of the splits' partial sums (0: no split)
+  double us;          // estimated time
 };
 GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated);
 hipError_t launch_w8a8_gemm(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStream_t st);

@@ -1,8 +1,8 @@
-// The 8-bit products for more rows than the streaming kernel takes: tiled matrix-core GEMM.
+// The 8-bit products for more rows than the other kernels take: tiled matrix-core GEMM.
 #include <algorithm>
 #include <cmath>
 
-#include "q8_device.h"
+#include "w8a8_dma.h"
 
 namespace paro {
 namespace {
@@ -10,26 +10,6 @@ namespace {
 constexpr int kCUs = 256;
 constexpr int kXcds = 8;
 
-// 16 (4) bytes per lane straight into LDS: lane l's land at lds + 16 l (4 l). The compiler does not
-// see these loads, so the kernel waits for them itself (stage_wait); they have no output register.
-__device__ inline void dma16(uint32_t lds, uint32_t voff, const void* base) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %1, %2"
-      :
-      : "s"(lds), "v"(voff), "s"(base)
-      : "memory", "m0");
-}
-__device__ inline void dma4(uint32_t lds, uint32_t voff, const void* base) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "global_load_lds_dword %1, %2"
-      :
-      : "s"(lds), "v"(voff), "s"(base)
-      : "memory", "m0");
-}
 // All but the N youngest of this wave's memory operations are done and so are its LDS reads; then
 // the workgroup's waves meet.
 template <int N>
@@ -72,10 +52,6 @@ struct Tile {
   static constexpr int LDS = SCALES + (XS + BN) * 4;
   static_assert(XS % 64 == 0 && BN % 64 == 0 && LDS <= 160 * 1024, "scales 64 a load; one CU's LDS");
 };
-
-// Byte offset of chunk c (16 bytes) of a tile row in a stage: rows of 128 bytes, the chunk index
-// mixed with the row so that 16 consecutive rows' chunk c lie in 16 distinct slots modulo 256 bytes.
-__device__ inline uint32_t swz(uint32_t row, uint32_t c) { return row * 128 + ((c ^ ((row >> 1) & 7)) << 4); }
 
 // Where a tile lies.
 struct Place {
@@ -254,7 +230,7 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
     }
   };
   aim();
-  const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)smem));
+  const uint32_t lds0 = lds_address(smem);
   const uint32_t ldsw = __builtin_amdgcn_readfirstlane(lds0 + uint32_t(wave * T::LOADS) * 1024);
   auto issue = [&](uint32_t buf) {  // the next stage into buffer `buf`; after the last tile its last stage again
     if (at == q.steps) {
@@ -472,8 +448,7 @@ constexpr double kMaxPartBytes = double(size_t(128) << 20);
 GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated) {
   const double rows = double(N) * (gated ? 2 : 1);
   const int steps = D / 128;
-  GemmPlanQ8 best{1, 1, 0};
-  double best_us = 1e30;
+  GemmPlanQ8 best{1, 1, 0, 1e30};
   for (int t = 0; t < int(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
     const TileCost& k = kTiles[t];
     const double tiles = std::ceil(double(M) / k.bm) * std::ceil(rows / k.bn);
@@ -488,10 +463,7 @@ GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated) {
       const double hbm = rows * D / kHbmBytesPerUs;
       us = kLaunchUs + std::cbrt(us * us * us + hbm * hbm * hbm);
       if (s > 1) us += kSplitUs + 2 * part / kPartBytesPerUs;
-      if (us < best_us) {
-        best_us = us;
-        best = GemmPlanQ8{t, s, s > 1 ? align256(size_t(part)) : 0};
-      }
+      if (us < best.us) best = GemmPlanQ8{t, s, s > 1 ? align256(size_t(part)) : 0, us};
     }
   }
   return best;

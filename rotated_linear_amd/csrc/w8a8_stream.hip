@@ -1,4 +1,4 @@
-// The 8-bit products for a few rows of x: the weights are streamed once, straight into registers.
+// The 8-bit products for a row or two of x: the weights are streamed once, straight into registers.
 #include "q8_device.h"
 
 namespace paro {
@@ -107,8 +107,8 @@ hipError_t launch(const W8A8Call& c, hipStream_t st) {
 }
 
 // Eight waves where there is at most one workgroup per CU, else four. Measured on MI355X, cold
-// weights: M = 1, 8960 -> 1536 (192 workgroups) 5.0 us with eight, 5.8 with four; M = 8, 4096 -> 4096
-// (256) 6.0 and 6.7; M = 1, gated 4096 -> 14336 (3584) 20.3 and 18.9 us (6.2 TB/s).
+// weights: M = 1, 8960 -> 1536 (192 workgroups) 5.0 us with eight, 5.8 with four; gated 4096 -> 14336
+// (3584) 20.3 and 18.9 us (6.2 TB/s).
 template <int P, bool GATED>
 hipError_t launch_waves(const W8A8Call& c, hipStream_t st) {
   constexpr int cols = 16 / P * (GATED ? 1 : 2);
@@ -117,23 +117,17 @@ hipError_t launch_waves(const W8A8Call& c, hipStream_t st) {
 
 template <bool GATED>
 hipError_t launch_rows(const W8A8Call& c, hipStream_t st) {
-  if (c.M <= 4 && c.D % 256 == 0) return launch_waves<4, GATED>(c, st);
-  if (c.M <= 8) return launch_waves<2, GATED>(c, st);
-  return launch<1, GATED ? 2 : 1, 8, GATED>(c, st);
+  return c.D % 256 == 0 ? launch_waves<4, GATED>(c, st) : launch_waves<2, GATED>(c, st);
 }
 
 }  // namespace
 
-// The rows of x pass through every workgroup's L1, as many bytes as a tile of weights at M = 16: past
-// 32 MB of weights the tiled kernel, which shares x through LDS, is faster there. Measured, cold
-// weights, M = 16: 4096 -> 4096 7.4 us here, 9.5 tiled; 14336 -> 4096 20.7 and 16.4; gated 4096 ->
-// 14336 31.4 and 28.1. Up to 8 rows the stream always wins (M = 8, 4096 -> 4096: 6.0 and 9.5).
+// Measured against the kernel that brings x and w through LDS, cold weights: M = 1, 4096 -> 4096 5.2
+// us here, 5.2 there; 8960 -> 1536 5.0 and 6.2; gated 4096 -> 14336 19.0 and 21.4. From a few rows on
+// the other is ahead: M = 4, 14336 -> 4096 12.3 and 12.1; M = 8, 8960 -> 1536 9.1 and 7.0.
 // (A grid of more than 2^32 threads cannot be launched: layers of more than 2^24 columns go to the
 // tiled kernel, whose grid does not grow with them.)
-bool w8a8_stream_takes(int M, int D, int N, bool gated) {
-  if (N > 1 << 24) return false;
-  return M <= 8 || (M <= 16 && size_t(N) * (gated ? 2 : 1) * D <= size_t(32) << 20);
-}
+bool w8a8_stream_takes(int M, int N) { return M <= 2 && N <= 1 << 24; }
 
 hipError_t launch_w8a8_stream(const W8A8Call& c, hipStream_t st) {
   return c.gated ? launch_rows<true>(c, st) : launch_rows<false>(c, st);
