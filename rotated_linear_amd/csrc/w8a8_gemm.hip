@@ -57,6 +57,7 @@ struct Tile {
 struct Place {
   int m0, n0;  // first row and column of y
   int split, t0, steps;
+  int start;  // the walk over the steps begins here and wraps
 };
 
 // Tile number `tile` (of tiles_m * tiles_n * splits): splits innermost, then groups of 4 tile rows
@@ -74,6 +75,10 @@ __device__ inline Place place(const GemmArgs& a, int tile) {
   p.n0 = (in / gsz) * (GATED ? T::BN / 2 : T::BN);
   p.t0 = p.split * a.steps_per_split;
   p.steps = min(a.steps_per_split, a.c.D / T::BK - p.t0);
+  // With one row of tiles no two tiles share rows of w, and each starts its walk one step after its
+  // neighbour: rows a multiple of 2 KB apart lie in the same L2 channel (M = 40, gated 4096 -> 14336:
+  // 30.7 -> 26.4 us). Tiles that share rows of w keep together (starting them apart: up to 6 % slower).
+  p.start = a.tiles_m == 1 ? in / gsz % p.steps : 0;
   return p;
 }
 
@@ -243,8 +248,9 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
         at = q.steps - 1;
       }
     }
+    const int step = at + q.start < q.steps ? at + q.start : at + q.start - q.steps;
 #pragma unroll
-    for (int i = 0; i < T::LOADS; ++i) dma16(ldsw + buf * T::STAGE + i * 1024, voff[i], src[i] + size_t(at) * T::BK);
+    for (int i = 0; i < T::LOADS; ++i) dma16(ldsw + buf * T::STAGE + i * 1024, voff[i], src[i] + size_t(step) * T::BK);
     ++at;
   };
   // The scales of a tile (x rows, then w rows) into LDS: the waves take 64 each.
