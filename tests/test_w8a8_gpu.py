@@ -342,7 +342,9 @@ TILED = [(654, 384, 11023, False), (1606, 256, 15152, False), (138, 11904, 5769,
          (69, 128, 11270, False), (270, 128, 11200, False), (33, 4224, 1481, False), (702, 5504, 134, False), (33, 128, 9174, True),
          (130, 128, 8624, True), (33, 4224, 803, True), (1060, 4736, 33, True), (413, 128, 4667, False), (1160, 768, 3330, False),
          (1067, 7808, 265, False), (278, 15488, 544, False), (820, 128, 1219, True), (1185, 768, 1666, True), (1303, 11008, 65, True),
-         (129, 384, 10994, False), (1034, 3200, 17, False), (65, 384, 9115, True), (34, 2688, 713, True)]
+         (129, 384, 10994, False), (1034, 3200, 17, False), (65, 384, 9115, True), (34, 2688, 713, True),
+         # one row of tiles (each starts its walk over the channels elsewhere), whole and split
+         (64, 2048, 9000, False), (40, 1536, 7000, True), (64, 14336, 264, False), (50, 8960, 120, True)]
 
 
 @pytest.mark.parametrize("M,D,N,gated", TILED)
@@ -366,6 +368,33 @@ def test_tiled_kernel(M, D, N, gated):
         assert over(y.double().cpu().numpy() - ref, bound) <= 1, dt
 
 
+# 16 columns a workgroup: one to four fragments of rows, fewer steps than waves, few and many
+# workgroups, ragged rows and columns, and streamed rows with tails of every kind.
+COLUMN = [(3, 128, 15), (16, 384, 200), (9, 1152, 4100), (17, 128, 33), (32, 2048, 48), (24, 640, 4500), (33, 1152, 200), (64, 384, 4111),
+          (50, 2048, 900), (64, 128, 17), (48, 1536, 4099), (31, 896, 4112), (8, 4096, 4096), (1, 128, 4), (2, 384, 1030), (1, 640, 9000),
+          (2, 4352, 33), (1, 16128, 12)]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,D,N", COLUMN)
+def test_short_x_kernels(M, D, N, gated):
+    C.log(f"w8a8 short x M={M} D={D} N={N} gated={gated}")
+    xq, xs, wq, ws = operands(57, M, D, N * (2 if gated else 1), full=not gated)
+    if gated:
+        ws = ws * np.float32(20)
+        ref, g, u = Q.gated(xq, xs, wq, ws)
+    else:
+        ref = Q.linear(xq, xs, wq, ws)
+    fn = rl.paro_w8a8_gated_linear if gated else rl.paro_w8a8_linear
+    d = on_gpu(xq, xs, wq, ws)
+    for dt in ("bf16", "f32"):
+        y, ok = guarded((M, N), DT[dt])
+        fn(*d, out=y)
+        assert ok()
+        bound = gated_bound(ref, g, u, dt) if gated else linear_bound(ref, dt)
+        assert over(y.double().cpu().numpy() - ref, bound) <= 1, dt
+
+
 @pytest.mark.parametrize("D,N", [(256, 70), (1536, 256), (4096, 640), (8960, 136)])
 def test_rows_do_not_depend_on_the_other_rows(D, N):
     """A row alone (streamed weights), in a short batch and in a long one (every kernel and split):
@@ -377,7 +406,7 @@ def test_rows_do_not_depend_on_the_other_rows(D, N):
     for dt in (torch.float16, torch.float32):
         full = rl.paro_w8a8_linear(xq, xs, wq, ws, dt)
         full_g = rl.paro_w8a8_gated_linear(xq, xs, wq, ws, dt)
-        for m in (1, 3, 7, 12, 16, 17, 40, 64, 65, 130, 300):
+        for m in (1, 2, 3, 7, 12, 16, 17, 33, 40, 64, 65, 130, 300):
             assert torch.equal(rl.paro_w8a8_linear(xq[:m], xs[:m], wq, ws, dt), full[:m]), (m, dt)
             assert torch.equal(rl.paro_w8a8_gated_linear(xq[:m], xs[:m], wq, ws, dt), full_g[:m]), (m, dt)
     q, s, h = rl.paro_rmsnorm_q8(x, g, residual=x)
