@@ -175,6 +175,22 @@ def test_binding_refusals():
     raises(ValueError, "as many gate rows as up rows", rl.paro_w8a8_gated_linear, q, s, w[:9], ws[:9])
 
 
+def test_compiled_binding_declines_what_it_does_not_take():
+    """It returns None, having done nothing, for CPU tensors, other objects and wrong counts; the checks
+    above then speak. bind() takes nine addresses, none of them zero."""
+    from rotated_linear_amd import _binding as b
+
+    x, q, s = torch.zeros(2, 256, dtype=torch.float16), torch.zeros(2, 256, dtype=torch.int8), torch.zeros(2)
+    assert b.linear(False, q, s, q, s, None, None, None) is None and b.linear(False, q, s) is None
+    assert b.linear(False, None, 3, "w", s, torch.float16, None, None) is None
+    assert b.quantize(False, x, 0, None, None, None) is None and b.quantize(True, 1, 0, None, None, None) is None
+    assert b.dequantize(q, s, None, None) is None and b.dequantize() is None
+    assert b.rmsnorm(True, x, x[0], 1e-6, None, None, None, None) is None and b.rmsnorm(None) is None
+    for bad in ((), (1,) * 8, (1,) * 8 + (0,), (1,) * 8 + ("x",)):
+        with pytest.raises((TypeError, ValueError)):
+            b.bind(*bad)
+
+
 # ---- the oracle against hand-worked values ----
 
 def test_oracle_rounding():

@@ -466,6 +466,54 @@ def test_empty_calls():
     torch.cuda.synchronize()
 
 
+class Unusual(torch.Tensor):
+    pass
+
+
+def test_both_ways_of_the_binding_agree():
+    """Calls that fit go through the compiled binding; a tensor subclass goes the checked way to the
+    same library call, with and without given outputs."""
+    from rotated_linear_amd import _binding as b
+
+    M, D, N = 70, 1024, 200
+    x, _ = rows(95, M, D, "f16")
+    g = torch.ones(D, dtype=torch.float16, device="cuda")
+    L = W.custom_linear(96, 1, D, 16, 4)
+    rot = rl.paro_rotation_prepare(L.pairs, L.theta, L.scale)
+    wq, ws = rl.paro_pack_weights_q8(rows(97, N, D, "f16")[0])
+    q, s = rl.paro_quantize_q8(x, rot)
+    assert b.linear(False, q, s, wq, ws, None, None, None) is not None
+    assert b.quantize(False, x, 0, None, None, None) is not None
+    assert b.dequantize(q, s, torch.float32, None) is not None
+    assert b.rmsnorm(True, x, g, 1e-6, x, None, None, None) is not None
+    u = x.as_subclass(Unusual)
+    uq = q.as_subclass(Unusual)
+    assert b.quantize(False, u, 0, None, None, None) is None and b.linear(False, uq, s, wq, ws, None, None, None) is None
+    plain = torch.Tensor
+    for f, a, ua in ((rl.paro_quantize_q8, (x, rot), (u, rot)), (rl.paro_pack_weights_q8, (x, rot), (u, rot)),
+                     (rl.paro_rmsnorm_q8, (x, g, 1e-6, x), (u, g, 1e-6, u)), (rl.paro_rmsnorm, (x, g, 1e-6, x), (u, g, 1e-6, u)),
+                     (rl.paro_dequantize_q8, (q, s), (uq, s)),
+                     (rl.paro_w8a8_linear, (q, s, wq, ws), (uq, s, wq, ws)),
+                     (rl.paro_w8a8_gated_linear, (q, s, wq, ws), (uq, s, wq, ws))):
+        got, want = f(*ua), f(*a)
+        for t, v in zip(*((o if isinstance(o, tuple) else (o,)) for o in (got, want))):
+            assert torch.equal(t.as_subclass(plain), v), f
+    eq, es = torch.empty_like(q), torch.empty_like(s)
+    r = rl.paro_quantize_q8(x, rot, out=(eq, es))
+    assert r[0].data_ptr() == eq.data_ptr() and torch.equal(eq, q) and torch.equal(es, s)
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    assert rl.paro_w8a8_linear(q, s, wq, ws, out=y).data_ptr() == y.data_ptr()
+    with pytest.raises(rl.ParoError, match="EINVAL"):  # an odd address is refused by the library
+        rl.paro_dequantize_q8(q, torch.zeros(M + 1, device="cuda")[1:])
+    with pytest.raises(rl.ParoError, match="EWORKSPACE"):
+        big = torch.zeros(200, 8960, dtype=torch.int8, device="cuda")
+        rl.paro_w8a8_linear(big, torch.ones(200, device="cuda"), big, torch.ones(200, device="cuda"),
+                            ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(rl.ParoError, match="EINVAL"):  # h over x
+        rl.paro_rmsnorm_q8(x, g, 1e-6, residual=x.clone(), residual_out=x)
+    torch.cuda.synchronize()
+
+
 # ---- a decoder layer's MLP: norm, gate and up, quantiser behind the transform, down ----
 
 class Mlp:
