@@ -421,30 +421,31 @@ hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st)
   return a.part ? launch_reduce<GATED>(c, part, a.splits, st) : hipSuccess;
 }
 
-// The tilings: waves side by side in rows and columns, stages in LDS, and workgroups on a CU (by LDS).
-using T256 = Tile<256, 256, 2, 4, 128, 2>;      // 8 waves, one workgroup
-using T128 = Tile<128, 128, 2, 2, 128, 2>;      // two workgroups
-using T128Deep = Tile<128, 128, 2, 2, 128, 4>;  // one
-using T128x64 = Tile<128, 64, 2, 2, 128, 3>;    // one
-using T64x128 = Tile<64, 128, 1, 4, 128, 3>;    // one
-using T64 = Tile<64, 64, 1, 2, 128, 3>;         // two
-using T32 = Tile<32, 64, 1, 2, 128, 4>;         // two
+// The tilings: waves side by side in rows and columns, stages in LDS. Eight waves where the tile has
+// room for them: a CU's matrix cores then have a second wave each while the first waits (a 128 x 128
+// tile's step of 128 channels takes 0.43 us with eight, 0.59 with four; a 128 x 64 tile's 0.29 and
+// 0.44).
+using T256 = Tile<256, 256, 2, 4, 128, 2>;     // one workgroup on a CU (by LDS)
+using T256x128 = Tile<256, 128, 4, 2, 128, 2>; // one
+using T128 = Tile<128, 128, 2, 4, 128, 4>;     // one
+using T128x64 = Tile<128, 64, 4, 2, 128, 4>;   // one
+using T64 = Tile<64, 64, 4, 2, 128, 4>;        // two
+using T32 = Tile<32, 64, 2, 2, 128, 4>;        // two
 
-// Estimated time of a call in microseconds, from a fit to 616 measured combinations of shape, tiling
-// and split (MI355X, cold weights, M = 16..2048, D = 1536..14336, N = 1024..28672; 7 % rms off): a
-// launch; the units that a CU works through, per 128 channels of a unit (alone on a CU, and with
-// `cap` units on it) plus its end; the weights' way from HBM; these two joined as the cube root of
-// the sum of their cubes, since they overlap but not wholly; and for a split a launch and the partial
-// sums out and back. The choice by it was 1.4 % slower than the fastest measured one on average, 14 %
-// at worst.
+// Estimated time of a call in microseconds, from a fit to 2106 measured combinations of shape, tiling
+// and split (MI355X, cold weights, 58 shapes: M = 18..4096, D = 128..16256, N = 64..23000; 11 % rms
+// off): a launch; the units that a CU works through, per 128 channels of a unit (alone on a CU, and
+// with `cap` units on it or on every CU) plus its start and end; the weights' way from HBM; these two
+// joined as the cube root of the sum of their cubes, since they overlap but not wholly; and for a
+// split a launch and the partial sums out and back. The choice by it was 1.6 % slower than the fastest
+// measured one on average, 16 % at worst.
 struct TileCost {
   int bm, bn, cap;
   double alone, full, end;
 };
-constexpr TileCost kTiles[] = {{256, 256, 1, 1.29, 1.42, 3.15}, {128, 128, 2, 0.92, 1.31, 0.63}, {128, 128, 1, 0.59, 0.62, 1.69},
-                               {128, 64, 1, 0.434, 0.46, 0.68}, {64, 128, 1, 0.465, 0.487, 0.48}, {64, 64, 2, 0.374, 0.563, 0.79},
-                               {32, 64, 2, 0.253, 0.384, 0.54}};
-constexpr double kLaunchUs = 2.66, kSplitUs = 2.9, kHbmBytesPerUs = 5.13e6, kPartBytesPerUs = 4.67e6;
+constexpr TileCost kTiles[] = {{256, 256, 1, 1.24, 1.56, 9.0}, {256, 128, 1, 0.836, 0.967, 5.44}, {128, 128, 1, 0.425, 0.526, 3.24},
+                               {128, 64, 1, 0.286, 0.366, 1.85}, {64, 64, 2, 0.198, 0.482, 1.46}, {32, 64, 2, 0.157, 0.316, 1.07}};
+constexpr double kLaunchUs = 3.18, kSplitUs = 2.77, kHbmBytesPerUs = 4.57e6, kPartBytesPerUs = 5.37e6;
 
 // Partial sums of a split reduction at most (larger ones cost more than a split gives).
 constexpr double kMaxPartBytes = double(size_t(128) << 20);
@@ -465,7 +466,8 @@ GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated) {
       const double on_cu = std::ceil(tiles * ((steps + per - 1) / per) / kCUs);  // units of the busiest CU
       const double rounds = std::floor(on_cu / k.cap), rest = on_cu - rounds * k.cap;
       double us = rounds * (per * k.full + k.end);
-      if (rest > 0) us += per * (k.cap == 1 ? k.alone : k.alone + (k.full - k.alone) * (rest - 1) / (k.cap - 1)) + k.end;
+      if (k.cap == 1 && on_cu == 1) us = per * k.alone + k.end;
+      if (rest > 0) us += per * (k.alone + (k.full - k.alone) * (rest - 1) / (k.cap - 1)) + k.end;
       const double hbm = rows * D / kHbmBytesPerUs;
       us = kLaunchUs + std::cbrt(us * us * us + hbm * hbm * hbm);
       if (s > 1) us += kSplitUs + 2 * part / kPartBytesPerUs;
@@ -481,11 +483,10 @@ template <bool GATED>
 hipError_t launch_plan(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStream_t st) {
   switch (p.tile) {
     case 0: return launch_tile<T256, GATED>(c, part, p.splits, st);
-    case 1: return launch_tile<T128, GATED>(c, part, p.splits, st);
-    case 2: return launch_tile<T128Deep, GATED>(c, part, p.splits, st);
+    case 1: return launch_tile<T256x128, GATED>(c, part, p.splits, st);
+    case 2: return launch_tile<T128, GATED>(c, part, p.splits, st);
     case 3: return launch_tile<T128x64, GATED>(c, part, p.splits, st);
-    case 4: return launch_tile<T64x128, GATED>(c, part, p.splits, st);
-    case 5: return launch_tile<T64, GATED>(c, part, p.splits, st);
+    case 4: return launch_tile<T64, GATED>(c, part, p.splits, st);
     default: return launch_tile<T32, GATED>(c, part, p.splits, st);
   }
 }

@@ -344,7 +344,14 @@ TILED = [(654, 384, 11023, False), (1606, 256, 15152, False), (138, 11904, 5769,
          (1067, 7808, 265, False), (278, 15488, 544, False), (820, 128, 1219, True), (1185, 768, 1666, True), (1303, 11008, 65, True),
          (129, 384, 10994, False), (1034, 3200, 17, False), (65, 384, 9115, True), (34, 2688, 713, True),
          # one row of tiles (each starts its walk over the channels elsewhere), whole and split
-         (64, 2048, 9000, False), (40, 1536, 7000, True), (64, 14336, 264, False), (50, 8960, 120, True)]
+         (64, 2048, 9000, False), (40, 1536, 7000, True), (64, 14336, 264, False), (50, 8960, 120, True),
+         (715, 128, 13689, False), (3335, 128, 7016, False), (329, 128, 14149, True), (1095, 128, 9883, True), (140, 6656, 8597, True),
+         (579, 128, 9795, False), (1417, 128, 10819, False), (135, 13184, 8885, False), (193, 128, 12305, True), (3196, 128, 2479, True),
+         (145, 11520, 4205, True), (199, 128, 12575, False), (520, 128, 12901, False), (4134, 16000, 69, False), (67, 128, 12863, True),
+         (322, 128, 9902, True), (4418, 15232, 34, True), (66, 256, 11509, False), (716, 512, 5400, False), (4138, 5120, 19, False),
+         (2991, 6272, 18, False), (66, 256, 5591, True), (2483, 512, 769, True), (1368, 9088, 34, True), (1380, 9728, 35, True),
+         (161, 128, 11014, False), (1370, 4864, 18, False), (66, 128, 11288, True), (325, 11648, 33, True), (35, 15872, 1600, True),
+         (8, 8320, 18, False), (1427, 4224, 16, False), (8, 5504, 17, True), (8, 15488, 1455, True)]
 
 
 @pytest.mark.parametrize("M,D,N,gated", TILED)
