@@ -31,7 +31,7 @@ struct GemmArgs {
   int tiles_m, tiles_n, splits, steps_per_split;
 };
 
-template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_>
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_, int PR_ = 32>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_;
   static constexpr int NW = WM * WN, NT = NW * 64;
@@ -44,7 +44,7 @@ struct Tile {
   static_assert(FN % 2 == 0 && (FM == 1 || FM % 2 == 0), "16 gate and 16 up rows in turn; x fragments in halves");
   // Results leave through LDS in pieces of PR rows, up to 64 bytes of a row at a time, rows 80 bytes
   // apart.
-  static constexpr int PR = FM == 1 ? 16 : 32;
+  static constexpr int PR = FM == 1 ? 16 : PR_;
   static constexpr int EP = 80;
   static constexpr int OUT = STAGE * S;           // LDS: the stages, each wave's results, the scales
   static constexpr int SCALES = OUT + NW * PR * EP;
@@ -428,23 +428,25 @@ hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st)
 using T256 = Tile<256, 256, 2, 4, 128, 2>;     // one workgroup on a CU (by LDS)
 using T256x128 = Tile<256, 128, 4, 2, 128, 2>; // one
 using T128 = Tile<128, 128, 2, 4, 128, 4>;     // one
+using T128Two = Tile<128, 128, 2, 4, 128, 2, 16>;  // two: for a little more than one tile per CU
 using T128x64 = Tile<128, 64, 4, 2, 128, 4>;   // one
 using T64 = Tile<64, 64, 4, 2, 128, 4>;        // two
 using T32 = Tile<32, 64, 2, 2, 128, 4>;        // two
 
-// Estimated time of a call in microseconds, from a fit to 2106 measured combinations of shape, tiling
+// Estimated time of a call in microseconds, from a fit to 2457 measured combinations of shape, tiling
 // and split (MI355X, cold weights, 58 shapes: M = 18..4096, D = 128..16256, N = 64..23000; 11 % rms
 // off): a launch; the units that a CU works through, per 128 channels of a unit (alone on a CU, and
 // with `cap` units on it or on every CU) plus its start and end; the weights' way from HBM; these two
 // joined as the cube root of the sum of their cubes, since they overlap but not wholly; and for a
-// split a launch and the partial sums out and back. The choice by it was 1.6 % slower than the fastest
-// measured one on average, 16 % at worst.
+// split a launch and the partial sums out and back. The choice by it was 1.5 % slower than the fastest
+// measured one on average, 19 % at worst.
 struct TileCost {
   int bm, bn, cap;
   double alone, full, end;
 };
 constexpr TileCost kTiles[] = {{256, 256, 1, 1.24, 1.56, 9.0}, {256, 128, 1, 0.836, 0.967, 5.44}, {128, 128, 1, 0.425, 0.526, 3.24},
-                               {128, 64, 1, 0.286, 0.366, 1.85}, {64, 64, 2, 0.198, 0.482, 1.46}, {32, 64, 2, 0.157, 0.316, 1.07}};
+                               {128, 128, 2, 0.651, 1.045, 3.05}, {128, 64, 1, 0.286, 0.366, 1.85}, {64, 64, 2, 0.198, 0.482, 1.46},
+                               {32, 64, 2, 0.157, 0.316, 1.07}};
 constexpr double kLaunchUs = 3.18, kSplitUs = 2.77, kHbmBytesPerUs = 4.57e6, kPartBytesPerUs = 5.37e6;
 
 // Partial sums of a split reduction at most (larger ones cost more than a split gives).
@@ -485,8 +487,9 @@ hipError_t launch_plan(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStr
     case 0: return launch_tile<T256, GATED>(c, part, p.splits, st);
     case 1: return launch_tile<T256x128, GATED>(c, part, p.splits, st);
     case 2: return launch_tile<T128, GATED>(c, part, p.splits, st);
-    case 3: return launch_tile<T128x64, GATED>(c, part, p.splits, st);
-    case 4: return launch_tile<T64, GATED>(c, part, p.splits, st);
+    case 3: return launch_tile<T128Two, GATED>(c, part, p.splits, st);
+    case 4: return launch_tile<T128x64, GATED>(c, part, p.splits, st);
+    case 5: return launch_tile<T64, GATED>(c, part, p.splits, st);
     default: return launch_tile<T32, GATED>(c, part, p.splits, st);
   }
 }

@@ -351,6 +351,7 @@ TILED = [(654, 384, 11023, False), (1606, 256, 15152, False), (138, 11904, 5769,
          (322, 128, 9902, True), (4418, 15232, 34, True), (66, 256, 11509, False), (716, 512, 5400, False), (4138, 5120, 19, False),
          (2991, 6272, 18, False), (66, 256, 5591, True), (2483, 512, 769, True), (1368, 9088, 34, True), (1380, 9728, 35, True),
          (161, 128, 11014, False), (1370, 4864, 18, False), (66, 128, 11288, True), (325, 11648, 33, True), (35, 15872, 1600, True),
+         (263, 128, 13751, False), (584, 128, 13224, False), (129, 128, 11001, True), (324, 128, 10946, True),
          (8, 8320, 18, False), (1427, 4224, 16, False), (8, 5504, 17, True), (8, 15488, 1455, True)]
 
 
