@@ -18,7 +18,7 @@
  *   - Types: `dtype` is PARO_F16 or PARO_BF16 for rows that are read; outputs of the linears and
  *     of paro_dequantize_q8 may be PARO_F32 too. Codes are int8, scales float32.
  *   - Row quantiser (every call that writes q and scales): with a = the largest |v| of the row
- *     and c = max(a, 2^-100): scale = c / 127 and code = rint(v * (127 / c)), ties to even, so a
+ *     and c = max(a, 2^-100): scale = c / 127 and code = rint(v * 127 / c), ties to even, so a
  *     zero row has codes 0 and a positive scale. Arithmetic is float32 (float64 where stated)
  *     except for rounding of the result. A row with an infinity or a NaN has scale NaN and codes
  *     0, so everything computed from that row, and nothing else, is NaN.

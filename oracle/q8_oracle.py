@@ -43,8 +43,9 @@ def transform(x, pairs, theta, scale):
 
 
 def pack_weights(W, pairs=None, theta=None, scale=None):
-    """Codes and scales of the (folded) weight rows, every operation rounded on its own in float64:
-    the stages in order, times s, then code = rint(b * (127 / c)) and scale = float32(c / 127)."""
+    """Codes and scales of the (folded) weight rows: the stages in order, then times s, every operation
+    rounded on its own in float64; code = rint(b * 127 / c) of the exact quotient (in 64 digits, where a
+    value half way between two codes stays there) and scale = float32(c / 127)."""
     b = np.array(W, np.float64)
     if pairs is not None:
         for pk, tk in zip(pairs, theta):
@@ -56,7 +57,8 @@ def pack_weights(W, pairs=None, theta=None, scale=None):
             b[:, j] = c * bj - s * bi
         b = b * np.asarray(scale, np.float32).astype(np.float64)
     c = np.maximum(np.abs(b).max(axis=1), TOP_MIN)
-    q = np.rint(b * (127.0 / c)[:, None])
+    assert np.finfo(np.longdouble).nmant >= 63
+    q = np.rint(b.astype(np.longdouble) * 127 / c.astype(np.longdouble)[:, None])
     return q.astype(np.int8), (c / 127.0).astype(np.float32)
 
 

@@ -45,29 +45,43 @@ __device__ inline uint32_t abs_order(float v) { return __builtin_bit_cast(uint32
 constexpr uint32_t kAbsInf = 0x7F800000u;
 
 // The row quantiser's scale and code step from the row's largest magnitude (as abs_order): codes
-// are rint(v * step). A row with an infinity or a NaN: scale NaN and `bad` (codes 0).
+// are rint(v * 127 / c), step + low = 127 / c to twice float32's precision. A row with an infinity or
+// a NaN: scale NaN and `bad` (codes 0).
 struct RowQuant {
-  float scale, step;
+  float scale, step, low;
   bool bad;
 };
-__device__ inline RowQuant row_quant(uint32_t top) {
+// code_top: the largest magnitude of the values that the codes are made from, where these are not the
+// row itself but the row over a factor.
+__device__ inline RowQuant row_quant(uint32_t top, uint32_t code_top) {
   RowQuant r;
   r.bad = top >= kAbsInf;
-  const float c = fmaxf(__builtin_bit_cast(float, top), kQ8MinTop);
-  r.scale = r.bad ? __builtin_nanf("") : c / kQ8Max;
+  r.scale = r.bad ? __builtin_nanf("") : fmaxf(__builtin_bit_cast(float, top), kQ8MinTop) / kQ8Max;
+  const float c = fmaxf(__builtin_bit_cast(float, code_top), kQ8MinTop);
   r.step = kQ8Max / c;
+  r.low = __builtin_fmaf(-r.step, c, kQ8Max) / c;  // the division's remainder is exact
   return r;
 }
-// rint(v * step) in the low byte: adding 1.5 * 2^23 in the fused multiply-add leaves the nearest
-// whole number (ties to even, the product not rounded before) in the sum's low mantissa bits.
-// |v * step| <= 127 (1 + 2^-23), which never rounds past 127.
+__device__ inline RowQuant row_quant(uint32_t top) { return row_quant(top, top); }
+// The nearest whole number (ties to even) of |p| <= 127 in the low byte: adding 1.5 * 2^23 leaves it in
+// the sum's low mantissa bits.
+__device__ inline uint32_t whole_bits(float p) { return __builtin_bit_cast(uint32_t, p + 12582912.0f); }
+// The code of v, its product rounded once from nearly exact. A 16-bit row whose maximum is 127 times a
+// small number holds many values exactly half way between two codes: this way they stay half way and
+// go to the even code, where the product with a rounded step would go either way.
+__device__ inline uint32_t code_bits(float v, const RowQuant& q) {
+  return whole_bits(__builtin_fmaf(v, q.step, v * q.low));
+}
+// The same with the step rounded to float32, for values that are rounded themselves.
 __device__ inline uint32_t code_bits(float v, float step) {
-  return __builtin_bit_cast(uint32_t, __builtin_fmaf(v, step, 12582912.0f));
+  float p = v * step;
+  asm("" : "+v"(p));  // rounded on its own, not fused with the addition
+  return whole_bits(p);
 }
 // Four codes as one word.
-__device__ inline uint32_t codes4(float a, float b, float c, float d, float step) {
-  const uint32_t ab = __builtin_amdgcn_perm(code_bits(b, step), code_bits(a, step), 0x0c0c0400u);
-  const uint32_t cd = __builtin_amdgcn_perm(code_bits(d, step), code_bits(c, step), 0x04000c0cu);
+__device__ inline uint32_t codes4(float a, float b, float c, float d, const RowQuant& q) {
+  const uint32_t ab = __builtin_amdgcn_perm(code_bits(b, q), code_bits(a, q), 0x0c0c0400u);
+  const uint32_t cd = __builtin_amdgcn_perm(code_bits(d, q), code_bits(c, q), 0x04000c0cu);
   return ab | cd;
 }
 

@@ -56,10 +56,11 @@ __global__ __launch_bounds__(1024) void pack_q8_kernel(int N, int D, int K, cons
     top = stop;
     const bool bad = top >= 0x7FF0000000000000ull;
     const double c0 = fmax(__builtin_bit_cast(double, top), double(kQ8MinTop));
-    const double step = 127.0 / c0;
+    // 127 / c0 to twice float64's precision, so that a weight half way between two codes stays there
+    const double step = 127.0 / c0, low = __builtin_fma(-step, c0, 127.0) / c0;
     for (int p = tid; p < P; p += nt) {
-      const uint32_t lo = uint32_t(int(__builtin_rint(brow[2 * p] * step))) & 0xFFu;
-      const uint32_t hi = uint32_t(int(__builtin_rint(brow[2 * p + 1] * step))) & 0xFFu;
+      const uint32_t lo = uint32_t(int(__builtin_rint(__builtin_fma(brow[2 * p], step, brow[2 * p] * low)))) & 0xFFu;
+      const uint32_t hi = uint32_t(int(__builtin_rint(__builtin_fma(brow[2 * p + 1], step, brow[2 * p + 1] * low)))) & 0xFFu;
       reinterpret_cast<uint16_t*>(q + n * D)[p] = bad ? uint16_t(0) : uint16_t(lo | (hi << 8));
     }
     if (tid == 0) scales[n] = bad ? __builtin_nanf("") : float(c0 / 127.0);

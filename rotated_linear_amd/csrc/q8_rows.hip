@@ -38,7 +38,8 @@ __device__ inline void wave_reduce(uint32_t& top, double& sum, bool with_sum) {
 //
 // With t = float32(h * gamma) and inv = float32(1 / sqrt(mean(h^2) + eps)), n = t * inv. Rounding is
 // monotonic, so the row's largest |n| is the largest |t| times inv: one reduction (the sum of squares
-// in float64 and the largest |t|) gives both the norm and the scale.
+// in float64 and the largest |t|) gives both the norm and the scale. The codes are those of t over its
+// own maximum, the same numbers without the rounding of the product with inv.
 template <int DT, bool NORM, bool Q8, int VPT>
 __global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
   __shared__ uint32_t stop[2][16];
@@ -126,9 +127,15 @@ __global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
       }
       if constexpr (NORM) {
         inv = float(1.0 / __builtin_sqrt(sum / a.D + double(a.eps)));
-        top = abs_order(__builtin_bit_cast(float, top) * inv);
+        const uint32_t ntop = abs_order(__builtin_bit_cast(float, top) * inv);
+        constexpr uint32_t kMinBits = __builtin_bit_cast(uint32_t, kQ8MinTop);
+        // (a row under the smallest scale, or t under it, takes its codes from n itself)
+        const bool from_t = Q8 && ntop >= kMinBits && top >= kMinBits;
+        rq = row_quant(ntop, from_t ? top : ntop);
+        if (from_t) inv = 1.0f;
+      } else {
+        rq = row_quant(top);
       }
-      rq = row_quant(top);
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -139,8 +146,8 @@ __global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
       }
       if (c < chunks) {
         if constexpr (Q8) {
-          uint2 q = make_uint2(codes4(t[i][0], t[i][1], t[i][2], t[i][3], rq.step),
-                               codes4(t[i][4], t[i][5], t[i][6], t[i][7], rq.step));
+          uint2 q = make_uint2(codes4(t[i][0], t[i][1], t[i][2], t[i][3], rq),
+                               codes4(t[i][4], t[i][5], t[i][6], t[i][7], rq));
           if (rq.bad) q = make_uint2(0, 0);
           reinterpret_cast<uint2*>(a.q)[row * chunks + c] = q;
         } else {

@@ -171,6 +171,30 @@ def test_quantize_odd_rows():
     assert bool(back[1:4].isnan().all()) and bool(back[[0, 4, 5, 6, 7]].isfinite().all())
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+def test_values_half_way_between_codes_go_to_the_even_one(dt):
+    """Rows whose maximum is 127 m 2^e hold values m (2 k + 1) 2^(e-1), exactly half way between two
+    codes, also where 127 / maximum has no exact float32: k rounds to even there. The same through the
+    norm with a gamma of one number."""
+    ms = [1, 3, 5, 7, 9, 11, 13, 15] if dt == "f16" else [1]  # 127 m in the type's digits
+    D = 256
+    k = np.arange(D) - 128
+    x = np.stack([np.where(np.abs(k) == 128, 127.0, np.clip(k + 0.5, -127, 127)) * m * 2.0 ** e for m in ms for e in (-9, 0, 4)])
+    ok = Q.round_to(x, dt) == x  # the halves that the type holds
+    x = np.where(ok, x, 0.0)
+    x[:, 0] = np.abs(x).max(axis=1)
+    want = np.rint(Q.quantize_exact(x)[0])
+    t = torch.from_numpy(x).to(DT[dt]).cuda()
+    assert np.array_equal(t.double().cpu().numpy(), x)
+    assert (np.abs(Q.quantize_exact(x)[0] % 1 - 0.5) < 1e-9).sum() > 20 * len(ms)
+    q, _ = rl.paro_quantize_q8(t)
+    assert np.array_equal(q.cpu().numpy(), want)
+    q, _ = rl.paro_pack_weights_q8(t)
+    assert np.array_equal(q.cpu().numpy(), want) and np.array_equal(Q.pack_weights(x)[0], want)
+    q, _, _ = rl.paro_rmsnorm_q8(t, torch.full((D,), 0.75, dtype=DT[dt], device="cuda"), 1e-6)
+    assert np.array_equal(q.cpu().numpy(), want)
+
+
 ROT = [(1, 128, 1, "f16"), (1, 1536, 8, "f16"), (16, 1536, 8, "bf16"), (3, 256, 2, "f16"), (65, 4096, 8, "f16"), (257, 1152, 8, "bf16"),
        (520, 2048, 8, "f16"), (2, 14336, 8, "f16"), (300, 8960, 8, "f16"), (5, 16384, 8, "bf16"), (1100, 512, 12, "f16"),
        (9, 640, 0, "f16"), (2, 4096, 64, "f16"), (513, 9216, 2, "f16"), (600, 12288, 2, "bf16"), (260, 16384, 1, "f16"),
