@@ -75,9 +75,10 @@ paro_status paro_dequantize_q8(int M, int D, const int8_t* q, const float* scale
 /*
  * paro_pack_weights_q8 -- build-time weights in 8 bits: the row quantiser in float64 on each row of
  * W (r == NULL), or on the row with the transform folded in (the K stages of r, then times s, as
- * paro_pack_weights folds it), so that transform(x) . W'^T = x . W^T. Every product and sum is
- * float64 with no fused multiply-add; scale is rounded once to float32. W dtype [N][D]; qweight
- * int8 [N][D] row-major (row n is weight row n), scales float32 [N].
+ * paro_pack_weights folds it), so that transform(x) . W'^T = x . W^T. Every product and sum of
+ * the fold is float64 with no fused multiply-add, v * 127 / c is held to twice that precision, and scale
+ * is rounded once to float32. W dtype [N][D]; qweight int8 [N][D] row-major (row n is weight row n),
+ * scales float32 [N].
  */
 paro_status paro_pack_weights_q8(const paro_rotation* r, int N, int D, int dtype, const void* W, int8_t* qweight,
                                  float* scales, void* stream);

@@ -2,8 +2,11 @@
 // in float64 by its largest magnitude.
 //
 // One workgroup per weight row, the row in LDS as float64. Bound by LDS: every stage gathers and
-// rewrites the row. Compiled with -ffp-contract=off: each product and each sum is rounded on its own,
-// so the codes are those of the stated definition.
+// rewrites the row. Measured, K = 8: 4096 x 4096 86 us, 1024 x 14336 92 us; 256 x 1536 (a pair per
+// thread and stage) 9.9 us, 11.6 with four. Loading the next stage's records ahead did not pay: it takes
+// registers, and with them the waves that hide LDS's latency. Compiled with -ffp-contract=off: each product
+// and each sum of the fold is rounded on its own, so the codes are those of the stated definition (the
+// quantiser asks for its one fused product by name).
 #include <algorithm>
 
 #include "q8_device.h"

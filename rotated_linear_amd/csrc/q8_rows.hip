@@ -1,6 +1,8 @@
 // Row kernels of the 8-bit path: residual addition + RMS norm (8-bit or 16-bit output), the row
 // quantiser, and reading 8-bit rows back. All are bound by HBM: one pass over the row, which stays
-// in registers between its statistics and its output.
+// in registers between its statistics and its output. Measured (cold rows): rmsnorm with residual
+// 4096 x 4096 25.8 us (7 bytes a channel, 4.6 TB/s; a copy of 1 GiB runs at 4.7), quantiser 12.8 us
+// (3.9 TB/s), read-back 11.9 us (4.2 TB/s); a single row of 4096 2.7 to 3.1 us, a launch.
 #include <algorithm>
 
 #include "q8_device.h"
@@ -185,7 +187,8 @@ __global__ __launch_bounds__(256) void dequantize_kernel(size_t total, uint32_t 
 template <int DT, bool NORM, bool Q8>
 hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
   const int chunks = a.D / 8;
-  // few rows: as many threads as chunks (latency); many rows: two chunks a thread
+  // Few rows: as many threads as chunks (latency). Many rows: two chunks a thread, whose next row is on
+  // its way.
   const int vpt = chunks > 1024 || (a.M >= 512 && chunks > 64) ? 2 : 1;
   const int nt = std::max(64, ((chunks + vpt - 1) / vpt + 63) / 64 * 64);
   const unsigned grid = unsigned(std::min(a.M, kCUs * (2048 / nt)));
