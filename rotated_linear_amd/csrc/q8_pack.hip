@@ -1,12 +1,15 @@
 // Build-time weights in 8 bits: each row of W, with the transform folded in or as it is, quantised
 // in float64 by its largest magnitude.
 //
-// One workgroup per weight row, the row in LDS as float64. Bound by LDS: every stage gathers and
-// rewrites the row. Measured, K = 8: 4096 x 4096 86 us, 1024 x 14336 92 us; 256 x 1536 (a pair per
-// thread and stage) 9.9 us, 11.6 with four. Loading the next stage's records ahead did not pay: it takes
-// registers, and with them the waves that hide LDS's latency. Compiled with -ffp-contract=off: each product
-// and each sum of the fold is rounded on its own, so the codes are those of the stated definition (the
-// quantiser asks for its one fused product by name).
+// One workgroup per weight row, the row in LDS as float64. Bound by LDS and the float64 units together:
+// every stage gathers and rewrites the row (at D = 4096 about 27 us a 4096 rows at LDS's full rate, and as
+// much again for some 16 instructions a pair). Measured, K = 8, cold W: 4096 x 4096 81 us, 1024 x 14336 90,
+// 256 x 1536 7.9. Two or four rows a workgroup, which read a record once for all, were no faster (77 us
+// where this takes 70): the records come from L2 in time, and wider LDS accesses move no more bytes a
+// cycle. Loading the next stage's records ahead did not pay either: it takes registers, and with them the
+// waves that hide LDS's latency. Compiled with -ffp-contract=off: each product and each sum of the fold is
+// rounded on its own, so the codes are those of the stated definition (the quantiser asks for its fused
+// products by name).
 #include <algorithm>
 
 #include "q8_device.h"
@@ -14,7 +17,8 @@
 namespace paro {
 namespace {
 
-template <int DT>
+// A thread takes U pairs of a stage at once (a stage's pairs are disjoint).
+template <int DT, int U>
 __global__ __launch_bounds__(1024) void pack_q8_kernel(int N, int D, int K, const uint16_t* W, const PairRec* recs,
                                                        const float* s, int8_t* q, float* scales) {
   extern __shared__ double brow[];  // [D]
@@ -31,64 +35,81 @@ __global__ __launch_bounds__(1024) void pack_q8_kernel(int N, int D, int K, cons
     }
     __syncthreads();
     for (int k = 0; k < K; ++k) {
-      for (int p = tid; p < P; p += nt) {
-        const PairRec r = recs[size_t(k) * P + p];
-        const int i = int((r.ij & 0xFFFFu) >> 2), j = int(r.ij >> 18);  // the fields are 4 i and 4 j
-        const double c = r.c, sn = r.s;
-        const double bi = brow[i], bj = brow[j];
-        brow[i] = c * bi + sn * bj;
-        brow[j] = c * bj - sn * bi;
+      const PairRec* const stage = recs + size_t(k) * P;
+      for (int p = tid; p < P; p += U * nt) {
+        PairRec rec[U];
+        double bi[U], bj[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) rec[u] = stage[min(p + u * nt, P - 1)];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          bi[u] = brow[(rec[u].ij & 0xFFFFu) >> 2];  // the fields are 4 i and 4 j
+          bj[u] = brow[rec[u].ij >> 18];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (u && p + u * nt >= P) break;
+          const double c = rec[u].c, sn = rec[u].s;
+          brow[(rec[u].ij & 0xFFFFu) >> 2] = c * bi[u] + sn * bj[u];
+          brow[rec[u].ij >> 18] = c * bj[u] - sn * bi[u];
+        }
       }
       __syncthreads();
     }
-    unsigned long long top = 0;  // |v| as an ordered integer (an infinity, then a NaN, on top)
-    for (int p = tid; p < P; p += nt) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        double b = brow[2 * p + e];
-        if (s) {
-          b = b * static_cast<double>(s[2 * p + e]);
-          brow[2 * p + e] = b;
-        }
-        top = max(top, __builtin_bit_cast(unsigned long long, b) & 0x7FFFFFFFFFFFFFFFull);
-      }
+    double top = 0, nan = 0;  // the largest |v| that is a number; NaN where any v is an infinity or a NaN
+    for (int c = tid; c < D; c += nt) {
+      double b = brow[c];
+      if (s) brow[c] = b = b * static_cast<double>(s[c]);
+      top = fmax(top, fabs(b));
+      nan = __builtin_fma(b, 0.0, nan);
     }
-    for (int off = 32; off >= 1; off >>= 1) top = max(top, __shfl_xor(top, off));
-    if ((tid & 63) == 0) atomicMax(&stop, top);
+    if (nan != nan) top = __builtin_inf();
+    unsigned long long bits = __builtin_bit_cast(unsigned long long, top);
+    for (int off = 32; off >= 1; off >>= 1) bits = max(bits, __shfl_xor(bits, off));
+    if ((tid & 63) == 0) atomicMax(&stop, bits);
     __syncthreads();
-    top = stop;
-    const bool bad = top >= 0x7FF0000000000000ull;
-    const double c0 = fmax(__builtin_bit_cast(double, top), double(kQ8MinTop));
+    bits = stop;
+    const bool bad = bits >= 0x7FF0000000000000ull;
+    const double c0 = fmax(__builtin_bit_cast(double, bits), double(kQ8MinTop));
     // 127 / c0 to twice float64's precision, so that a weight half way between two codes stays there
     const double step = 127.0 / c0, low = __builtin_fma(-step, c0, 127.0) / c0;
+    // 1.5 * 2^52 + v: v rounded to an integer, ties to even, in the low bits
+    auto code = [&](double b) {
+      const double v = __builtin_fma(b, step, b * low) + 0x1.8p52;
+      return uint32_t(__builtin_bit_cast(unsigned long long, v)) & 0xFFu;
+    };
     for (int p = tid; p < P; p += nt) {
-      const uint32_t lo = uint32_t(int(__builtin_rint(__builtin_fma(brow[2 * p], step, brow[2 * p] * low)))) & 0xFFu;
-      const uint32_t hi = uint32_t(int(__builtin_rint(__builtin_fma(brow[2 * p + 1], step, brow[2 * p + 1] * low)))) & 0xFFu;
-      reinterpret_cast<uint16_t*>(q + n * D)[p] = bad ? uint16_t(0) : uint16_t(lo | (hi << 8));
+      const uint32_t v = code(brow[2 * p]) | code(brow[2 * p + 1]) << 8;
+      reinterpret_cast<uint16_t*>(q + n * D)[p] = bad ? uint16_t(0) : uint16_t(v);
     }
     if (tid == 0) scales[n] = bad ? __builtin_nanf("") : float(c0 / 127.0);
     __syncthreads();  // the row and its maximum are done with
   }
 }
 
+template <int DT, int U>
+hipError_t launch(const DevRot& R, int N, int nt, const void* W, int8_t* q, float* scales, hipStream_t st) {
+  const auto kernel = &pack_q8_kernel<DT, U>;
+  const size_t lds = size_t(R.D) * sizeof(double);
+  if (lds + 64 > 64 * 1024)
+    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(lds)))
+      return e;
+  hipLaunchKernelGGL(kernel, dim3(unsigned(std::min(N, 1 << 20))), dim3(nt), lds, st, N, R.D, R.K,
+                     static_cast<const uint16_t*>(W), R.rec, R.s, q, scales);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_pack_q8(const DevRot& R, int N, int dtype, const void* W, int8_t* q, float* scales, hipStream_t st) {
-  const size_t lds = size_t(R.D) * sizeof(double);
-  const void* fn = dtype == PARO_F16 ? reinterpret_cast<const void*>(&pack_q8_kernel<PARO_F16>)
-                                     : reinterpret_cast<const void*>(&pack_q8_kernel<PARO_BF16>);
-  if (lds + 64 > 64 * 1024)
-    if (hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, int(lds))) return e;
-  const int share = N <= 256 ? 1 : 4;  // pairs of a thread per stage
-  const int nt = std::min(1024, (R.D / 2 / share + 63) / 64 * 64);
-  const dim3 grid(unsigned(std::min(N, 1 << 20)));
+  // Few rows: a pair per thread and stage (16 x 4096: 10.4 us; with four 11.6). Many: four pairs a thread,
+  // taken at once (4096 x 4096 with W in the Infinity Cache 70 us; one after the other 75).
+  const int P = R.D / 2;
+  const int nt = std::min(1024, (P / (N <= 256 ? 1 : 4) + 63) / 64 * 64);
+  const bool four = P > 3 * nt;
   if (dtype == PARO_F16)
-    hipLaunchKernelGGL((pack_q8_kernel<PARO_F16>), grid, dim3(nt), lds, st, N, R.D, R.K, static_cast<const uint16_t*>(W), R.rec,
-                       R.s, q, scales);
-  else
-    hipLaunchKernelGGL((pack_q8_kernel<PARO_BF16>), grid, dim3(nt), lds, st, N, R.D, R.K, static_cast<const uint16_t*>(W), R.rec,
-                       R.s, q, scales);
-  return hipGetLastError();
+    return four ? launch<PARO_F16, 4>(R, N, nt, W, q, scales, st) : launch<PARO_F16, 1>(R, N, nt, W, q, scales, st);
+  return four ? launch<PARO_BF16, 4>(R, N, nt, W, q, scales, st) : launch<PARO_BF16, 1>(R, N, nt, W, q, scales, st);
 }
 
 }  // namespace paro
