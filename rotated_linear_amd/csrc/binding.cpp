@@ -1,5 +1,6 @@
 // The 8-bit path's Python calls without ctypes: checks, outputs and the C call in one step. A decode
-// step's kernels take 3 to 6 us each; through ctypes a call costs 7 to 10 us of host time.
+// step's kernels take 3 to 6 us each; through ctypes a call costs 7 to 10 us of host time, here 3.7 to 4.9
+// (2.5 of it the runtime's launch).
 //
 // Every function here returns None, having done nothing, when an argument is not what the call takes
 // (another type, shape, device, stride or a tensor subclass), when another GPU is current, or when the
@@ -7,6 +8,7 @@
 // entry points (include/paro_w8a8.h) are handed over as addresses by bind().
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <ATen/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -58,7 +60,13 @@ bool starts(const Tensor* t, int* device, int* rows, int* cols) {
   return c10::hip::current_device() == *device;
 }
 void* stream(int device) { return c10::hip::getCurrentHIPStream(c10::DeviceIndex(device)).stream(); }
-Tensor make(const Tensor& like, at::IntArrayRef sizes, ScalarType type) { return at::empty(sizes, like.options().dtype(type)); }
+// A new tensor on the current GPU, from the allocator that `like` came from: torch's empty without its
+// dispatcher, 0.3 us instead of 0.7. (Memory that torch has not allocated names no allocator.)
+Tensor make(const Tensor& like, at::IntArrayRef sizes, ScalarType type) {
+  if (c10::Allocator* const a = like.storage().allocator())
+    return at::detail::empty_generic(sizes, a, c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
+  return at::empty(sizes, like.options().dtype(type));
+}
 
 // An output argument: None (then `*t` becomes a new tensor) or a tensor that fits.
 bool output(PyObject* o, const Tensor& like, int device, ScalarType type, at::IntArrayRef sizes, Tensor* t) {
@@ -126,6 +134,7 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int device, M, D;
   if (!starts(x, &device, &M, &D) || dtype_code(x->scalar_type()) < 0 || x->scalar_type() == ScalarType::Float) Py_RETURN_NONE;
   const auto* rot = static_cast<const paro_rotation*>(PyLong_AsVoidPtr(a[2]));
+  if (!rot && PyErr_Occurred()) return nullptr;
   if (rot) {
     const Tensor* desc = tensor(a[3]);
     if (!desc || !desc->is_cuda() || desc->get_device() != device || rot->dev != desc->const_data_ptr()) Py_RETURN_NONE;

@@ -652,3 +652,27 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for y1, y2 in got:
         assert torch.equal(y1, want[0]) and torch.equal(y2, want[1])
+
+
+def test_outputs_are_ordinary_tensors():
+    """Outputs the calls make: torch's own kind, memory that torch counts and takes back, also in
+    inference mode and for inputs whose memory torch has not allocated."""
+    x = torch.randn(3, 256, device="cuda").half()
+    like = torch.empty(3, 256, dtype=torch.int8, device="cuda")
+    q, s = rl.paro_quantize_q8(x)
+    assert q.device == like.device and q.stride() == like.stride() and not q.requires_grad
+    assert torch._C._dispatch_keys(q) == torch._C._dispatch_keys(like)
+    other = torch.from_dlpack(x)
+    q2, s2 = rl.paro_quantize_q8(other)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    kept = [rl.paro_quantize_q8(x) for _ in range(4)]
+    assert torch.cuda.memory_allocated() == before + 4 * (1024 + 512)
+    del kept
+    assert torch.cuda.memory_allocated() == before
+    with torch.inference_mode():
+        qi, _ = rl.paro_quantize_q8(x)
+        y = rl.paro_w8a8_linear(qi, s, like.zero_(), torch.ones(3, device="cuda"))
+        assert qi.is_inference() and y.is_inference() and torch.equal(y, torch.zeros_like(y))
+    assert torch.equal((q + 1) - 1, q)
