@@ -7,8 +7,8 @@
 // walks blocks of R rows with the next block's rows on their way meanwhile. After the last stage the
 // rows are read twice: once for each row's largest magnitude, once for its codes. The second read
 // costs LDS the half of one stage and saves the registers that would hold the row in between.
-// Measured, K = 8: 4096 x 4096 41.9 us (the 16-bit transform alone 39.6), 2048 x 8960 52.9 (48.7),
-// 64 x 4096 8.1 (8.4), 1024 x 14336 41.6 (43.0).
+// Measured, K = 8: 4096 x 4096 41.6 us (the 16-bit transform alone 38.9), 4096 x 1536 16.8 (19.8), 2048 x
+// 8960 50.2 (48.4), 64 x 4096 7.4 (7.9), 1000 x 14336 41.3 (42.8).
 #include <algorithm>
 
 #include "q8_device.h"
@@ -229,23 +229,34 @@ hipError_t launch_exact(const RotQ8Args& a, hipStream_t st) {
   return a.D / 2 == PPT * NT ? launch<DT, NT, R, PPT, PD, true>(a, st) : launch<DT, NT, R, PPT, PD, false>(a, st);
 }
 
-// Threads, pairs per thread and ring depth by row width, as in the 16-bit transform: past 6144
-// channels a block fills a CU's LDS, and 1024 threads give that CU its waves.
+// Threads, pairs per thread and stages of records in flight by row width: the smallest set that wastes few
+// slots, since a stage takes as long as its fullest thread (K = 8: 4096 x 1536 20.4 us with 512 x 2 slots for
+// its 768 pairs, 16.5 with 384 x 2; 2048 x 7168 41.5 with 512 x 7, 38.1 with 896 x 4). Two stages ahead, not
+// four (4096 x 2048 23.1 -> 19.9 us); one where two would take the registers of the widest blocks (1000 x
+// 14336 40.4 us, 55 with two). One and two rows have the registers for more threads with fewer pairs (256 x
+// 4096 7.3 -> 7.0 us); four rows have not (4096 x 4096 39.9 -> 43.0).
 template <int DT, int R>
 hipError_t launch_ppt(const RotQ8Args& a, hipStream_t st) {
   const int P = a.D / 2;
-  if (P <= 512) return launch_exact<DT, 512, R, 1, 4>(a, st);
-  if (P <= 1024) return launch_exact<DT, 512, R, 2, 4>(a, st);
-  if (P <= 1536) return launch_exact<DT, 512, R, 3, (R == 4 ? 2 : 4)>(a, st);
-  if (P <= 2048) return launch_exact<DT, 512, R, 4, (R == 1 ? 4 : 2)>(a, st);
-  if (P <= 3072) return launch_exact<DT, 512, R, 6, (R == 1 ? 2 : 1)>(a, st);
-  if constexpr (R == 4) {
+  constexpr bool few = R < 4;
+  if (P <= 256) return launch_exact<DT, 256, R, 1, 2>(a, st);
+  if (P <= 384) return launch_exact<DT, 384, R, 1, 2>(a, st);
+  if (P <= 512) return launch_exact<DT, few ? 512 : 256, R, few ? 1 : 2, 2>(a, st);
+  if (P <= 384 * 2) return launch_exact<DT, 384, R, 2, 2>(a, st);
+  if (P <= 512 * 2) return launch_exact<DT, 512, R, 2, 2>(a, st);
+  if (P <= 512 * 3) return launch_exact<DT, 512, R, 3, 2>(a, st);
+  if (P <= 1024 * 2) return launch_exact<DT, few ? 1024 : 512, R, few ? 2 : 4, 2>(a, st);
+  if (P <= 1024 * 3) return launch_exact<DT, 1024, R, 3, 2>(a, st);
+  if (P <= 896 * 4) return launch_exact<DT, 896, R, 4, 2>(a, st);
+  if (P <= 1024 * 4) return launch_exact<DT, 1024, R, 4, few ? 2 : 1>(a, st);
+  if (P <= 896 * 5) return launch_exact<DT, 896, R, 5, few ? 2 : 1>(a, st);
+  if constexpr (!few) {
     return launch_exact<DT, 1024, R, 5, 1>(a, st);  // 4-row blocks go to 9216 channels
   } else {
-    if (P <= 4608) return launch_exact<DT, 1024, R, 5, (R == 1 ? 2 : 1)>(a, st);
-    if (P <= 6144) return launch_exact<DT, 1024, R, 6, 1>(a, st);
-    if (P <= 7168) return launch_exact<DT, 1024, R, 7, 1>(a, st);
-    return launch_exact<DT, 512, R, 16, 1>(a, st);
+    if (P <= 1024 * 5) return launch_exact<DT, 1024, R, 5, 2>(a, st);
+    if (P <= 1024 * 6) return launch_exact<DT, 1024, R, 6, (R == 1 ? 2 : 1)>(a, st);
+    if (P <= 1024 * 7) return launch_exact<DT, 1024, R, 7, 1>(a, st);
+    return launch_exact<DT, 1024, R, 8, 1>(a, st);
   }
 }
 

@@ -233,6 +233,28 @@ def test_quantize_behind_the_transform(M, D, K, dt):
         assert torch.equal(q1[0], q[m]) and torch.equal(s1[0], sc[m]), m
 
 
+@pytest.mark.parametrize("D", [128, 256, 512, 640, 768, 896, 1024, 1280, 1536, 1664, 2048, 2304, 2944, 4096, 4224, 5120, 6144, 6272,
+                               7168, 7296, 8192, 8320, 8960, 9088, 9216, 9344, 10240, 10368, 12288, 12416, 14336, 14464, 16384])
+def test_quantize_behind_the_transform_at_every_width(D):
+    """One, two and four rows a workgroup, with pairs that divide over its threads and that do not."""
+    K, M = 3, 520
+    L = W.custom_linear(31, 5, D, 16, K)
+    rot = rl.paro_rotation_prepare(L.pairs, L.theta, L.scale)
+    x, x64 = rows(9, M, D, "f16")
+    (q, qok), (sc, scok) = guarded((M, D), torch.int8), guarded((M,), torch.float32)
+    rl.paro_quantize_q8(x, rot, out=(q, sc))
+    assert qok() and scok()
+    pick = C.sample_rows(M, 12, 1)
+    real, want = Q.quantize_exact(Q.transform(x64[pick], L.pairs, L.theta, L.scale))
+    dtop, dcode = rotated_bounds(x64[pick], L.scale, K, real, want)
+    assert over(sc.double().cpu().numpy()[pick] - want, dtop / 127 + want * 2 * U) <= 1
+    assert over(q.cpu().numpy()[pick].astype(np.float64) - real, 0.5 + 127 * 2 * U + dcode) <= 1
+    for a, b in ((0, 300), (M - 7, M)):  # the same rows in calls of two rows and of one row a workgroup
+        (qb, qbok), (sb, sbok) = guarded((b - a, D), torch.int8), guarded((b - a,), torch.float32)
+        rl.paro_quantize_q8(x[a:b].clone(), rot, out=(qb, sb))
+        assert qbok() and sbok() and torch.equal(qb, q[a:b]) and torch.equal(sb, sc[a:b])
+
+
 def test_quantize_behind_the_transform_odd_rows():
     D = 512
     L = W.custom_linear(33, 1, D, 16, 8)
