@@ -11,8 +11,9 @@
 // against 417; without the loads to LDS, in a copy for timing, 372). Hence the 16 x 16 x 64 product
 // rather than 32 x 32 x 32, which reads and writes an accumulator twice for the same channels (457 ->
 // 417 us). The library product of the same codes to plain 32-bit sums takes 461 us there; the gated
-// 4096 x 4096 -> 14336 takes 379 us, the library's product of that size 468. Smaller tilings wait for
-// their loads: the estimate below holds the measured time per step of each.
+// 4096 x 4096 -> 14336 takes 379 us, the library's product of that size 468. Smaller tilings
+// are bound by LDS and their loads about equally (1021 x 8960 -> 1537 in 128 x 64 tiles: loads alone
+// 22.8 us, reads and products alone 25.8, both 29.2): the estimate below holds each one's time per step.
 // The steps, at 8192^3: 256 x 256 tiles in four waves 575 us; in eight, reads between the products 507;
 // results through LDS and the scales read from there 481; stages of 128 channels, two of them, instead
 // of four of 64 464; loads that pass the ends of tiles 457; the 16 x 16 x 64 product 417.
@@ -443,7 +444,7 @@ hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st)
 // tile's step of 128 channels takes 0.43 us with eight, 0.59 with four; a 128 x 64 tile's 0.29 and
 // 0.44).
 using T256 = Tile<256, 256, 2, 4, 128, 2>;     // one workgroup on a CU (by LDS)
-using T256x128 = Tile<256, 128, 4, 2, 128, 2>; // one
+using T256x128 = Tile<256, 128, 4, 2, 128, 3, 16>; // one; a third stage: 1427 x 9216 -> 5095 99 -> 82 us
 using T128 = Tile<128, 128, 2, 4, 128, 4>;     // one
 using T128Two = Tile<128, 128, 2, 4, 128, 2, 16>;  // two: for a little more than one tile per CU
 using T128x64 = Tile<128, 64, 4, 2, 128, 4>;   // one
@@ -452,7 +453,8 @@ using T32 = Tile<32, 64, 2, 2, 128, 4>;        // two
 
 // Estimated time of a call in microseconds, from a fit to 2457 measured combinations of shape, tiling
 // and split (MI355X, cold weights, 58 shapes: M = 18..4096, D = 128..16256, N = 64..23000; 11 % rms
-// off): a launch; the units that a CU works through, per 128 channels of a unit (alone on a CU, and
+// off; the 256 x 128 tile had two stages then: with lower times for it, 35 shapes came out no faster as a
+// whole, since more of them went to it that other tilings do better): a launch; the units that a CU works through, per 128 channels of a unit (alone on a CU, and
 // with `cap` units on it or on every CU) plus its start and end; the weights' way from HBM; these two
 // joined as the cube root of the sum of their cubes, since they overlap but not wholly; and for a
 // split a launch and the partial sums out and back. The choice by it was 1.5 % slower than the fastest

@@ -398,7 +398,10 @@ TILED = [(654, 384, 11023, False), (1606, 256, 15152, False), (138, 11904, 5769,
          (2991, 6272, 18, False), (66, 256, 5591, True), (2483, 512, 769, True), (1368, 9088, 34, True), (1380, 9728, 35, True),
          (161, 128, 11014, False), (1370, 4864, 18, False), (66, 128, 11288, True), (325, 11648, 33, True), (35, 15872, 1600, True),
          (263, 128, 13751, False), (584, 128, 13224, False), (129, 128, 11001, True), (324, 128, 10946, True),
-         (8, 8320, 18, False), (1427, 4224, 16, False), (8, 5504, 17, True), (8, 15488, 1455, True)]
+         (8, 8320, 18, False), (1427, 4224, 16, False), (8, 5504, 17, True), (8, 15488, 1455, True),
+         # three stages of 256 x 128 tiles, whole, aligned and ragged
+         (268, 1536, 13633, False), (322, 1536, 11376, False), (136, 1536, 11013, True), (146, 1536, 11176, True),
+         (193, 2048, 8193, True), (579, 2048, 6584, False)]
 
 
 @pytest.mark.parametrize("M,D,N,gated", TILED)
