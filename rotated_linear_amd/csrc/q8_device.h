@@ -94,7 +94,8 @@ __device__ inline float scaled(int sum, float xs, float ws) {
   return v;
 }
 
-// silu(g) u = g u / (1 + exp(-g)); exp(-g) past float32 gives an infinity and the quotient -0.
+// silu(g) u = g u / (1 + exp(-g)); exp(-g) past float32 gives an infinity and the quotient -0, and the
+// reciprocal instruction may give 0 for one under 2^-126 already.
 __device__ inline float silu_mul(float g, float u) {
   float v = g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896f)) * u;
   asm("" : "+v"(v));
