@@ -72,12 +72,6 @@ __device__ inline uint32_t whole_bits(float p) { return __builtin_bit_cast(uint3
 __device__ inline uint32_t code_bits(float v, const RowQuant& q) {
   return whole_bits(__builtin_fmaf(v, q.step, v * q.low));
 }
-// The same with the step rounded to float32, for values that are rounded themselves.
-__device__ inline uint32_t code_bits(float v, float step) {
-  float p = v * step;
-  asm("" : "+v"(p));  // rounded on its own, not fused with the addition
-  return whole_bits(p);
-}
 // Four codes as one word.
 __device__ inline uint32_t codes4(float a, float b, float c, float d, const RowQuant& q) {
   const uint32_t ab = __builtin_amdgcn_perm(code_bits(b, q), code_bits(a, q), 0x0c0c0400u);

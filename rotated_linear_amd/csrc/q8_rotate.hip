@@ -37,6 +37,10 @@ __device__ inline int fresh_tid() {
   return t;
 }
 
+__device__ inline float from_lane(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
 template <int CTRL, int ROWS>
 __device__ inline uint32_t dpp_max(uint32_t v) {
   return max(v, uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false)));
@@ -154,13 +158,18 @@ __global__ __launch_bounds__(NT) void rotate_q8_kernel(const RotQ8Args a) {
       if ((to & 63) == 63) tops[(to >> 6) * R + r] = top[r];
     }
     __syncthreads();
+    // Lane l works out row l % R's scale and step (their divisions once, not R times), which then are
+    // the same in every lane: in scalar registers, of which there are plenty.
     RowQuant rq[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
+    {
       uint32_t t = 0;
 #pragma unroll
-      for (int w = 0; w < NT / 64; ++w) t = max(t, tops[w * R + r]);
-      rq[r] = row_quant(t);
+      for (int w = 0; w < NT / 64; ++w) t = max(t, tops[w * R + (to & (R - 1))]);
+      const RowQuant mine = row_quant(t);
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        rq[r] = RowQuant{from_lane(mine.scale, r), from_lane(mine.step, r), from_lane(mine.low, r),
+                         uint32_t(__builtin_amdgcn_readlane(int(t), r)) >= kAbsInf};
     }
     uint32_t ov[PPT][(R + 1) / 2];  // two codes a row, two rows a word
 #pragma unroll
@@ -175,7 +184,7 @@ __global__ __launch_bounds__(NT) void rotate_q8_kernel(const RotQ8Args a) {
       scaled_pair(j, is.x, is.y, va, vb);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        uint32_t w = __builtin_amdgcn_perm(code_bits(vb[r], rq[r].step), code_bits(va[r], rq[r].step), 0x0c0c0400u);
+        uint32_t w = __builtin_amdgcn_perm(code_bits(vb[r], rq[r]), code_bits(va[r], rq[r]), 0x0c0c0400u);
         if (rq[r].bad) w = 0;
         if (r & 1)
           ov[u][r / 2] |= w << 16;

@@ -1,0 +1,53 @@
+"""Numbers of the 8-bit path where they can go wrong, on the GPU: half-way values behind a transform.
+
+Tolerances count roundings: U = 2^-24 is half a float32 step.
+"""
+import numpy as np
+import pytest
+
+from oracle import q8_oracle as Q
+from tests import gpu_common as C
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+rl = pytest.importorskip("rotated_linear_amd")
+
+U = 2.0 ** -24
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def still(D, K):
+    """A transform that moves nothing: K stages of angle 0 (c = 1, s = 0) and channel scales of 1."""
+    r = np.random.default_rng([D, K])
+    pairs = np.stack([r.permutation(D).reshape(D // 2, 2) for _ in range(K)]) if K else np.zeros((0, D // 2, 2))
+    return rl.paro_rotation_prepare(pairs.astype(np.int32), np.zeros((K, D // 2), np.float32), np.ones(D, np.float32))
+
+
+def half_way_rows(M, D, dt):
+    """Rows with maximum 127 m 2^e and values m (2 k + 1) 2^(e - 1), half way between two codes."""
+    ms = [1, 3, 5, 7, 9, 11, 13, 15] if dt == "f16" else [1]  # 127 m in the type's digits
+    k = np.arange(D) % 256 - 128
+    base = np.where(k == -128, 127.0, np.clip(k + 0.5, -126.5, 126.5))
+    x = np.stack([base * ms[i % len(ms)] * 2.0 ** (i % 7 - 3) for i in range(M)])
+    x = np.where(Q.round_to(x, dt) == x, x, 0.0)  # the halves that the type holds
+    assert np.all(np.abs(x).max(axis=1) == 127.0 * np.array([ms[i % len(ms)] * 2.0 ** (i % 7 - 3) for i in range(M)]))
+    return x
+
+
+# one, two and four rows a workgroup; the widest four-row blocks, whose channel scales are read twice
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,D,K", [(9, 256, 0), (40, 256, 2), (300, 384, 3), (530, 512, 0), (520, 4096, 1), (513, 8704, 0), (514, 9216, 2)])
+def test_half_way_values_behind_a_transform_go_to_the_even_code(M, D, K, dt):
+    """The codes of a row are the same whether it comes through a transform that moves nothing or not:
+    rint of the exact quotient, ties to even."""
+    C.log(f"half way behind a transform M={M} D={D} K={K} {dt}")
+    x = half_way_rows(M, D, dt)
+    real, scale = Q.quantize_exact(x)
+    want = np.rint(real)
+    t = torch.from_numpy(x).to(DT[dt]).cuda()
+    q, s = rl.paro_quantize_q8(t, still(D, K))
+    assert np.array_equal(q.cpu().numpy(), want)
+    assert np.array_equal(s.double().cpu().numpy(), Q.round_to(scale, "f32"))
+    p, ps = rl.paro_quantize_q8(t)
+    assert torch.equal(p, q) and torch.equal(ps, s)
