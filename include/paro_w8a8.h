@@ -45,7 +45,8 @@ extern "C" {
  * x, residual, residual_out dtype [M][D], gamma dtype [D]; q int8 [M][D], scales float32 [M]. The
  * addition is float32 rounded once; the norm is that of the rounded h, the row that the next
  * layers see. The mean of squares is float64 (no overflow for bfloat16 rows), 1 / sqrt rounded
- * once to float32. eps must be finite and at least 2^-126. residual and residual_out go together
+ * once to float32; bfloat16 rows where h * gamma or 1 / sqrt leave float32's range, though n may not,
+ * have n in float64, rounded once. eps must be finite and at least 2^-126. residual and residual_out go together
  * (both or neither NULL, else PARO_EINVAL) and may be the same pointer: the stream is then updated
  * in place. x may not be residual_out.
  */

@@ -42,9 +42,14 @@ __device__ inline void wave_reduce(uint32_t& top, double& sum, bool with_sum) {
 // monotonic, so the row's largest |n| is the largest |t| times inv: one reduction (the sum of squares
 // in float64 and the largest |t|) gives both the norm and the scale. The codes are those of t over its
 // own maximum, the same numbers without the rounding of the product with inv.
+//
+// bfloat16 rows reach float32's ends: h * gamma may pass its range, or lose digits under 2^-126, where n is
+// an ordinary number, and inv too may lie under 2^-126. Such a row (one branch for the whole workgroup,
+// after the reduction) is read again and its n worked out in float64, with a reduction of its own.
+// float16 rows stay within 2^-48 .. 2^32 and have no such branch.
 template <int DT, bool NORM, bool Q8, int VPT>
 __global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
-  __shared__ uint32_t stop[2][16];
+  __shared__ uint32_t stop[2][16], ntop64[2][16];
   __shared__ double ssum[2][16];
   const int tid = threadIdx.x, nt = blockDim.x, waves = nt / 64;
   const int chunks = a.D / 8;
@@ -123,14 +128,45 @@ __global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
       __syncthreads();  // one per row: the other parity's slots are rewritten only after the next one
       top = 0;
       sum = 0;
-      for (int w = 0; w < waves; ++w) {
+#pragma unroll 4
+      for (int w = 0; w < waves; ++w) {  // (more sums at once would take the registers of a second workgroup)
         top = max(top, stop[parity][w]);
         if constexpr (NORM) sum += ssum[parity][w];
       }
       if constexpr (NORM) {
-        inv = float(1.0 / __builtin_sqrt(sum / a.D + double(a.eps)));
-        const uint32_t ntop = abs_order(__builtin_bit_cast(float, top) * inv);
+        const double inv64 = 1.0 / __builtin_sqrt(sum / a.D + double(a.eps));
+        inv = float(inv64);
+        uint32_t ntop = abs_order(__builtin_bit_cast(float, top) * inv);
         constexpr uint32_t kMinBits = __builtin_bit_cast(uint32_t, kQ8MinTop);
+        if constexpr (DT == PARO_BF16) {
+          // (beside a top of 2^-100 or more, what a product under 2^-126 loses is less than 2^-49 of it)
+          if (top >= kAbsInf || (top < kMinBits && sum != 0) || inv < 0x1p-126f) {  // uniform
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+              const int c = tid + i * nt;
+              if (c < chunks) {
+                const u32x4* const from = res ? ro : x;  // (h: this thread's own stores)
+                const u32x4 hr = from[row * chunks + c];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  uint32_t gv = gw[i][w];
+                  asm volatile("" : "+v"(gv));  // converted here again, not kept as floats from above
+                  t[i][2 * w] = float(double(from_bits16<DT>(hr[w] & 0xFFFFu)) * double(from_bits16<DT>(gv & 0xFFFFu)) * inv64);
+                  t[i][2 * w + 1] = float(double(from_bits16<DT>(hr[w] >> 16)) * double(from_bits16<DT>(gv >> 16)) * inv64);
+                  m = max(m, max(abs_order(t[i][2 * w]), abs_order(t[i][2 * w + 1])));
+                }
+              }
+            }
+            double none = 0;
+            wave_reduce(m, none, false);
+            if ((tid & 63) == 63) ntop64[parity][tid >> 6] = m;
+            __syncthreads();
+            for (int w = 0; w < waves; ++w) m = max(m, ntop64[parity][w]);
+            ntop = top = m;
+            inv = 1.0f;
+          }
+        }
         // (a row under the smallest scale, or t under it, takes its codes from n itself)
         const bool from_t = Q8 && ntop >= kMinBits && top >= kMinBits;
         rq = row_quant(ntop, from_t ? top : ntop);

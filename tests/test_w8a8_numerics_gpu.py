@@ -51,3 +51,41 @@ def test_half_way_values_behind_a_transform_go_to_the_even_code(M, D, K, dt):
     assert np.array_equal(s.double().cpu().numpy(), Q.round_to(scale, "f32"))
     p, ps = rl.paro_quantize_q8(t)
     assert torch.equal(p, q) and torch.equal(ps, s)
+
+
+@pytest.mark.parametrize("with_residual", [True, False])
+@pytest.mark.parametrize("M,D", [(7, 128), (6, 1536), (530, 4096), (1100, 6144), (700, 16384)])
+def test_norm_of_bfloat16_rows_at_the_ends_of_the_range(M, D, with_residual):
+    """n is an ordinary number where h * gamma is not: rows of large numbers under a large gamma, rows of
+    small ones under a small gamma (eps decides their norm), rows whose 1 / sqrt is under 2^-126, and
+    ordinary rows among them. A workgroup walks several rows in the larger calls."""
+    C.log(f"norm range M={M} D={D} residual={with_residual}")
+    r = np.random.default_rng([M, D])
+    eps = 2.0 ** -126
+    for power, g_power in ((124, 6), (-118, -24), (126, -10)):
+        x = r.normal(0, 1, (M, D))
+        if power == 126:
+            x = np.sign(x) * r.uniform(0.8, 1.9, (M, D))  # rms above 2^126
+        x[1::2] = np.ldexp(x[1::2], power)
+        res = np.zeros((M, D)) if power == 126 else x[::-1][: M] * 0.25 if M % 2 else np.roll(x, 2, axis=0) * 0.25
+        g = np.ldexp(r.normal(1, 0.3, D), g_power)
+        x, res, g = (torch.from_numpy(v.astype(np.float32)).bfloat16() for v in (x, res, g))
+        h64 = x.double().numpy()
+        if with_residual:
+            h64 = Q.round_to(Q.round_to(h64 + res.double().numpy(), "f32"), "bf16")
+        assert np.isfinite(h64).all()
+        n = Q.rmsnorm(h64, g.double().numpy(), eps)
+        kw = {"residual": res.cuda()} if with_residual else {}
+        y, h = rl.paro_rmsnorm(x.cuda(), g.cuda(), eps, **kw)
+        q, s, h8 = rl.paro_rmsnorm_q8(x.cuda(), g.cuda(), eps, **kw)
+        if with_residual:
+            assert np.array_equal(h.double().cpu().numpy(), h64) and torch.equal(h, h8)
+            stream = res.cuda()  # and the stream updated in place
+            y2, h2 = rl.paro_rmsnorm(x.cuda(), g.cuda(), eps, residual=stream, residual_out=stream)
+            assert torch.equal(y2, y) and torch.equal(h2, h)
+        # the bounds of the ordinary rows: three float32 roundings and the type's own, the scale's division,
+        # the codes' step and product
+        assert C.over_bound(y.double().cpu().numpy() - n, np.abs(n) * (4 * U + 2.0 ** -8) + 2.0 ** -134) <= 1, power
+        real, want = Q.quantize_exact(n)
+        assert C.over_bound(s.double().cpu().numpy() - want, want * 5 * U) <= 1, power
+        assert np.abs(q.cpu().numpy() - real).max() <= 0.5 + 127 * 6 * U, power
