@@ -88,10 +88,22 @@ __device__ inline float scaled(int sum, float xs, float ws) {
   return v;
 }
 
-// silu(g) u = g u / (1 + exp(-g)); exp(-g) past float32 gives an infinity and the quotient -0, and the
-// reciprocal instruction may give 0 for one under 2^-126 already.
+// silu(g) u = g u / (1 + exp(-g)) for an output of type DT. 16-bit outputs: exp(-g) past float32 gives an
+// infinity and the quotient -0, the reciprocal instruction may give 0 for one under 2^-126 already, and the
+// rounded argument of exp2 costs up to 1.2 |g| units of 2^-24, which a result of 11 or 8 bits does not
+// see. float32 outputs: exp(-|g|), which does not overflow, from the math library, and a quotient, each to
+// float32's last digit.
+template <int DT>
 __device__ inline float silu_mul(float g, float u) {
-  float v = g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896f)) * u;
+  float v;
+  if constexpr (DT == PARO_F32) {
+    const float e = expf(-fabsf(g)), den = 1.0f + e, num = g < 0 ? g * e : g;
+    // num / den from the reciprocal and its remainder; an infinite g, and any past 17, has den = 1
+    const float r = __builtin_amdgcn_rcpf(den), q = num * r;
+    v = (den == 1.0f ? num : __builtin_fmaf(__builtin_fmaf(-q, den, num), r, q)) * u;
+  } else {
+    v = g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896f)) * u;
+  }
   asm("" : "+v"(v));
   return v;
 }

@@ -116,7 +116,10 @@ __global__ __launch_bounds__(64 * W) void w8a8_column_kernel(const W8A8Call c) {
     }
     const float xs = c.xs[m];
     float y = scaled(v[0], xs, c.ws[n]);
-    if constexpr (GATED) y = silu_mul(y, scaled(v[1], xs, c.ws[size_t(c.N) + n]));
+    if constexpr (GATED) {
+      const float u = scaled(v[1], xs, c.ws[size_t(c.N) + n]);
+      y = c.ydtype == PARO_F32 ? silu_mul<PARO_F32>(y, u) : silu_mul<PARO_F16>(y, u);
+    }
     const size_t at = size_t(m) * c.N + n;
     if (c.ydtype == PARO_F32)
       static_cast<float*>(c.y)[at] = y;

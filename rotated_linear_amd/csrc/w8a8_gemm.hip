@@ -187,7 +187,7 @@ __device__ inline void store_tile(const GemmArgs& a, const Place& p, const i32x4
               const float4 u4 = *reinterpret_cast<const float4*>(wsc + 16);
               const float u0[4] = {u4.x, u4.y, u4.z, u4.w};
 #pragma unroll
-              for (int e = 0; e < 4; ++e) v[e] = silu_mul(v[e], scaled(acc[i + u][j + 1][e], xs[u], u0[e]));
+              for (int e = 0; e < 4; ++e) v[e] = silu_mul<DT>(v[e], scaled(acc[i + u][j + 1][e], xs[u], u0[e]));
             }
             put4<DT>(at, v);
           }
@@ -393,7 +393,7 @@ __global__ __launch_bounds__(256) void reduce_kernel(const W8A8Call c, const int
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       v[e] = scaled(g[e], xs, c.ws[n + e]);
-      if constexpr (GATED) v[e] = silu_mul(v[e], scaled(u[e], xs, c.ws[size_t(c.N) + n + e]));
+      if constexpr (GATED) v[e] = silu_mul<DT>(v[e], scaled(u[e], xs, c.ws[size_t(c.N) + n + e]));
     }
     if constexpr (V == 4) {
       put4<DT>(static_cast<char*>(c.y) + (m * c.N + n) * (DT == PARO_F32 ? 4 : 2), v);

@@ -92,7 +92,10 @@ __global__ __launch_bounds__(64 * W) void w8a8_stream_kernel(const W8A8Call c) {
     };
     const float xs = c.xs[m];
     float v = scaled(sum(t), xs, c.ws[n]);
-    if constexpr (GATED) v = silu_mul(v, scaled(sum(t + YT), xs, c.ws[size_t(c.N) + n]));
+    if constexpr (GATED) {
+      const float u = scaled(sum(t + YT), xs, c.ws[size_t(c.N) + n]);
+      v = c.ydtype == PARO_F32 ? silu_mul<PARO_F32>(v, u) : silu_mul<PARO_F16>(v, u);
+    }
     const size_t at = size_t(m) * c.N + n;
     if (c.ydtype == PARO_F32)
       static_cast<float*>(c.y)[at] = v;

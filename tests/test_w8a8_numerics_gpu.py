@@ -89,3 +89,34 @@ def test_norm_of_bfloat16_rows_at_the_ends_of_the_range(M, D, with_residual):
         real, want = Q.quantize_exact(n)
         assert C.over_bound(s.double().cpu().numpy() - want, want * 5 * U) <= 1, power
         assert np.abs(q.cpu().numpy() - real).max() <= 0.5 + 127 * 6 * U, power
+
+
+def exact_gates(seed, M, D, F):
+    """Codes and scales (powers of two) whose gates and ups are exact in float32: sums under 2^24 over a
+    power of two, gates from a fraction to about +-100, so that nothing but the activation rounds."""
+    r = np.random.default_rng([seed, M, D, F])
+    xq = r.integers(-127, 128, (M, D)).astype(np.int8)
+    wq = r.integers(-127, 128, (2 * F, D)).astype(np.int8)
+    xs = np.ldexp(1.0, r.integers(-3, 3, M)).astype(np.float32)
+    spread = int(np.rint(np.log2(73.0 * 73.0 * np.sqrt(D))))  # a sum's standard deviation, about
+    ws = np.ldexp(1.0, r.integers(1, 6, 2 * F) - spread).astype(np.float32)
+    return xq, xs, wq, ws
+
+
+# streamed, by columns, tiled, and tiled with a split reduction
+@pytest.mark.parametrize("M,D,F", [(1, 128, 600), (2, 256, 129), (8, 256, 300), (40, 1152, 200), (64, 128, 33), (130, 640, 515), (200, 8960, 65),
+                                   (700, 512, 1030)])
+def test_silu_in_float32(M, D, F):
+    """A float32 output of the gated linear carries the activation to float32, whatever the gate. With exact
+    g and u, in units of U: exp(-|g|) 2 (one float32 step), for a negative gate its product with g 1; 1 + exp
+    1 and at most 1 of exp's own; the quotient 1; the product with u 1: 7, 2 % more for their products.
+    Under 2^-126 exp(-|g|) is off by the last digit there, 2^-149, and the products and the quotient by half
+    of one each."""
+    C.log(f"silu f32 M={M} D={D} F={F}")
+    xq, xs, wq, ws = exact_gates(71, M, D, F)
+    v, g, u = Q.gated(xq, xs, wq, ws)
+    assert np.array_equal(g, g.astype(np.float32)) and np.array_equal(u, u.astype(np.float32))
+    if M * F > 20000:
+        assert g.min() < -95 and g.max() > 95 and np.abs(g).min() < 0.01
+    y = rl.paro_w8a8_gated_linear(*(torch.from_numpy(a).cuda() for a in (xq, xs, wq, ws)), torch.float32).double().cpu().numpy()
+    assert C.over_bound(y - v, 7.15 * U * np.abs(v) + 2.0 ** -149 * (np.abs(g * u) + np.abs(u) + 1)) <= 1
