@@ -22,6 +22,7 @@
  *     zero row has codes 0 and a positive scale. Arithmetic is float32 (float64 where stated)
  *     except for rounding of the result. A row with an infinity or a NaN has scale NaN and codes
  *     0, so everything computed from that row, and nothing else, is NaN.
+ *   - Forward only: these are the calls of a served model, and none has a backward pass.
  *   - Results do not depend on the other rows of a call, on the workspace or on its previous
  *     contents, and are the same bits every time.
  */
@@ -105,10 +106,10 @@ size_t paro_w8a8_gated_workspace_bytes(int M, int D, int F);
  * paro_w8a8_gated_linear -- both projections of a gated feed-forward block, the activation and the
  * product in one: with g and u the linears of qweight's first and last F rows,
  *     y[m][f] = silu(g[m][f]) * u[m][f],  silu(g) = g / (1 + exp(-g))
- * in float32, rounded once to ydtype. A float32 y has the activation to float32's last digits; a 16-bit y
- * to its own, and where 1 / (1 + exp(-g)) is under 2^-126 (g below -87.3) that may count as 0. qweight int8 [2F][D] (gate rows 0..F-1, then up rows; F below
- * 2^29), wscales float32 [2F], y [M][F]; the rest as in paro_w8a8_linear. Forward only: the codes are
- * constants of a served model.
+ * in float32, rounded once to ydtype. A float32 y has the activation to float32's last digits; a
+ * 16-bit y to its own, and where 1 / (1 + exp(-g)) is under 2^-126 (g below -87.3) that may count as
+ * 0. qweight int8 [2F][D] (gate rows 0..F-1, then up rows; F below 2^29), wscales float32 [2F], y
+ * [M][F]; the rest as in paro_w8a8_linear.
  */
 paro_status paro_w8a8_gated_linear(int M, int D, int F, const int8_t* x, const float* xscales, const int8_t* qweight,
                                    const float* wscales, void* y, int ydtype, void* ws, size_t ws_bytes, void* stream);

@@ -3,12 +3,13 @@
 // (2.5 of it the runtime's launch).
 //
 // Every function here returns None, having done nothing, when an argument is not what the call takes
-// (another type, shape, device, stride or a tensor subclass), when another GPU is current, or when the
+// (another type, shape, device, stride or a tensor subclass, or a gradient asked for), when another GPU is current, or when the
 // library refuses: w8a8.py then goes through its own checks, which say what is wrong. The library's
 // entry points (include/paro_w8a8.h) are handed over as addresses by bind().
 #include <Python.h>
 #include <ATen/ATen.h>
 #include <ATen/EmptyTensor.h>
+#include <ATen/core/grad_mode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -80,6 +81,18 @@ bool output(PyObject* o, const Tensor& like, int device, ScalarType type, at::In
   return true;
 }
 
+// Autograd would lose a gradient without a word: the calls are forward only.
+template <class... T>
+bool wants_grad(const T*... t) {
+  return at::GradMode::is_enabled() && (... || (t && t->requires_grad()));
+}
+// A tensor of the caller's was written: its version counter says so to autograd.
+void wrote(PyObject* o) {
+  if (o == Py_None) return;
+  const Tensor* const t = tensor(o);
+  if (!t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // The type of an output: `o` (a torch.dtype or None), else the output's own, else float16.
 bool out_type(PyObject* o, const Tensor* out, ScalarType* type) {
   if (o == Py_None)
@@ -107,7 +120,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
   const int N = gated ? rows / 2 : rows;
   if ((a[6] != Py_None && !fits(out, type, device, M, N)) ||
-      (a[7] != Py_None && !(ws && fits(ws, ScalarType::Byte, device, ws->numel()))))
+      (a[7] != Py_None && !(ws && fits(ws, ScalarType::Byte, device, ws->numel()))) || wants_grad(xs, wsc, out))
     Py_RETURN_NONE;
   Tensor y = out ? *out : make(*x, {M, N}, type);
   const auto call = [&](void* work, size_t bytes) {
@@ -122,6 +135,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     st = call(work.mutable_data_ptr(), bytes);
   }
   if (st != PARO_OK) Py_RETURN_NONE;
+  wrote(a[6]);
   return THPVariable_Wrap(y);
   END_HANDLE_TH_ERRORS
 }
@@ -140,11 +154,15 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!desc || !desc->is_cuda() || desc->get_device() != device || rot->dev != desc->const_data_ptr()) Py_RETURN_NONE;
   }
   Tensor q, s;
-  if (!output(a[4], *x, device, ScalarType::Char, {M, D}, &q) || !output(a[5], *x, device, ScalarType::Float, {M}, &s)) Py_RETURN_NONE;
+  if (!output(a[4], *x, device, ScalarType::Char, {M, D}, &q) || !output(a[5], *x, device, ScalarType::Float, {M}, &s) ||
+      wants_grad(a[0] == Py_True ? nullptr : x, &s))  // packed weights are constants: W may be a parameter
+    Py_RETURN_NONE;
   const paro_status st = (a[0] == Py_True ? g_pack : g_quantize)(rot, M, D, dtype_code(x->scalar_type()), x->const_data_ptr(),
                                                                  static_cast<int8_t*>(q.mutable_data_ptr()),
                                                                  static_cast<float*>(s.mutable_data_ptr()), stream(device));
   if (st != PARO_OK) Py_RETURN_NONE;
+  wrote(a[4]);
+  wrote(a[5]);
   return Py_BuildValue("(NN)", THPVariable_Wrap(q), THPVariable_Wrap(s));
   END_HANDLE_TH_ERRORS
 }
@@ -160,10 +178,11 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !out_type(a[2], a[3] == Py_None ? nullptr : tensor(a[3]), &type))
     Py_RETURN_NONE;
   Tensor x;
-  if (!output(a[3], *q, device, type, {M, D}, &x)) Py_RETURN_NONE;
+  if (!output(a[3], *q, device, type, {M, D}, &x) || wants_grad(s, &x)) Py_RETURN_NONE;
   const paro_status st = g_dequantize(M, D, static_cast<const int8_t*>(q->const_data_ptr()), static_cast<const float*>(s->const_data_ptr()),
                                       x.mutable_data_ptr(), dtype_code(type), stream(device));
   if (st != PARO_OK) Py_RETURN_NONE;
+  wrote(a[3]);
   return THPVariable_Wrap(x);
   END_HANDLE_TH_ERRORS
 }
@@ -182,7 +201,8 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float eps = float(PyFloat_AS_DOUBLE(a[3]));
   Tensor h, q, s;
   if (!output(a[6], *x, device, q8 ? ScalarType::Char : type, {M, D}, &q) ||
-      (q8 && !output(a[7], *x, device, ScalarType::Float, {M}, &s)) || (has && !output(a[5], *x, device, type, {M, D}, &h)))
+      (q8 && !output(a[7], *x, device, ScalarType::Float, {M}, &s)) || (has && !output(a[5], *x, device, type, {M, D}, &h)) ||
+      wants_grad(x, gamma, res, has ? &h : nullptr, &q, q8 ? &s : nullptr))
     Py_RETURN_NONE;
   void* const hp = has ? h.mutable_data_ptr() : nullptr;
   const void* const rp = has ? res->const_data_ptr() : nullptr;
@@ -191,12 +211,17 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (g_rmsnorm_q8(M, D, dtype_code(type), x->const_data_ptr(), rp, gamma->const_data_ptr(), eps, hp,
                      static_cast<int8_t*>(q.mutable_data_ptr()), static_cast<float*>(s.mutable_data_ptr()), stream(device)) != PARO_OK)
       Py_RETURN_NONE;
+    wrote(a[5]);
+    wrote(a[6]);
+    wrote(a[7]);
     if (!has) return Py_BuildValue("(NNO)", THPVariable_Wrap(q), THPVariable_Wrap(s), none);
     return Py_BuildValue("(NNN)", THPVariable_Wrap(q), THPVariable_Wrap(s), THPVariable_Wrap(h));
   }
   if (g_rmsnorm(M, D, dtype_code(type), x->const_data_ptr(), rp, gamma->const_data_ptr(), eps, hp, q.mutable_data_ptr(),
                 stream(device)) != PARO_OK)
     Py_RETURN_NONE;
+  wrote(a[5]);
+  wrote(a[6]);
   if (!has) return Py_BuildValue("(NO)", THPVariable_Wrap(q), none);
   return Py_BuildValue("(NN)", THPVariable_Wrap(q), THPVariable_Wrap(h));
   END_HANDLE_TH_ERRORS

@@ -1,6 +1,7 @@
 """Python binding of the 8-bit path (include/paro_w8a8.h): residual RMS norm, row quantisation,
 8-bit weights and the W8A8 products. Argument marshalling only, as in the package; the names mirror
-the C ABI.
+the C ABI. The calls are forward only: with gradients enabled a tensor that requires one is refused
+(weights to be packed aside, which become constants).
 
 A decode-sized call takes a few microseconds on the GPU, so a call whose operands are as they should
 be goes through the compiled ``_binding`` (checks, outputs and the C call in one step). Where that
@@ -62,9 +63,24 @@ def _channels(D):
         raise ParoError(2, "D")
 
 
-def _call(fn, what, dev, *args):
+def _forward_only(named):
+    """The calls have no backward pass: refuse a tensor of ``named`` (name -> tensor or None) whose gradient
+    would be lost without a word."""
+    if torch.is_grad_enabled():
+        for name, t in named.items():
+            if t is not None and t.requires_grad:
+                raise RuntimeError(f"{name} requires a gradient and this call is forward only: "
+                                   "detach it, or make the call under torch.no_grad()")
+
+
+def _call(fn, what, dev, *args, wrote=()):
+    """The C call on dev's current stream. ``wrote``: the outputs that the caller gave, whose version counters
+    then tell autograd that they changed."""
     with torch.cuda.device(dev):
         _check(fn(*args, _stream_ptr(dev)), what)
+    for t in wrote:
+        if t is not None:
+            torch.autograd.graph.increment_version(t)
 
 
 def _norm(q8, x, gamma, eps, residual, residual_out, outs):
@@ -81,14 +97,16 @@ def _norm(q8, x, gamma, eps, residual, residual_out, outs):
     for t, kind in zip(outs, kinds):
         if t is not None:
             _want(t, *kind)
-    dev = _on_gpu({"x": x, "gamma": gamma, "residual": residual, "residual_out": residual_out,
-                   **{k[2]: t for t, k in zip(outs, kinds)}})
+    named = {"x": x, "gamma": gamma, "residual": residual, "residual_out": residual_out, **{k[2]: t for t, k in zip(outs, kinds)}}
+    _forward_only(named)
+    dev = _on_gpu(named)
+    wrote = (residual_out, *outs)
     outs = [torch.empty(k[1], dtype=k[0], device=dev) if t is None else t for t, k in zip(outs, kinds)]
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(residual)
     name = "paro_rmsnorm_q8" if q8 else "paro_rmsnorm"
     _call(getattr(_lib, name), name, dev, M, D, _DTYPE[x.dtype], _ptr(x), _ptr(residual), _ptr(gamma), eps,
-          _ptr(residual_out), *map(_ptr, outs))
+          _ptr(residual_out), *map(_ptr, outs), wrote=wrote)
     return (*outs, residual_out)
 
 
@@ -121,11 +139,15 @@ def _quantize(pack, x, rot, out):
     if out is not None:
         _want(q, torch.int8, (M, D), qname)
         _want(scales, torch.float32, (M,), "scales")
-    dev = _on_gpu({what: x, qname: q, "scales": scales, "the transform": None if rot is None else rot.desc})
+    named = {what: x, qname: q, "scales": scales, "the transform": None if rot is None else rot.desc}
+    _forward_only({k: t for k, t in named.items() if k != "W"})  # packed weights are constants: W may be a parameter
+    dev = _on_gpu(named)
+    wrote = (q, scales)
     if out is None:
         q = torch.empty((M, D), dtype=torch.int8, device=dev)
         scales = torch.empty(M, dtype=torch.float32, device=dev)
-    _call(getattr(_lib, name), name, dev, None if rot is None else rot.ptr, M, D, _DTYPE[x.dtype], _ptr(x), _ptr(q), _ptr(scales))
+    _call(getattr(_lib, name), name, dev, None if rot is None else rot.ptr, M, D, _DTYPE[x.dtype], _ptr(x), _ptr(q), _ptr(scales),
+          wrote=wrote)
     return q, scales
 
 
@@ -157,9 +179,11 @@ def paro_dequantize_q8(q, scales, out_dtype=None, out=None):
         raise TypeError(f"the output must be float16, bfloat16 or float32, got {dtype}")
     if out is not None:
         _want(out, dtype, (M, D), "out")
-    dev = _on_gpu({"q": q, "scales": scales, "out": out})
+    named = {"q": q, "scales": scales, "out": out}
+    _forward_only(named)
+    dev = _on_gpu(named)
     x = torch.empty((M, D), dtype=dtype, device=dev) if out is None else out
-    _call(_lib.paro_dequantize_q8, "paro_dequantize_q8", dev, M, D, _ptr(q), _ptr(scales), _ptr(x), _DTYPE[dtype])
+    _call(_lib.paro_dequantize_q8, "paro_dequantize_q8", dev, M, D, _ptr(q), _ptr(scales), _ptr(x), _DTYPE[dtype], wrote=(out,))
     return x
 
 
@@ -193,13 +217,15 @@ def _linear(gated, x, x_scales, qweight, w_scales, out_dtype, out, ws):
     if out is not None:
         _want(out, dtype, (M, N), "out")
     _want_ws(ws)
-    dev = _on_gpu({"x": x, "x_scales": x_scales, "qweight": qweight, "w_scales": w_scales, "out": out, "ws": ws})
+    named = {"x": x, "x_scales": x_scales, "qweight": qweight, "w_scales": w_scales, "out": out, "ws": ws}
+    _forward_only(named)
+    dev = _on_gpu(named)
     y = torch.empty((M, N), dtype=dtype, device=dev) if out is None else out
     name, need = ("paro_w8a8_gated_linear", paro_w8a8_gated_workspace_bytes) if gated else ("paro_w8a8_linear", paro_w8a8_workspace_bytes)
     if ws is None and need(M, D, N):
         ws = torch.empty(need(M, D, N), dtype=torch.uint8, device=dev)
     _call(getattr(_lib, name), name, dev, M, D, N, _ptr(x), _ptr(x_scales), _ptr(qweight), _ptr(w_scales), _ptr(y), _DTYPE[dtype],
-          _ptr(ws), 0 if ws is None else ws.numel())
+          _ptr(ws), 0 if ws is None else ws.numel(), wrote=(out,))
     return y
 
 
