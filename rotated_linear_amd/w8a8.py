@@ -6,11 +6,14 @@ the C ABI. The calls are forward only: with gradients enabled a tensor that requ
 A decode-sized call takes a few microseconds on the GPU, so a call whose operands are as they should
 be goes through the compiled ``_binding`` (checks, outputs and the C call in one step). Where that
 declines (it returns None and has done nothing), the functions here check the operands one by one,
-say what is wrong, or make the call on another GPU than the current one.
+say what is wrong, or make the call on another GPU than the current one. Without the extension, or
+with one that was built for another torch, every call goes that way: the same kernels, some 4 us more
+of host time each.
 """
 from __future__ import annotations
 
 import ctypes
+import warnings
 
 import torch
 
@@ -18,8 +21,19 @@ from . import F16, F32, GROUP, MAX_D, ParoError, _check, _i, _lib, _on_gpu, _ptr
 
 try:
     from . import _binding
+    _for = getattr(_binding, "torch_version", "another version")
+    if _for != torch.__version__.split("+")[0]:
+        raise ImportError(f"it was built for torch {_for}, this is {torch.__version__}")
 except ImportError as e:
-    raise ImportError("the package's _binding is missing: build it with `python -m rotated_linear_amd._build`") from e
+    warnings.warn(f"rotated_linear_amd runs without its compiled binding ({e}): the 8-bit calls take more host time. "
+                  "Build it with `python -m rotated_linear_amd._build`.", RuntimeWarning, stacklevel=2)
+
+    class _binding:  # declines every call
+        @staticmethod
+        def _declines(*_):
+            return None
+
+        bind = linear = quantize = dequantize = rmsnorm = _declines
 
 BF16 = 2
 _DTYPE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
