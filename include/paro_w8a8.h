@@ -94,7 +94,9 @@ size_t paro_w8a8_workspace_bytes(int M, int D, int N);
  * integer sum is exact, then float32, rounded once to ydtype (PARO_F16, PARO_BF16 or PARO_F32).
  * x int8 [M][D], xscales float32 [M], qweight int8 [N][D], wscales float32 [N], y [M][N]. ws holds
  * at least paro_w8a8_workspace_bytes(M, D, N) bytes (else PARO_EWORKSPACE; NULL where that is 0)
- * and overlaps no operand. Two calls that may run at the same time need two workspaces.
+ * and overlaps no operand. Two calls that may run at the same time need two workspaces. M and N are
+ * at most 2^31 - 512 (PARO_EINVAL). The products are taken in the order written: a sum times xscales[m]
+ * that passes float32 is an infinity, whatever wscales[n].
  */
 paro_status paro_w8a8_linear(int M, int D, int N, const int8_t* x, const float* xscales, const int8_t* qweight,
                              const float* wscales, void* y, int ydtype, void* ws, size_t ws_bytes, void* stream);

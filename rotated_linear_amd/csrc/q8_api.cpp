@@ -1,5 +1,6 @@
 // Host side of the 8-bit path (include/paro_w8a8.h): argument checks and dispatch. Every error
 // path returns before anything is enqueued on the stream.
+#include <limits.h>
 #include <math.h>
 
 #include "q8_internal.h"
@@ -32,6 +33,11 @@ bool any_overlap(const Span (&outs)[NO], const Span (&ins)[NI]) {
 
 // The byte offsets of a gated call's 2 F scales stay below 2^32.
 constexpr int kMaxGatedF = (1 << 29) - 1;
+// Rows of x and of y's columns: rounded up to a tile they still are ints.
+constexpr int kMaxProductRows = INT_MAX - 511;
+bool good_rows(int M, int N, bool gated) {
+  return M >= 0 && N >= 0 && M <= kMaxProductRows && N <= (gated ? kMaxGatedF : kMaxProductRows);
+}
 
 bool good_ptr(const void* p) { return p && aligned16(p); }
 bool good_D(int D) { return D >= PARO_GROUP && D <= PARO_MAX_D && D % PARO_GROUP == 0; }
@@ -85,7 +91,7 @@ paro_status norm(int M, int D, int dtype, const void* x, const void* residual, c
 
 paro_status linear(int M, int D, int N, bool gated, const int8_t* x, const float* xs, const int8_t* w, const float* wsc,
                    void* y, int ydtype, void* ws, size_t ws_bytes, void* stream) {
-  if (M < 0 || N < 0 || (gated && N > kMaxGatedF) || !out_dtype(ydtype)) return PARO_EINVAL;
+  if (!good_rows(M, N, gated) || !out_dtype(ydtype)) return PARO_EINVAL;
   if (!good_D(D)) return PARO_ESHAPE;
   if (M == 0 || N == 0) return PARO_OK;
   if (!good_ptr(x) || !good_ptr(xs) || !good_ptr(w) || !good_ptr(wsc) || !good_ptr(y)) return PARO_EINVAL;
@@ -164,11 +170,11 @@ paro_status paro_pack_weights_q8(const paro_rotation* r, int N, int D, int dtype
 }
 
 size_t paro_w8a8_workspace_bytes(int M, int D, int N) {
-  return M > 0 && N > 0 && good_D(D) ? plan(M, D, N, false).tiled.part_bytes : 0;
+  return M > 0 && N > 0 && good_rows(M, N, false) && good_D(D) ? plan(M, D, N, false).tiled.part_bytes : 0;
 }
 
 size_t paro_w8a8_gated_workspace_bytes(int M, int D, int F) {
-  return M > 0 && F > 0 && F <= kMaxGatedF && good_D(D) ? plan(M, D, F, true).tiled.part_bytes : 0;
+  return M > 0 && F > 0 && good_rows(M, F, true) && good_D(D) ? plan(M, D, F, true).tiled.part_bytes : 0;
 }
 
 paro_status paro_w8a8_linear(int M, int D, int N, const int8_t* x, const float* xscales, const int8_t* qweight,
