@@ -89,14 +89,15 @@ paro_status norm(int M, int D, int dtype, const void* x, const void* residual, c
                                  as_stream(stream)));
 }
 
-paro_status linear(int M, int D, int N, bool gated, const int8_t* x, const float* xs, const int8_t* w, const float* wsc,
+// forced: the plan to take instead of the shape's own, or nullptr.
+paro_status linear(const Plan* forced, int M, int D, int N, bool gated, const int8_t* x, const float* xs, const int8_t* w, const float* wsc,
                    void* y, int ydtype, void* ws, size_t ws_bytes, void* stream) {
   if (!good_rows(M, N, gated) || !out_dtype(ydtype)) return PARO_EINVAL;
   if (!good_D(D)) return PARO_ESHAPE;
   if (M == 0 || N == 0) return PARO_OK;
   if (!good_ptr(x) || !good_ptr(xs) || !good_ptr(w) || !good_ptr(wsc) || !good_ptr(y)) return PARO_EINVAL;
   const size_t rows = size_t(N) * (gated ? 2 : 1);
-  const Plan p = plan(M, D, N, gated);
+  const Plan p = forced ? *forced : plan(M, D, N, gated);
   const size_t need = p.tiled.part_bytes;
   if (need && (!ws || ws_bytes < need)) return PARO_EWORKSPACE;
   if (need && !aligned16(ws)) return PARO_EINVAL;
@@ -179,13 +180,41 @@ size_t paro_w8a8_gated_workspace_bytes(int M, int D, int F) {
 
 paro_status paro_w8a8_linear(int M, int D, int N, const int8_t* x, const float* xscales, const int8_t* qweight,
                              const float* wscales, void* y, int ydtype, void* ws, size_t ws_bytes, void* stream) {
-  return linear(M, D, N, false, x, xscales, qweight, wscales, y, ydtype, ws, ws_bytes, stream);
+  return linear(nullptr, M, D, N, false, x, xscales, qweight, wscales, y, ydtype, ws, ws_bytes, stream);
 }
 
 paro_status paro_w8a8_gated_linear(int M, int D, int F, const int8_t* x, const float* xscales, const int8_t* qweight,
                                    const float* wscales, void* y, int ydtype, void* ws, size_t ws_bytes,
                                    void* stream) {
-  return linear(M, D, F, true, x, xscales, qweight, wscales, y, ydtype, ws, ws_bytes, stream);
+  return linear(nullptr, M, D, F, true, x, xscales, qweight, wscales, y, ydtype, ws, ws_bytes, stream);
+}
+
+void paro_internal_w8a8_plan(int M, int D, int N, int gated, int* kernel, int* tile, int* splits) {
+  const Plan p = plan(M, D, N, gated != 0);
+  *kernel = int(p.kernel);
+  *tile = p.kernel == Kernel::kTiled ? p.tiled.tile : -1;
+  *splits = p.kernel == Kernel::kTiled ? p.tiled.splits : 1;
+}
+
+int paro_internal_w8a8_tiling(int tile, int* bm, int* bn, int* workgroups) {
+  if (tile < 0 || tile >= kTilingsQ8) return 0;
+  const TilingQ8 t = tiling_w8a8(tile);
+  *bm = t.bm;
+  *bn = t.bn;
+  *workgroups = t.workgroups;
+  return 1;
+}
+
+size_t paro_internal_w8a8_tiled_workspace_bytes(int M, int N, int gated, int splits) {
+  return part_bytes_w8a8(M, N, gated != 0, splits);
+}
+
+paro_status paro_internal_w8a8_tiled(int tile, int splits, int gated, int M, int D, int N, const int8_t* x, const float* xscales,
+                                     const int8_t* qweight, const float* wscales, void* y, int ydtype, void* ws, size_t ws_bytes,
+                                     void* stream) {
+  if (tile < 0 || tile >= kTilingsQ8 || splits < 1 || splits > D / PARO_GROUP) return PARO_EINVAL;
+  const Plan p{Kernel::kTiled, {tile, splits, part_bytes_w8a8(M, N, gated != 0, splits), 0}};
+  return linear(&p, M, D, N, gated != 0, x, xscales, qweight, wscales, y, ydtype, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

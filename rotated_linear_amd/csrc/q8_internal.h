@@ -59,6 +59,26 @@ struct GemmPlanQ8 {
   double us;          // estimated time
 };
 GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated);
+constexpr int kTilingsQ8 = 7;
+struct TilingQ8 {
+  int bm, bn;      // rows of x and of w in a tile
+  int workgroups;  // that the GPU holds at once
+};
+TilingQ8 tiling_w8a8(int tile);
+// Workspace of a reduction in this many parts (1: none).
+size_t part_bytes_w8a8(int M, int N, bool gated, int splits);
 hipError_t launch_w8a8_gemm(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStream_t st);
 
 }  // namespace paro
+
+// For tests, and in no header of the library: which kernel a product takes (0 streamed, 1 by columns, 2 tiled)
+// with its tiling and split, what a tiling is, and a product in a given tiling and split (at most one part for
+// each 128 channels; the rest as in paro_w8a8_linear and paro_w8a8_gated_linear).
+extern "C" {
+void paro_internal_w8a8_plan(int M, int D, int N, int gated, int* kernel, int* tile, int* splits);
+int paro_internal_w8a8_tiling(int tile, int* bm, int* bn, int* workgroups);  // 0 past the last one
+size_t paro_internal_w8a8_tiled_workspace_bytes(int M, int N, int gated, int splits);
+paro_status paro_internal_w8a8_tiled(int tile, int splits, int gated, int M, int D, int N, const int8_t* x, const float* xscales,
+                                     const int8_t* qweight, const float* wscales, void* y, int ydtype, void* ws, size_t ws_bytes,
+                                     void* stream);
+}

@@ -419,6 +419,11 @@ hipError_t launch_reduce(const W8A8Call& c, const int* part, int splits, hipStre
   return go(four ? reduce_kernel<4, GATED, PARO_BF16> : reduce_kernel<1, GATED, PARO_BF16>);
 }
 
+template <class T>
+constexpr TilingQ8 tiling() {
+  return TilingQ8{T::BM, T::BN, kCUs * int(160 * 1024 / T::LDS)};
+}
+
 template <class T, bool GATED>
 hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st) {
   GemmArgs a;
@@ -433,8 +438,7 @@ hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st)
   const void* fn = reinterpret_cast<const void*>(&w8a8_gemm_kernel<T, GATED>);
   if (hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS)) return e;
   const long total = long(a.tiles_m) * a.tiles_n * a.splits;
-  const long resident = long(kCUs) * std::max(1, int(160 * 1024 / T::LDS));
-  hipLaunchKernelGGL((w8a8_gemm_kernel<T, GATED>), dim3(unsigned(std::min(total, resident))), dim3(T::NT), T::LDS, st, a);
+  hipLaunchKernelGGL((w8a8_gemm_kernel<T, GATED>), dim3(unsigned(std::min<long>(total, tiling<T>().workgroups))), dim3(T::NT), T::LDS, st, a);
   if (hipError_t e = hipGetLastError()) return e;
   return a.part ? launch_reduce<GATED>(c, part, a.splits, st) : hipSuccess;
 }
@@ -468,16 +472,31 @@ constexpr TileCost kTiles[] = {{256, 256, 1, 1.24, 1.56, 9.0}, {256, 128, 1, 0.8
                                {32, 64, 2, 0.157, 0.316, 1.07}};
 constexpr double kLaunchUs = 3.18, kSplitUs = 2.77, kHbmBytesPerUs = 4.57e6, kPartBytesPerUs = 5.37e6;
 
+constexpr TilingQ8 kTilings[kTilingsQ8] = {tiling<T256>(),    tiling<T256x128>(), tiling<T128>(), tiling<T128Two>(),
+                                           tiling<T128x64>(), tiling<T64>(),      tiling<T32>()};
+constexpr bool costs_name_the_tilings() {
+  for (int t = 0; t < kTilingsQ8; ++t)
+    if (kTiles[t].bm != kTilings[t].bm || kTiles[t].bn != kTilings[t].bn || kTiles[t].cap * kCUs != kTilings[t].workgroups) return false;
+  return sizeof(kTiles) / sizeof(kTiles[0]) == kTilingsQ8;
+}
+static_assert(costs_name_the_tilings(), "the cost table's rows are the tilings");
+
 // Partial sums of a split reduction at most (larger ones cost more than a split gives).
 constexpr double kMaxPartBytes = double(size_t(128) << 20);
 
 }  // namespace
 
+TilingQ8 tiling_w8a8(int tile) { return kTilings[tile]; }
+
+size_t part_bytes_w8a8(int M, int N, bool gated, int splits) {
+  return splits > 1 ? align256(size_t(splits) * M * N * (gated ? 2 : 1) * 4) : 0;
+}
+
 GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated) {
   const double rows = double(N) * (gated ? 2 : 1);
   const int steps = D / 128;
   GemmPlanQ8 best{1, 1, 0, 1e30};
-  for (int t = 0; t < int(sizeof(kTiles) / sizeof(kTiles[0])); ++t) {
+  for (int t = 0; t < kTilingsQ8; ++t) {
     const TileCost& k = kTiles[t];
     const double tiles = std::ceil(double(M) / k.bm) * std::ceil(rows / k.bn);
     for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
@@ -492,7 +511,7 @@ GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated) {
       const double hbm = rows * D / kHbmBytesPerUs;
       us = kLaunchUs + std::cbrt(us * us * us + hbm * hbm * hbm);
       if (s > 1) us += kSplitUs + 2 * part / kPartBytesPerUs;
-      if (us < best.us) best = GemmPlanQ8{t, s, s > 1 ? align256(size_t(part)) : 0, us};
+      if (us < best.us) best = GemmPlanQ8{t, s, part_bytes_w8a8(M, N, gated, s), us};
     }
   }
   return best;
