@@ -13,7 +13,6 @@ constexpr float kQ8MinTop = 0x1p-100f;
 // Rows of 16-bit elements, read as the library's own vector types.
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 using i32x4 = int __attribute__((ext_vector_type(4)));
-using i32x16 = int __attribute__((ext_vector_type(16)));
 
 struct NormArgs {
   int M, D, dtype;

@@ -17,7 +17,6 @@
 namespace paro {
 namespace {
 
-constexpr size_t kLds = 160 * 1024;
 constexpr int kCUs = 256;
 
 struct RotQ8Args {
@@ -220,6 +219,7 @@ __global__ __launch_bounds__(NT) void rotate_q8_kernel(const RotQ8Args a) {
 
 template <int DT, int NT, int R, int PPT, int PD, bool EXACT>
 hipError_t launch(const RotQ8Args& a, hipStream_t st) {
+  static_assert((R == 4 ? 9216 : PARO_MAX_D) * R * sizeof(float) + NT / 64 * R * sizeof(uint32_t) <= 160 * 1024, "one CU's LDS");
   const size_t lds = size_t(a.D) * R * sizeof(float) + NT / 64 * R * sizeof(uint32_t);
   const void* fn = reinterpret_cast<const void*>(&rotate_q8_kernel<DT, NT, R, PPT, PD, EXACT>);
   if (lds > 64 * 1024)
@@ -271,10 +271,8 @@ hipError_t launch_ppt(const RotQ8Args& a, hipStream_t st) {
 
 template <int DT>
 hipError_t launch_rows(const RotQ8Args& a, hipStream_t st) {
-  // rows per block: as few as give every CU one block, up to what LDS holds with the maxima beside it
-  const size_t row = size_t(a.D) * sizeof(float);
-  const auto fits = [&](int r) { return r * row + 16 * r * sizeof(uint32_t) <= kLds; };
-  if (a.M <= kCUs || !fits(2)) return launch_ppt<DT, 1>(a, st);
+  // rows per block: as few as give every CU one block; two rows of any width fit in LDS, four up to 9216 channels
+  if (a.M <= kCUs) return launch_ppt<DT, 1>(a, st);
   if (a.M <= 2 * kCUs || a.D > 9216) return launch_ppt<DT, 2>(a, st);
   return launch_ppt<DT, 4>(a, st);
 }
