@@ -55,8 +55,9 @@ paro_status paro_rmsnorm_q8(int M, int D, int dtype, const void* x, const void* 
                             float eps, void* residual_out, int8_t* q, float* scales, void* stream);
 
 /*
- * paro_rmsnorm -- the same norm with y = dtype(n) [M][D] as its output: the 16-bit rows that
- * paro_rotate and the W4A16 linears read. Arguments as in paro_rmsnorm_q8.
+ * paro_rmsnorm -- the same norm with y = dtype(n) [M][D] as its output: rows for paro_quantize_q8
+ * behind a transform, and, in float16 only, for paro_rotate and the W4A16 linears. Arguments as in
+ * paro_rmsnorm_q8.
  */
 paro_status paro_rmsnorm(int M, int D, int dtype, const void* x, const void* residual, const void* gamma, float eps,
                          void* residual_out, void* y, void* stream);
@@ -79,7 +80,7 @@ paro_status paro_dequantize_q8(int M, int D, const int8_t* q, const float* scale
  * W (r == NULL), or on the row with the transform folded in (the K stages of r, then times s, as
  * paro_pack_weights folds it), so that transform(x) . W'^T = x . W^T. Every product and sum of
  * the fold is float64 with no fused multiply-add, v * 127 / c is held to twice that precision, and scale
- * is rounded once to float32. W dtype [N][D]; qweight int8 [N][D] row-major (row n is weight row n),
+ * is rounded once to float32 (past its range, which no s of ordinary size takes a row to, an infinity). W dtype [N][D]; qweight int8 [N][D] row-major (row n is weight row n),
  * scales float32 [N].
  */
 paro_status paro_pack_weights_q8(const paro_rotation* r, int N, int D, int dtype, const void* W, int8_t* qweight,

@@ -1,10 +1,11 @@
 // Build-time weights in 8 bits: each row of W, with the transform folded in or as it is, quantised
 // in float64 by its largest magnitude.
 //
-// One workgroup per weight row, the row in LDS as float64. Bound by LDS and the float64 units together:
-// every stage gathers and rewrites the row (at D = 4096 about 27 us a 4096 rows at LDS's full rate, and as
-// much again for some 16 instructions a pair). Measured, K = 8, cold W: 4096 x 4096 81 us, 1024 x 14336 90,
-// 256 x 1536 7.9. Two or four rows a workgroup, which read a record once for all, were no faster (77 us
+// One workgroup per weight row, the row in LDS as float64. Every stage gathers and rewrites the row: at D =
+// 4096 about 27 us a 4096 rows at LDS's full rate, and as much again for some 16 float64 instructions a pair.
+// The two hardly overlap. Measured (graph replays, cold W), K = 8: 4096 x 4096 73.6 us, 1024 x 14336 86, 256 x
+// 1536 6.4. Rows without a transform take the same passes with no stages: 4096 x 4096 26.2 us (10.6 of bytes),
+// 28672 x 4096 154, 4096 x 14336 118, 256 x 1536 3.6. Two or four rows a workgroup, which read a record once for all, were no faster (77 us
 // where this takes 70): the records come from L2 in time, and wider LDS accesses move no more bytes a
 // cycle. Loading the next stage's records ahead did not pay either: it takes registers, and with them the
 // waves that hide LDS's latency. Compiled with -ffp-contract=off: each product and each sum of the fold is

@@ -2,13 +2,19 @@
 // and the division by the channel scales in float32 (rotation_core.h), then 8-bit codes, in one
 // kernel. The rotated row never leaves the chip and is not rounded to 16 bits in between.
 //
-// Bound by LDS like the 16-bit transform (rotate.hip), and built like it: a workgroup holds R rows in
+// Built like the 16-bit transform (rotate.hip): a workgroup holds R rows in
 // LDS as float32, interleaved by channel, streams the stages' records through a register ring, and
 // walks blocks of R rows with the next block's rows on their way meanwhile. After the last stage the
 // rows are read twice: once for each row's largest magnitude, once for its codes. The second read
 // costs LDS the half of one stage and saves the registers that would hold the row in between.
-// Measured, K = 8: 4096 x 4096 41.6 us (the 16-bit transform alone 38.9), 4096 x 1536 16.8 (19.8), 2048 x
-// 8960 50.2 (48.4), 64 x 4096 7.4 (7.9), 1000 x 14336 41.3 (42.8).
+// Measured (graph replays, cold rows), K = 8: 4096 x 4096 37.5 us (the 16-bit transform alone 35.0), 4096 x
+// 1536 16.1 (19.1), 2048 x 8960 46.8 (45.6), 64 x 4096 6.2 (6.4), 1000 x 14336 39.6 (39.4), 16 x 1536 4.2 (4.3).
+//
+// What bounds it: the stages, 16 of the 19 passes over the row in LDS. No unit is full (4096 x 4096: LDS
+// active 39 % of a CU's cycles and stalled by bank conflicts 10 %, VALU 43 %, HBM 10.6 us of 37.5), and the
+// barriers are not it either (a timing copy of the 16-bit transform without them 34.6 us against 37.0). A
+// copy of its stages with half the LDS traffic ran a four-row stage in 1300 cycles instead of 2000: carrying
+// one channel of each pair in a register from stage to stage is what is left to build.
 #include <algorithm>
 
 #include "q8_device.h"

@@ -1,8 +1,9 @@
 // Row kernels of the 8-bit path: residual addition + RMS norm (8-bit or 16-bit output), the row
 // quantiser, and reading 8-bit rows back. All are bound by HBM: one pass over the row, which stays
-// in registers between its statistics and its output. Measured (cold rows): rmsnorm with residual
-// 4096 x 4096 25.8 us (7 bytes a channel, 4.6 TB/s; a copy of 1 GiB runs at 4.7), quantiser 12.8 us
-// (3.9 TB/s), read-back 11.9 us (4.2 TB/s); a single row of 4096 2.7 to 3.1 us, a launch.
+// in registers between its statistics and its output. Measured (graph replays, cold rows): rmsnorm_q8 with
+// residual 4096 x 4096 bf16 25.4 us (7 bytes a channel, 4.6 TB/s; a copy of 1 GiB runs at 4.7), rmsnorm
+// 26.1 us (8 bytes, 5.1 TB/s), quantiser 13.0 us (3.9 TB/s), read-back 12.3 us (4.1 TB/s); a single row of
+// 4096 2.7, 2.4, 2.1 and 1.9 us, a launch.
 #include <algorithm>
 
 #include "q8_device.h"

@@ -457,12 +457,14 @@ using T32 = Tile<32, 64, 2, 2, 128, 4>;        // two
 
 // Estimated time of a call in microseconds, from a fit to 2457 measured combinations of shape, tiling
 // and split (MI355X, cold weights, 58 shapes: M = 18..4096, D = 128..16256, N = 64..23000; 11 % rms
-// off; the 256 x 128 tile had two stages then: with lower times for it, 35 shapes came out no faster as a
-// whole, since more of them went to it that other tilings do better): a launch; the units that a CU works through, per 128 channels of a unit (alone on a CU, and
+// off): a launch; the units that a CU works through, per 128 channels of a unit (alone on a CU, and
 // with `cap` units on it or on every CU) plus its start and end; the weights' way from HBM; these two
 // joined as the cube root of the sum of their cubes, since they overlap but not wholly; and for a
 // split a launch and the partial sums out and back. The choice by it was 1.5 % slower than the fastest
-// measured one on average, 19 % at worst.
+// measured one on average, 19 % at worst. The 256 x 128 tile had two stages when the fit was made; it has
+// three now, so its times here are too high, and some shapes that would gain up to 5 % by it go to others.
+// Lowering its row alone moved shapes to it that others do better (35 shapes, no faster as a whole): the
+// whole table wants fitting again.
 struct TileCost {
   int bm, bn, cap;
   double alone, full, end;

@@ -135,8 +135,8 @@ def paro_rmsnorm_q8(x, gamma, eps=1e-6, residual=None, out=None, residual_out=No
 
 
 def paro_rmsnorm(x, gamma, eps=1e-6, residual=None, out=None, residual_out=None):
-    """The same norm with its rows in x's type, as paro_rotate and the W4A16 linears read them:
-    (y [M][D], h). ``out``: an optional tensor for y."""
+    """The same norm with its rows in x's type, for paro_quantize_q8 behind a transform or (float16) for
+    paro_rotate and the W4A16 linears: (y [M][D], h). ``out``: an optional tensor for y."""
     r = _binding.rmsnorm(False, x, gamma, eps, residual, residual_out, out, None)
     return r if r is not None else _norm(False, x, gamma, eps, residual, residual_out, (out,))
 

@@ -378,8 +378,8 @@ def test_gated_linear(M, D, F):
     assert torch.equal(y, rl.paro_w8a8_gated_linear(*d, torch.float32))
 
 
-# Every tiling of the tiled kernel: one tile per workgroup and several, reductions whole and split,
-# ragged ends and rows of y at 16-byte boundaries.
+# Shapes that the plan spreads over the tilings of the tiled kernel, whole and split, with ragged ends and rows
+# of y at 16-byte boundaries. (test_w8a8_tilings.py runs each tiling by name.)
 TILED = [(654, 384, 11023, False), (1606, 256, 15152, False), (138, 11904, 5769, False), (258, 384, 11466, True), (1158, 256, 9798, True),
          (134, 12032, 2840, True), (129, 128, 12350, False), (514, 128, 13270, False), (514, 128, 13272, False), (68, 128, 8478, True),
          (260, 128, 10981, True), (260, 128, 10984, True), (71, 9472, 8197, True), (129, 512, 13533, False), (2075, 13824, 65, False),
