@@ -13,6 +13,7 @@ of host time each.
 from __future__ import annotations
 
 import ctypes
+import re
 import warnings
 
 import torch
@@ -22,7 +23,7 @@ from . import F16, F32, GROUP, MAX_D, ParoError, _check, _i, _lib, _on_gpu, _ptr
 try:
     from . import _binding
     _for = getattr(_binding, "torch_version", "another version")
-    if _for != torch.__version__.split("+")[0]:
+    if re.match(r"\d+\.\d+\.\d+", torch.__version__)[0] != _for:  # (its headers name no pre-release)
         raise ImportError(f"it was built for torch {_for}, this is {torch.__version__}")
 except ImportError as e:
     warnings.warn(f"rotated_linear_amd runs without its compiled binding ({e}): the 8-bit calls take more host time. "

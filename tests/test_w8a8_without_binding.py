@@ -57,6 +57,20 @@ def test_the_binding_names_the_torch_it_was_built_for():
     assert _binding.torch_version == torch.__version__.split("+")[0]
 
 
+def test_a_pre_release_of_torch_keeps_the_binding():
+    """Its headers name 1.2.3 where torch itself says 1.2.3.dev4+5 or 1.2.3a0."""
+    run = """
+import sys, warnings, torch
+torch.__version__ = torch.__version__.split("+")[0] + sys.argv[1]
+warnings.simplefilter("error")
+import rotated_linear_amd.w8a8 as w
+print(w._binding.__name__)
+"""
+    for tail in (".dev20300101+rocm9", "a0+git1234"):
+        r = subprocess.run([sys.executable, "-c", run, tail], cwd=ROOT, capture_output=True, text=True, timeout=300)
+        assert r.stdout.strip() == "rotated_linear_amd._binding", r.stdout + r.stderr
+
+
 @pytest.mark.parametrize("broken", ["source", "compiler"])
 def test_a_binding_that_does_not_compile_does_not_stop_the_build(broken, tmp_path, monkeypatch):
     spec = importlib.util.spec_from_file_location("build_under_test", os.path.join(ROOT, "rotated_linear_amd", "_build.py"))
