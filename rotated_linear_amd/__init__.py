@@ -415,3 +415,7 @@ def paro_linear_batch(calls, out_dtype=None, outs=None, ws=None):
 from .w8a8 import (BF16, EXPORTS_W8A8, paro_dequantize_q8, paro_pack_weights_q8, paro_quantize_q8,  # noqa: E402,F401
                    paro_rmsnorm, paro_rmsnorm_q8, paro_w8a8_gated_linear, paro_w8a8_gated_workspace_bytes,
                    paro_w8a8_linear, paro_w8a8_workspace_bytes)
+
+# What surrounds the products of a decoder block (include/paro_block.h).
+from .block import (EXPORTS_BLOCK, paro_block_norm, paro_block_norm_q8, paro_moe_layer_w4a16, paro_moe_route,  # noqa: E402,F401
+                    paro_moe_route_workspace_bytes, paro_moe_w4a16, paro_moe_workspace_bytes, paro_w8a8_linear_epilogue)

@@ -108,4 +108,86 @@ __device__ inline float silu_mul(float g, float u) {
   return v;
 }
 
+// erfc(z) exp(z^2) / 2 for z >= 0 to 2^-19 of its value: t times a polynomial of degree 6 in t = 1 / (1 + z / 2),
+// fitted for the smallest relative error over 0 <= z <= 10 (least squares, reweighted by the error).
+__device__ inline float half_erfcx(float z) {
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(z, 0.5f, 1.0f));
+  float p = 0.04410196840763092f;
+  p = __builtin_fmaf(p, t, -0.17836840450763702f);
+  p = __builtin_fmaf(p, t, 0.19461128115653992f);
+  p = __builtin_fmaf(p, t, 0.018946044147014618f);
+  p = __builtin_fmaf(p, t, 0.14075161516666412f);
+  p = __builtin_fmaf(p, t, 0.13879111409187317f);
+  p = __builtin_fmaf(p, t, 0.14116570353507996f);
+  return p * t;
+}
+
+// act(v) for an output of type DT, as silu_mul is: float32 outputs from the math library's exp and erfc, 16-bit
+// outputs to their own last digits (a result under 2^-126 may count as 0 there). Every sum of products is a
+// fused one, written out, so that all kernels give the same bits.
+template <int DT, int V>
+__device__ inline void activate(float (&v)[V], int act) {
+  if (act == PARO_ACT_RELU || act == PARO_ACT_RELU2) {  // (a NaN stays one)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float r = v[i] < 0 ? 0.0f : v[i];
+      v[i] = act == PARO_ACT_RELU ? r : r * r;
+    }
+  } else if (act == PARO_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = silu_mul<DT>(v[i], 1.0f);
+  } else if (act == PARO_ACT_GELU) {
+    // half = erfc(|v| / sqrt(2)) / 2; v - v half where v is positive and v half where it is not keep their digits
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float a = fabsf(v[i]), z = a * 0.70710678118654752f;
+      float half;
+      if constexpr (DT == PARO_F32)
+        half = 0.5f * erfcf(z);
+      else
+        half = half_erfcx(z) * __builtin_amdgcn_exp2f(a * a * -0.72134752044448170f);
+      v[i] = v[i] < 0 ? v[i] * half : half == 0.0f ? v[i] : __builtin_fmaf(-v[i], half, v[i]);  // (an infinity stays one)
+    }
+  } else if (act == PARO_ACT_GELU_TANH) {  // v (1 + tanh(t / 2)) / 2 = v / (1 + exp(-t))
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float t = v[i] * __builtin_fmaf(0.071354816272600251f, v[i] * v[i], 1.5957691216057308f);
+      if constexpr (DT == PARO_F32) {
+        const float e = expf(-fabsf(t)), num = v[i] < 0 ? v[i] * e : v[i];
+        v[i] = num / (1.0f + e);
+      } else {
+        v[i] = v[i] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(t * -1.44269504088896f));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) asm("" : "+v"(v[i]));
+}
+
+// The steps of an output with an epilogue, behind scaled(): float32 each, the last one rounded to the output's
+// type by the caller. Opaque, as scaled() is.
+__device__ inline float plus(float v, float w) {
+  v += w;
+  asm("" : "+v"(v));
+  return v;
+}
+// Element i of an array of type ydtype.
+__device__ inline float load_element(const void* p, size_t i, int ydtype) {
+  if (ydtype == PARO_F32) return static_cast<const float*>(p)[i];
+  const uint32_t h = static_cast<const uint16_t*>(p)[i];
+  return ydtype == PARO_F16 ? from_bits16<PARO_F16>(h) : from_bits16<PARO_BF16>(h);
+}
+// y[m][n] of a call with an epilogue, from its product.
+__device__ inline float epilogue(const W8A8Call& c, float v, int m, int n) {
+  if (c.bias) v = plus(v, load_element(c.bias, n, c.ydtype));
+  float o[1] = {v};
+  if (c.ydtype == PARO_F32)
+    activate<PARO_F32>(o, c.act);
+  else
+    activate<PARO_F16>(o, c.act);
+  v = o[0];
+  if (c.residual) v = plus(v, load_element(c.residual, size_t(m) * c.N + n, c.ydtype));
+  return v;
+}
+
 }  // namespace paro

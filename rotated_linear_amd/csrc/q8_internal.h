@@ -1,6 +1,7 @@
 // Internal declarations of the 8-bit path (include/paro_w8a8.h).
 #pragma once
 
+#include "paro_block.h"
 #include "paro_internal.h"
 #include "paro_w8a8.h"
 
@@ -24,8 +25,14 @@ struct NormArgs {
   void* y;       // 16-bit output, or
   int8_t* q;     // codes and
   float* scales; // scales
+  // the norm and gate after a block (launch_block_norm): x is the block's output
+  const void* post_gamma;  // nullptr: no norm
+  const void* gate;        // nullptr: none
+  uint32_t gate_rows;      // row m takes the gate's row m / gate_rows
+  float residual_scale;
 };
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st);
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t st);
 hipError_t launch_quantize_q8(int M, int D, int dtype, const void* x, int8_t* q, float* scales, hipStream_t st);
 hipError_t launch_dequantize_q8(int M, int D, const int8_t* q, const float* scales, void* x, int dtype, hipStream_t st);
 // The row quantiser behind the transform R.
@@ -33,7 +40,8 @@ hipError_t launch_rotate_q8(const DevRot& R, int M, int dtype, const void* x, in
 // R.K == 0 and R.s == nullptr: no transform.
 hipError_t launch_pack_q8(const DevRot& R, int N, int dtype, const void* W, int8_t* q, float* scales, hipStream_t st);
 
-// One 8-bit product: y [M][N], or with `gated` y [M][N] = silu(gate) * up from weights [2N][D].
+// One 8-bit product: y [M][N], or with `gated` y [M][N] = silu(gate) * up from weights [2N][D], or with
+// `epilogue` y = act(product + bias) + residual.
 struct W8A8Call {
   int M, D, N;
   bool gated;
@@ -43,7 +51,13 @@ struct W8A8Call {
   const float* ws;
   void* y;
   int ydtype;
+  bool epilogue;
+  int act;               // paro_activation
+  const void* bias;      // ydtype [N], or nullptr
+  const void* residual;  // ydtype [M][N], or nullptr
 };
+// What a product kernel makes of its sums.
+enum Output { kPlain, kGated, kEpilogue };
 // A row or two: the weights streamed into registers, no workspace.
 bool w8a8_stream_takes(int M, int N);
 hipError_t launch_w8a8_stream(const W8A8Call& c, hipStream_t st);
@@ -80,4 +94,7 @@ size_t paro_internal_w8a8_tiled_workspace_bytes(int M, int N, int gated, int spl
 paro_status paro_internal_w8a8_tiled(int tile, int splits, int gated, int M, int D, int N, const int8_t* x, const float* xscales,
                                      const int8_t* qweight, const float* wscales, void* y, int ydtype, void* ws, size_t ws_bytes,
                                      void* stream);
+paro_status paro_internal_w8a8_tiled_epilogue(int tile, int splits, int M, int D, int N, const int8_t* x, const float* xscales,
+                                              const int8_t* qweight, const float* wscales, const void* bias, int activation,
+                                              const void* residual, void* y, int ydtype, void* ws, size_t ws_bytes, void* stream);
 }

@@ -36,6 +36,14 @@ __device__ inline void wave_reduce(uint32_t& top, double& sum, bool with_sum) {
   wave_step<0x143, 0xC>(top, sum, with_sum);  // row_bcast:31 into rows 2 and 3
 }
 
+// residual_scale * r + p, one fused multiply-add; with a scale of 1 that is the sum. Opaque to the compiler, as the
+// rounding to the row's type that follows is one of its own.
+__device__ inline float block_sum(float r, float scale, float p) {
+  float v = __builtin_fmaf(scale, r, p);
+  asm("" : "+v"(v));
+  return v;
+}
+
 // A workgroup walks rows blockIdx.x, + gridDim.x, ...; a thread holds VPT chunks of 8 channels. The
 // next row is loaded before this row's statistics are complete. NORM: the norm, else v = x.
 //
@@ -48,16 +56,21 @@ __device__ inline void wave_reduce(uint32_t& top, double& sum, bool with_sum) {
 // an ordinary number, and inv too may lie under 2^-126. Such a row (one branch for the whole workgroup,
 // after the reduction) is read again and its n worked out in float64, with a reduction of its own.
 // float16 rows stay within 2^-48 .. 2^32 and have no such branch.
-template <int DT, bool NORM, bool Q8, int VPT>
+//
+// BLOCK: x is a block's output, and h comes from it through a norm of its own (with post_gamma), a gate and the
+// scaled residual. That norm's sum needs a reduction of its own, in front of the other, and the next row is loaded
+// between the two: x, residual and gate are not done with before.
+template <int DT, bool NORM, bool Q8, bool BLOCK, int VPT>
 __global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
   __shared__ uint32_t stop[2][16], ntop64[2][16];
   __shared__ double ssum[2][16];
+  __shared__ double psum[BLOCK ? 2 : 1][16];
   const int tid = threadIdx.x, nt = blockDim.x, waves = nt / 64;
   const int chunks = a.D / 8;
   const u32x4* const x = static_cast<const u32x4*>(a.x);
   const u32x4* const res = static_cast<const u32x4*>(a.residual);
   u32x4* const ro = static_cast<u32x4*>(a.residual_out);
-  u32x4 gw[VPT], xw[VPT], rw[VPT];
+  u32x4 gw[VPT], xw[VPT], rw[VPT], pw[BLOCK ? VPT : 1], tw[BLOCK ? VPT : 1];
   auto load = [&](size_t row) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -65,6 +78,9 @@ __global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
       if (c < chunks) {
         xw[i] = x[row * chunks + c];
         if (NORM && res) rw[i] = res[row * chunks + c];
+        if constexpr (BLOCK) {
+          if (a.gate) tw[i] = static_cast<const u32x4*>(a.gate)[size_t(uint32_t(row) / a.gate_rows) * chunks + c];
+        }
       }
     }
   };
@@ -73,20 +89,74 @@ __global__ __launch_bounds__(1024) void rows_kernel(const NormArgs a) {
   if constexpr (NORM) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      if (tid + i * nt < chunks) gw[i] = static_cast<const u32x4*>(a.gamma)[tid + i * nt];
+      if (tid + i * nt < chunks) {
+        gw[i] = static_cast<const u32x4*>(a.gamma)[tid + i * nt];
+        if constexpr (BLOCK) {
+          if (a.post_gamma) pw[i] = static_cast<const u32x4*>(a.post_gamma)[tid + i * nt];
+        }
+      }
   }
   for (int parity = 0;; parity ^= 1) {
     float t[VPT][8];
     u32x4 hw[VPT];
     uint32_t top = 0;
     double sum = 0;
+    // the first norm: 1 / sqrt of a bfloat16 row of large numbers may lie under 2^-126, so these are scaled first
+    float first = 1.0f, down = 1.0f;
+    if constexpr (BLOCK) {
+      if (a.post_gamma) {  // uniform
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          float v[8];
+          unpack8<DT>(xw[i], v);
+          double s = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s = __builtin_fma(double(v[e]), double(v[e]), s);
+          sum += tid + i * nt < chunks ? s : 0.0;
+        }
+        uint32_t none = 0;
+        wave_reduce(none, sum, true);
+        if ((tid & 63) == 63) psum[parity][tid >> 6] = sum;
+        __syncthreads();
+        sum = 0;
+#pragma unroll 4
+        for (int w = 0; w < waves; ++w) sum += psum[parity][w];
+        double r = 1.0 / __builtin_sqrt(sum / a.D + double(a.eps));
+        if (DT == PARO_BF16 && r < 0x1p-64) {
+          down = 0x1p-64f;
+          r *= 0x1p64;
+        }
+        first = float(r);
+        sum = 0;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const bool live = tid + i * nt < chunks;
       float h[8];
       unpack8<DT>(xw[i], h);
+      if constexpr (BLOCK) {
+        if (a.post_gamma) {
+          float g[8];
+          unpack8<DT>(pw[i], g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] = h[e] * down * first * g[e];
+        }
+        if (a.gate) {
+          float g[8];
+          unpack8<DT>(tw[i], g);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] *= g[e];
+        }
+        float r[8];
+        unpack8<DT>(rw[i], r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = block_sum(r[e], a.residual_scale, h[e]);
+        hw[i] = pack8<DT>(h);
+        unpack8<DT>(hw[i], h);
+      }
       if constexpr (NORM) {
-        if (res) {
+        if (!BLOCK && res) {
           float r[8];
           unpack8<DT>(rw[i], r);
 #pragma unroll
@@ -221,7 +291,7 @@ __global__ __launch_bounds__(256) void dequantize_kernel(size_t total, uint32_t 
   }
 }
 
-template <int DT, bool NORM, bool Q8>
+template <int DT, bool NORM, bool Q8, bool BLOCK>
 hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
   const int chunks = a.D / 8;
   // Few rows: as many threads as chunks (latency). Many rows: two chunks a thread, whose next row is on
@@ -230,21 +300,25 @@ hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
   const int nt = std::max(64, ((chunks + vpt - 1) / vpt + 63) / 64 * 64);
   const unsigned grid = unsigned(std::min(a.M, kCUs * (2048 / nt)));
   if (vpt == 2)
-    hipLaunchKernelGGL((rows_kernel<DT, NORM, Q8, 2>), dim3(grid), dim3(nt), 0, st, a);
+    hipLaunchKernelGGL((rows_kernel<DT, NORM, Q8, BLOCK, 2>), dim3(grid), dim3(nt), 0, st, a);
   else
-    hipLaunchKernelGGL((rows_kernel<DT, NORM, Q8, 1>), dim3(grid), dim3(nt), 0, st, a);
+    hipLaunchKernelGGL((rows_kernel<DT, NORM, Q8, BLOCK, 1>), dim3(grid), dim3(nt), 0, st, a);
   return hipGetLastError();
 }
 
-template <bool NORM, bool Q8>
+template <bool NORM, bool Q8, bool BLOCK = false>
 hipError_t launch_rows(const NormArgs& a, hipStream_t st) {
-  return a.dtype == PARO_F16 ? launch_rows<PARO_F16, NORM, Q8>(a, st) : launch_rows<PARO_BF16, NORM, Q8>(a, st);
+  return a.dtype == PARO_F16 ? launch_rows<PARO_F16, NORM, Q8, BLOCK>(a, st) : launch_rows<PARO_BF16, NORM, Q8, BLOCK>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st) {
   return a.q ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);
+}
+
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t st) {
+  return a.q ? launch_rows<true, true, true>(a, st) : launch_rows<true, false, true>(a, st);
 }
 
 hipError_t launch_quantize_q8(int M, int D, int dtype, const void* x, int8_t* q, float* scales, hipStream_t st) {

@@ -8,7 +8,7 @@
 namespace paro {
 namespace {
 
-// FM fragments of 16 rows of x against 16 rows of w (GATED: 16 gate and 16 up rows). Wave s takes the
+// FM fragments of 16 rows of x against 16 rows of w (kGated: 16 gate and 16 up rows). Wave s takes the
 // steps s, s + W, ... of 128 channels: rows of x and w come straight into a ring of S stages of its
 // own in LDS, S steps ahead, so the waves never wait for each other until their sums are added.
 //
@@ -20,8 +20,9 @@ namespace {
 // 2 KB apart lie in the same L2 channel: M = 12, 4096 -> 4096 6.0 -> 5.4 us.
 // Tried: a wave of its own that touches the weights ahead of the others (64 x 14336 -> 4096 23.9 ->
 // 25.5 us), w's loads before x's (no change).
-template <int FM, bool GATED, int W, int S>
+template <int FM, Output KIND, int W, int S>
 __global__ __launch_bounds__(64 * W) void w8a8_column_kernel(const W8A8Call c) {
+  constexpr bool GATED = KIND == kGated;
   constexpr int WN = GATED ? 2 : 1;
   constexpr int ROWS = 16 * (FM + WN), STAGE = ROWS * 128, LOADS = ROWS / 8;
   extern __shared__ __attribute__((aligned(1024))) char smem[];  // [W][S][STAGE]
@@ -120,6 +121,7 @@ __global__ __launch_bounds__(64 * W) void w8a8_column_kernel(const W8A8Call c) {
       const float u = scaled(v[1], xs, c.ws[size_t(c.N) + n]);
       y = c.ydtype == PARO_F32 ? silu_mul<PARO_F32>(y, u) : silu_mul<PARO_F16>(y, u);
     }
+    if constexpr (KIND == kEpilogue) y = epilogue(c, y, m, n);
     const size_t at = size_t(m) * c.N + n;
     if (c.ydtype == PARO_F32)
       static_cast<float*>(c.y)[at] = y;
@@ -128,34 +130,34 @@ __global__ __launch_bounds__(64 * W) void w8a8_column_kernel(const W8A8Call c) {
   }
 }
 
-template <int FM, bool GATED, int W, int S>
+template <int FM, Output KIND, int W, int S>
 hipError_t launch(const W8A8Call& c, hipStream_t st) {
-  constexpr int lds = W * S * (FM + (GATED ? 2 : 1)) * 2048;
+  constexpr int lds = W * S * (FM + (KIND == kGated ? 2 : 1)) * 2048;
   static_assert(lds <= 160 * 1024, "one CU's LDS");
-  const void* fn = reinterpret_cast<const void*>(&w8a8_column_kernel<FM, GATED, W, S>);
+  const void* fn = reinterpret_cast<const void*>(&w8a8_column_kernel<FM, KIND, W, S>);
   if (lds > 64 * 1024)
     if (hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds)) return e;
-  hipLaunchKernelGGL((w8a8_column_kernel<FM, GATED, W, S>), dim3((c.N + 15) / 16), dim3(64 * W), lds, st, c);
+  hipLaunchKernelGGL((w8a8_column_kernel<FM, KIND, W, S>), dim3((c.N + 15) / 16), dim3(64 * W), lds, st, c);
   return hipGetLastError();
 }
 
 // At most one workgroup per CU: eight waves of two stages (as many as fit of the widest). More: four
 // waves, so that several workgroups share a CU. Measured: M = 8, 8960 -> 1536 7.0 us with eight waves,
 // 8.4 with four; M = 16, gated 4096 -> 14336 26.8 and 23.3 us.
-template <int FM, bool GATED>
+template <int FM, Output KIND>
 hipError_t launch_waves(const W8A8Call& c, hipStream_t st) {
-  if ((c.N + 15) / 16 > 256) return launch<FM, GATED, 4, 2>(c, st);
-  if constexpr (FM == 4 && GATED)
-    return launch<FM, GATED, 4, 3>(c, st);
+  if ((c.N + 15) / 16 > 256) return launch<FM, KIND, 4, 2>(c, st);
+  if constexpr (FM == 4 && KIND == kGated)
+    return launch<FM, KIND, 4, 3>(c, st);
   else
-    return launch<FM, GATED, 8, 2>(c, st);
+    return launch<FM, KIND, 8, 2>(c, st);
 }
 
-template <bool GATED>
+template <Output KIND>
 hipError_t launch_rows(const W8A8Call& c, hipStream_t st) {
-  if (c.M <= 16) return launch_waves<1, GATED>(c, st);
-  if (c.M <= 32) return launch_waves<2, GATED>(c, st);
-  return launch_waves<4, GATED>(c, st);
+  if (c.M <= 16) return launch_waves<1, KIND>(c, st);
+  if (c.M <= 32) return launch_waves<2, KIND>(c, st);
+  return launch_waves<4, KIND>(c, st);
 }
 
 }  // namespace
@@ -171,7 +173,7 @@ double w8a8_column_us(int M, int D, int N, bool gated) {
 }
 
 hipError_t launch_w8a8_column(const W8A8Call& c, hipStream_t st) {
-  return c.gated ? launch_rows<true>(c, st) : launch_rows<false>(c, st);
+  return c.epilogue ? launch_rows<kEpilogue>(c, st) : c.gated ? launch_rows<kGated>(c, st) : launch_rows<kPlain>(c, st);
 }
 
 }  // namespace paro

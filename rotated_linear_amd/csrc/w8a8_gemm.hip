@@ -80,8 +80,9 @@ struct Place {
 
 // Tile number `tile` (of tiles_m * tiles_n * splits): splits innermost, then groups of 4 tile rows
 // walked column by column, so that tiles worked on at the same time share rows of x and of w.
-template <class T, bool GATED>
+template <class T, Output KIND>
 __device__ inline Place place(const GemmArgs& a, int tile) {
+  constexpr bool GATED = KIND == kGated;
   Place p;
   p.split = tile % a.splits;
   tile /= a.splits;
@@ -115,6 +116,36 @@ __device__ inline void put4(char* at, const float (&v)[4]) {
   }
 }
 
+// Four neighbouring elements of type DT as they are stored.
+template <int DT>
+struct alignas(DT == PARO_F32 ? 16 : 8) Four {
+  uint32_t w[DT == PARO_F32 ? 4 : 2];
+};
+template <int DT>
+__device__ inline float element(const Four<DT>& f, int e) {
+  if constexpr (DT == PARO_F32) return __builtin_bit_cast(float, f.w[e]);
+  if constexpr (DT != PARO_F32) return from_bits16<DT>(e % 2 ? f.w[e / 2] >> 16 : f.w[e / 2] & 0xFFFFu);
+}
+// Elements n .. n + 3 of a row that starts at `row` and has N of them (0 past its end). Rows of a multiple of
+// four elements lie at multiples of their size.
+template <int DT>
+__device__ inline Four<DT> load4(const void* p, size_t row, int n, int N) {
+  Four<DT> f{};
+  if (N % 4 == 0) {
+    if (n < N) f = *reinterpret_cast<const Four<DT>*>(static_cast<const char*>(p) + (row + n) * (DT == PARO_F32 ? 4 : 2));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < N) {
+        if constexpr (DT == PARO_F32)
+          f.w[e] = static_cast<const uint32_t*>(p)[row + n + e];
+        else
+          f.w[e / 2] |= uint32_t(static_cast<const uint16_t*>(p)[row + n + e]) << (e % 2 * 16);
+      }
+  }
+  return f;
+}
+
 // Store one piece that the wave has put into buf: PR rows of PB bytes, 16 bytes a lane. dst: the
 // piece's first element; rows ld bytes apart; `rows` rows and `cols` elements of EB bytes exist.
 template <int EB, int EP, int PB, int PR>
@@ -144,11 +175,12 @@ __device__ inline void store_piece(const char* buf, char* dst, size_t ld, int ro
 
 // A wave's results: scaled (and gated) rows of y in type DT, or (PART) the int32 sums themselves.
 // A lane's column of a fragment is a row of y, its rows are columns of y, four at a time.
-template <class T, bool GATED, int DT, bool PART>
+template <class T, Output KIND, int DT, bool PART>
 __device__ inline void store_tile(const GemmArgs& a, const Place& p, const i32x4 (&acc)[T::FM][T::FN], char* smem,
                                   int wave) {
   const W8A8Call& c = a.c;
   const int lane = fresh_lane();
+  constexpr bool GATED = KIND == kGated;
   constexpr int EB = DT == PARO_F32 ? 4 : 2;
   constexpr bool G = GATED && !PART;
   constexpr int YF = G ? T::FN / 2 : T::FN;    // the wave's column fragments of the output,
@@ -206,9 +238,107 @@ __device__ inline void store_tile(const GemmArgs& a, const Place& p, const i32x4
   }
 }
 
-template <class T, bool GATED>
+// The same for a call with an epilogue. The residual is read as the lanes hold their sums, four columns of a row
+// each, a piece ahead of the one that is worked on. One copy of the activations serves every piece (unrolled over
+// the pieces they would not fit the instruction cache), so a piece's sums are first moved to registers of their own.
+template <class T, int DT>
+__device__ inline void store_tile_epilogue(const W8A8Call& c, const Place& p, const i32x4 (&acc)[T::FM][T::FN], char* smem, int wave) {
+  const int lane = fresh_lane();
+  constexpr int EB = DT == PARO_F32 ? 4 : 2;
+  constexpr int CF = T::FN < 4 / EB ? T::FN : 4 / EB;  // column and row fragments of a piece
+  constexpr int RF = T::PR / 16;
+  constexpr int ROW = T::FN / CF, PIECES = T::FM / RF * ROW;
+  const int wm = wave / T::WN, wn = wave % T::WN;
+  char* const buf = smem + T::OUT + wave * T::PR * T::EP;
+  const float* const sc = reinterpret_cast<const float*>(smem + T::SCALES);
+  const bool whole = c.N % (16 / EB) == 0;
+  const int mw = wm * T::FM * 16, nw = wn * T::FN * 16;  // the wave's first row and column in the tile
+  Four<DT> res[RF][CF], next[RF][CF];
+  // (only elements of y: in place of the residual, the others are another workgroup's to write)
+  auto fetch = [&](int piece) {
+#pragma unroll
+    for (int u = 0; u < RF; ++u)
+#pragma unroll
+      for (int k = 0; k < CF; ++k) {
+        const int m = p.m0 + mw + (piece / ROW * RF + u) * 16 + (lane & 15);
+        const int n = p.n0 + nw + (piece % ROW * CF + k) * 16 + 4 * (lane >> 4);
+        next[u][k] = m < c.M ? load4<DT>(c.residual, size_t(m) * c.N, n, c.N) : Four<DT>{};
+      }
+  };
+  if (c.residual) fetch(0);
+#pragma unroll 1
+  for (int piece = 0; piece < PIECES; ++piece) {
+    i32x4 sum[RF][CF];
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q)
+      if (q == piece) {  // uniform
+#pragma unroll
+        for (int u = 0; u < RF; ++u)
+#pragma unroll
+          for (int k = 0; k < CF; ++k) sum[u][k] = acc[q / ROW * RF + u][q % ROW * CF + k];
+      }
+    const int mf = mw + piece / ROW * RF * 16, nf = nw + piece % ROW * CF * 16;
+    Four<DT> bias[CF];
+    if (c.bias) {
+#pragma unroll
+      for (int k = 0; k < CF; ++k) bias[k] = load4<DT>(c.bias, 0, p.n0 + nf + k * 16 + 4 * (lane >> 4), c.N);
+    }
+    if (c.residual) {
+#pragma unroll
+      for (int u = 0; u < RF; ++u)
+#pragma unroll
+        for (int k = 0; k < CF; ++k) res[u][k] = next[u][k];
+      if (piece + 1 < PIECES) fetch(piece + 1);
+    }
+    float v[RF * CF * 4];
+#pragma unroll
+    for (int k = 0; k < CF; ++k) {
+      const float4 w4 = *reinterpret_cast<const float4*>(sc + T::XS + nf + k * 16 + 4 * (lane >> 4));
+      const float ws[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+      for (int u = 0; u < RF; ++u) {
+        const float xs = sc[mf + u * 16 + (lane & 15)];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float& o = v[(u * CF + k) * 4 + e];
+          o = scaled(sum[u][k][e], xs, ws[e]);
+          if (c.bias) o = plus(o, element<DT>(bias[k], e));
+        }
+      }
+    }
+    activate<DT>(v, c.act);
+#pragma unroll
+    for (int u = 0; u < RF; ++u)
+#pragma unroll
+      for (int k = 0; k < CF; ++k) {
+        float o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          o[e] = v[(u * CF + k) * 4 + e];
+          if (c.residual) o[e] = plus(o[e], element<DT>(res[u][k], e));
+        }
+        put4<DT>(buf + (u * 16 + (lane & 15)) * T::EP + (16 * k + 4 * (lane >> 4)) * EB, o);
+      }
+    // one wave's LDS accesses are carried out in order; the compiler keeps them in order too
+    asm volatile("" ::: "memory");
+    store_piece<EB, T::EP, CF * 16 * EB, T::PR>(buf, static_cast<char*>(c.y) + (size_t(p.m0 + mf) * c.N + p.n0 + nf) * EB,
+                                                size_t(c.N) * EB, c.M - p.m0 - mf, c.N - p.n0 - nf, whole, lane);
+    asm volatile("" ::: "memory");
+  }
+}
+
+template <class T, Output KIND, int DT>
+__device__ inline void store_outputs(const GemmArgs& a, const Place& p, const i32x4 (&acc)[T::FM][T::FN], char* smem, int wave) {
+  if constexpr (KIND == kEpilogue)
+    store_tile_epilogue<T, DT>(a.c, p, acc, smem, wave);
+  else
+    store_tile<T, KIND, DT, false>(a, p, acc, smem, wave);
+}
+
+template <class T, Output KIND>
 __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
+  constexpr bool GATED = KIND == kGated;
   const W8A8Call& c = a.c;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -227,7 +357,7 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
   // The loads run S stages ahead of the products and pass from one tile to the next without a
   // break: `ahead` is the tile they are in, step `at` of it.
   int ahead = tile, at = 0;
-  Place q = place<T, GATED>(a, ahead);
+  Place q = place<T, KIND>(a, ahead);
   uint32_t voff[T::LOADS];
   const char* src[T::LOADS];
   auto aim = [&]() {
@@ -260,7 +390,7 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
       if (ahead + stride < end) {
         ahead += stride;
         at = 0;
-        q = place<T, GATED>(a, ahead);
+        q = place<T, KIND>(a, ahead);
         aim();
       } else {
         at = q.steps - 1;
@@ -316,7 +446,7 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
   read_x(0, 0);
   uint32_t buf = 0;
   for (; tile < end; tile += stride) {
-    const Place p = place<T, GATED>(a, tile);
+    const Place p = place<T, KIND>(a, tile);
     i32x4 acc[T::FM][T::FN];
 #pragma unroll
     for (int i = 0; i < T::FM; ++i)
@@ -360,22 +490,35 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
     // with S steps or more the scales' loads were waited for at a later stage's barrier
     if (p.steps < T::S) stage_wait<0>();
     if (a.part)
-      store_tile<T, GATED, PARO_F32, true>(a, p, acc, smem, wave);
+      store_tile<T, KIND, PARO_F32, true>(a, p, acc, smem, wave);
     else if (c.ydtype == PARO_F32)
-      store_tile<T, GATED, PARO_F32, false>(a, p, acc, smem, wave);
+      store_outputs<T, KIND, PARO_F32>(a, p, acc, smem, wave);
     else if (c.ydtype == PARO_F16)
-      store_tile<T, GATED, PARO_F16, false>(a, p, acc, smem, wave);
+      store_outputs<T, KIND, PARO_F16>(a, p, acc, smem, wave);
     else
-      store_tile<T, GATED, PARO_BF16, false>(a, p, acc, smem, wave);
+      store_outputs<T, KIND, PARO_BF16>(a, p, acc, smem, wave);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads past the last stage land before the LDS is given up
 }
 
+// V elements from element i on (V = 4: i a multiple of 4) in float32.
+template <int DT, int V>
+__device__ inline void load_elements(const void* p, size_t i, float (&v)[V]) {
+  if constexpr (V == 4) {
+    const Four<DT> f = *reinterpret_cast<const Four<DT>*>(static_cast<const char*>(p) + i * (DT == PARO_F32 ? 4 : 2));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = element<DT>(f, e);
+  } else {
+    v[0] = load_element(p, i, DT);
+  }
+}
+
 // y from the S partial sums of a split reduction: a thread takes V columns of a row (their sums of
 // every split in flight together), the integer sums are exact in any order.
-template <int V, bool GATED, int DT>
+template <int V, Output KIND, int DT>
 __global__ __launch_bounds__(256) void reduce_kernel(const W8A8Call c, const int* part, int splits) {
   using IV = int __attribute__((ext_vector_type(V)));
+  constexpr bool GATED = KIND == kGated;
   const size_t rows = size_t(c.N) * (GATED ? 2 : 1), plane = size_t(c.M) * rows;
   const size_t per_row = c.N / V, total = per_row * c.M;
   for (size_t t = size_t(blockIdx.x) * 256 + threadIdx.x; t < total; t += size_t(gridDim.x) * 256) {
@@ -395,6 +538,20 @@ __global__ __launch_bounds__(256) void reduce_kernel(const W8A8Call c, const int
       v[e] = scaled(g[e], xs, c.ws[n + e]);
       if constexpr (GATED) v[e] = silu_mul<DT>(v[e], scaled(u[e], xs, c.ws[size_t(c.N) + n + e]));
     }
+    if constexpr (KIND == kEpilogue) {
+      float w[V];
+      if (c.bias) {
+        load_elements<DT, V>(c.bias, n, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = plus(v[e], w[e]);
+      }
+      activate<DT>(v, c.act);
+      if (c.residual) {
+        load_elements<DT, V>(c.residual, m * c.N + n, w);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = plus(v[e], w[e]);
+      }
+    }
     if constexpr (V == 4) {
       put4<DT>(static_cast<char*>(c.y) + (m * c.N + n) * (DT == PARO_F32 ? 4 : 2), v);
     } else if constexpr (DT == PARO_F32) {
@@ -405,7 +562,7 @@ __global__ __launch_bounds__(256) void reduce_kernel(const W8A8Call c, const int
   }
 }
 
-template <bool GATED>
+template <Output KIND>
 hipError_t launch_reduce(const W8A8Call& c, const int* part, int splits, hipStream_t st) {
   const bool four = c.N % 4 == 0;
   const size_t total = size_t(c.M) * (c.N / (four ? 4 : 1));
@@ -414,9 +571,9 @@ hipError_t launch_reduce(const W8A8Call& c, const int* part, int splits, hipStre
     hipLaunchKernelGGL(kernel, grid, dim3(256), 0, st, c, part, splits);
     return hipGetLastError();
   };
-  if (c.ydtype == PARO_F32) return go(four ? reduce_kernel<4, GATED, PARO_F32> : reduce_kernel<1, GATED, PARO_F32>);
-  if (c.ydtype == PARO_F16) return go(four ? reduce_kernel<4, GATED, PARO_F16> : reduce_kernel<1, GATED, PARO_F16>);
-  return go(four ? reduce_kernel<4, GATED, PARO_BF16> : reduce_kernel<1, GATED, PARO_BF16>);
+  if (c.ydtype == PARO_F32) return go(four ? reduce_kernel<4, KIND, PARO_F32> : reduce_kernel<1, KIND, PARO_F32>);
+  if (c.ydtype == PARO_F16) return go(four ? reduce_kernel<4, KIND, PARO_F16> : reduce_kernel<1, KIND, PARO_F16>);
+  return go(four ? reduce_kernel<4, KIND, PARO_BF16> : reduce_kernel<1, KIND, PARO_BF16>);
 }
 
 template <class T>
@@ -424,23 +581,23 @@ constexpr TilingQ8 tiling() {
   return TilingQ8{T::BM, T::BN, kCUs * int(160 * 1024 / T::LDS)};
 }
 
-template <class T, bool GATED>
+template <class T, Output KIND>
 hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st) {
   GemmArgs a;
   a.c = c;
   a.tiles_m = (c.M + T::BM - 1) / T::BM;
-  const int yn = GATED ? T::BN / 2 : T::BN;
+  const int yn = KIND == kGated ? T::BN / 2 : T::BN;
   a.tiles_n = (c.N + yn - 1) / yn;
   const int steps = c.D / T::BK;
   a.steps_per_split = (steps + splits - 1) / splits;
   a.splits = (steps + a.steps_per_split - 1) / a.steps_per_split;  // every split has steps
   a.part = a.splits > 1 ? part : nullptr;
-  const void* fn = reinterpret_cast<const void*>(&w8a8_gemm_kernel<T, GATED>);
+  const void* fn = reinterpret_cast<const void*>(&w8a8_gemm_kernel<T, KIND>);
   if (hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS)) return e;
   const long total = long(a.tiles_m) * a.tiles_n * a.splits;
-  hipLaunchKernelGGL((w8a8_gemm_kernel<T, GATED>), dim3(unsigned(std::min<long>(total, tiling<T>().workgroups))), dim3(T::NT), T::LDS, st, a);
+  hipLaunchKernelGGL((w8a8_gemm_kernel<T, KIND>), dim3(unsigned(std::min<long>(total, tiling<T>().workgroups))), dim3(T::NT), T::LDS, st, a);
   if (hipError_t e = hipGetLastError()) return e;
-  return a.part ? launch_reduce<GATED>(c, part, a.splits, st) : hipSuccess;
+  return a.part ? launch_reduce<KIND>(c, part, a.splits, st) : hipSuccess;
 }
 
 // The tilings: waves side by side in rows and columns, stages in LDS. Eight waves where the tile has
@@ -521,23 +678,25 @@ GemmPlanQ8 plan_gemm_w8a8(int M, int D, int N, bool gated) {
 
 namespace {
 
-template <bool GATED>
+template <Output KIND>
 hipError_t launch_plan(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStream_t st) {
   switch (p.tile) {
-    case 0: return launch_tile<T256, GATED>(c, part, p.splits, st);
-    case 1: return launch_tile<T256x128, GATED>(c, part, p.splits, st);
-    case 2: return launch_tile<T128, GATED>(c, part, p.splits, st);
-    case 3: return launch_tile<T128Two, GATED>(c, part, p.splits, st);
-    case 4: return launch_tile<T128x64, GATED>(c, part, p.splits, st);
-    case 5: return launch_tile<T64, GATED>(c, part, p.splits, st);
-    default: return launch_tile<T32, GATED>(c, part, p.splits, st);
+    case 0: return launch_tile<T256, KIND>(c, part, p.splits, st);
+    case 1: return launch_tile<T256x128, KIND>(c, part, p.splits, st);
+    case 2: return launch_tile<T128, KIND>(c, part, p.splits, st);
+    case 3: return launch_tile<T128Two, KIND>(c, part, p.splits, st);
+    case 4: return launch_tile<T128x64, KIND>(c, part, p.splits, st);
+    case 5: return launch_tile<T64, KIND>(c, part, p.splits, st);
+    default: return launch_tile<T32, KIND>(c, part, p.splits, st);
   }
 }
 
 }  // namespace
 
 hipError_t launch_w8a8_gemm(const W8A8Call& c, const GemmPlanQ8& p, int* part, hipStream_t st) {
-  return c.gated ? launch_plan<true>(c, p, part, st) : launch_plan<false>(c, p, part, st);
+  return c.epilogue ? launch_plan<kEpilogue>(c, p, part, st)
+         : c.gated  ? launch_plan<kGated>(c, p, part, st)
+                    : launch_plan<kPlain>(c, p, part, st);
 }
 
 }  // namespace paro

@@ -14,8 +14,9 @@ constexpr int kRing = 4;  // steps in flight per wave
 // products of equal parts, P diagonal blocks, add up to the result, and a wave-wide load of w reads
 // 64 P consecutive bytes of R rows. The matrix instructions idle anyway; wide pieces of a row and
 // small tiles (so that narrow layers fill the GPU too) are what a short x gains by it.
-template <int P, int WT, int W, bool GATED>
+template <int P, int WT, int W, Output KIND>
 __global__ __launch_bounds__(64 * W) void w8a8_stream_kernel(const W8A8Call c) {
+  constexpr bool GATED = KIND == kGated;
   constexpr int R = 16 / P;
   constexpr int YT = GATED ? WT / 2 : WT;  // tiles of y's columns
   __shared__ i32x4 red[W][WT][64];
@@ -96,6 +97,7 @@ __global__ __launch_bounds__(64 * W) void w8a8_stream_kernel(const W8A8Call c) {
       const float u = scaled(sum(t + YT), xs, c.ws[size_t(c.N) + n]);
       v = c.ydtype == PARO_F32 ? silu_mul<PARO_F32>(v, u) : silu_mul<PARO_F16>(v, u);
     }
+    if constexpr (KIND == kEpilogue) v = epilogue(c, v, m, n);
     const size_t at = size_t(m) * c.N + n;
     if (c.ydtype == PARO_F32)
       static_cast<float*>(c.y)[at] = v;
@@ -104,25 +106,25 @@ __global__ __launch_bounds__(64 * W) void w8a8_stream_kernel(const W8A8Call c) {
   }
 }
 
-template <int P, int WT, int W, bool GATED>
+template <int P, int WT, int W, Output KIND>
 hipError_t launch(const W8A8Call& c, hipStream_t st) {
-  constexpr int cols = 16 / P * (GATED ? WT / 2 : WT);
-  hipLaunchKernelGGL((w8a8_stream_kernel<P, WT, W, GATED>), dim3((c.N + cols - 1) / cols), dim3(64 * W), 0, st, c);
+  constexpr int cols = 16 / P * (KIND == kGated ? WT / 2 : WT);
+  hipLaunchKernelGGL((w8a8_stream_kernel<P, WT, W, KIND>), dim3((c.N + cols - 1) / cols), dim3(64 * W), 0, st, c);
   return hipGetLastError();
 }
 
 // Eight waves where there is at most one workgroup per CU, else four. Measured on MI355X, cold
 // weights: M = 1, 8960 -> 1536 (192 workgroups) 5.0 us with eight, 5.8 with four; gated 4096 -> 14336
 // (3584) 20.3 and 18.9 us (6.2 TB/s).
-template <int P, bool GATED>
+template <int P, Output KIND>
 hipError_t launch_waves(const W8A8Call& c, hipStream_t st) {
-  constexpr int cols = 16 / P * (GATED ? 1 : 2);
-  return (c.N + cols - 1) / cols <= 256 ? launch<P, 2, 8, GATED>(c, st) : launch<P, 2, 4, GATED>(c, st);
+  constexpr int cols = 16 / P * (KIND == kGated ? 1 : 2);
+  return (c.N + cols - 1) / cols <= 256 ? launch<P, 2, 8, KIND>(c, st) : launch<P, 2, 4, KIND>(c, st);
 }
 
-template <bool GATED>
+template <Output KIND>
 hipError_t launch_rows(const W8A8Call& c, hipStream_t st) {
-  return c.D % 256 == 0 ? launch_waves<4, GATED>(c, st) : launch_waves<2, GATED>(c, st);
+  return c.D % 256 == 0 ? launch_waves<4, KIND>(c, st) : launch_waves<2, KIND>(c, st);
 }
 
 }  // namespace
@@ -135,7 +137,7 @@ hipError_t launch_rows(const W8A8Call& c, hipStream_t st) {
 bool w8a8_stream_takes(int M, int N) { return M <= 2 && N <= 1 << 24; }
 
 hipError_t launch_w8a8_stream(const W8A8Call& c, hipStream_t st) {
-  return c.gated ? launch_rows<true>(c, st) : launch_rows<false>(c, st);
+  return c.epilogue ? launch_rows<kEpilogue>(c, st) : c.gated ? launch_rows<kGated>(c, st) : launch_rows<kPlain>(c, st);
 }
 
 }  // namespace paro
