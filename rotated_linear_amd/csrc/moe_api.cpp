@@ -14,7 +14,7 @@ bool good_sizes(int M, int E, int top_k, bool routed) {
 
 // A workspace's sections, each at a multiple of 256 bytes.
 struct Layout {
-  size_t logits, x, a, a_rotated, count, active, token, weight, total;
+  size_t logits, x, a, a_rotated, part, units, unit, slot, total;
 };
 Layout layout(int M, int D, int F, int E, int top_k) {
   Layout l;
@@ -24,15 +24,16 @@ Layout layout(int M, int D, int F, int E, int top_k) {
     at += align256(bytes);
     return here;
   };
-  const size_t slots = size_t(M) * top_k;
+  const size_t pairs = size_t(M) * top_k;
   l.logits = take(size_t(M) * E * 8);
   l.x = take(size_t(M) * D * 2);
-  l.a = take(slots * F * 2);
-  l.a_rotated = take(slots * F * 2);
-  l.count = take(4);
-  l.active = take(size_t(E) * sizeof(MoeActive));
-  l.token = take(slots * 4);
-  l.weight = take(slots * 4);
+  l.a = take(pairs * F * 2);
+  l.a_rotated = take(pairs * F * 2);
+  const int splits = moe_down_splits(M, D, F, E, top_k);
+  l.part = take(splits > 1 ? size_t(splits) * M * D * 4 : 0);
+  l.units = take(4);
+  l.unit = take(size_t(moe_units_max(M, E, top_k)) * sizeof(MoeUnit));
+  l.slot = take(pairs * sizeof(MoeSlot));
   l.total = at;
   return l;
 }
@@ -97,10 +98,11 @@ paro_status experts(int M, int D, int F, int E, int top_k, const void* x, const 
   c.dn_zr = static_cast<const uint16_t*>(down->zeros);
   c.a = reinterpret_cast<uint16_t*>(base + l.a);
   c.a_down = c.a;
+  c.a_nibble_order = rot_a == nullptr;
+  c.part = reinterpret_cast<float*>(base + l.part);
+  c.t = MoeTables{reinterpret_cast<int*>(base + l.units), reinterpret_cast<MoeUnit*>(base + l.unit), reinterpret_cast<MoeSlot*>(base + l.slot)};
   c.y = y;
   c.ydtype = ydtype;
-  c.t = MoeTables{reinterpret_cast<int*>(base + l.count), reinterpret_cast<MoeActive*>(base + l.active),
-                  reinterpret_cast<int*>(base + l.token), reinterpret_cast<float*>(base + l.weight)};
   const hipStream_t st = as_stream(stream);
   hipError_t e = hipSuccess;
   if (r) {
@@ -113,14 +115,15 @@ paro_status experts(int M, int D, int F, int E, int top_k, const void* x, const 
   }
   if (e == hipSuccess && rot_x) {
     uint16_t* const xr = reinterpret_cast<uint16_t*>(base + l.x);
-    e = launch_rotate(rx, M, c.x, xr, false, st);
+    e = launch_rotate(rx, M, c.x, xr, true, st);
     c.x = xr;
+    c.x_nibble_order = true;
   }
   if (e == hipSuccess) e = launch_moe_gate_up(c, st);
   if (e == hipSuccess && rot_a) {
-    // (all the slots there may be: those that have no pair hold what they held, and no product reads them)
+    // (every row there may be: those of pairs without an expert hold what they held, and no product reads them)
     uint16_t* const ar = reinterpret_cast<uint16_t*>(base + l.a_rotated);
-    e = launch_rotate(ra, M * top_k, c.a, ar, false, st);
+    e = launch_rotate(ra, M * top_k, c.a, ar, true, st);
     c.a_down = ar;
   }
   if (e == hipSuccess) e = launch_moe_down(c, st);

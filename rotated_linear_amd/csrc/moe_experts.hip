@@ -8,143 +8,444 @@
 namespace paro {
 namespace {
 
-constexpr int kMaxM = PARO_MOE_MAX_M;
-constexpr int kFrags = kMaxM / 16;  // 16-row fragments of an expert's tokens
+constexpr int kCUs = 256;
 
-__device__ inline _Float16 as_half(uint16_t v) { return __builtin_bit_cast(_Float16, v); }
+// 128 channels (a group) of 16 weight rows are a contiguous kilobyte: a lane's 16 bytes are row lane & 15, channels
+// 32 (lane >> 4) on. The same channels of 16 rows of x, 8-channel words in the order dequant_word gives them:
+struct Rows {
+  h8 v[4];
+};
 
-// 16 weight rows times 128 channels: a lane's 16 bytes (row lane & 15, channels 32 (lane >> 4) on) with the row's scale and
-// zero, against the fragments of 16 rows in a: acc[f][row of a][row of w] += products.
-__device__ inline void group_product(const uint4& w, uint16_t scale, uint16_t zero, const h8 (&a)[kFrags][4], int frags, f4 (&acc)[kFrags]) {
-  const _Float16 z = as_half(zero);
+// sum[row of x][row of w] += the group's products. sz: the scale and, in the upper half, the zero of the lane's row.
+__device__ inline void group_product(const uint4& w, uint32_t sz, const Rows& a, f4& sum) {
+  const _Float16 z = __builtin_bit_cast(_Float16, uint16_t(sz >> 16));
   const _Float16 zl = -(static_cast<_Float16>(1024.0f) + z), zh = -(static_cast<_Float16>(64.0f) + z);
   const h2 zlo = {zl, zl}, zhi = {zh, zh};
   const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
-  h8 b[4];
+  f4 g = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) b[k] = dequant_word(wv[k], zlo, zhi, 0x000F000Fu, 0x00F000F0u, 0x64006400u);
-  const float s = static_cast<float>(as_half(scale));
+  for (int k = 0; k < 4; ++k)
+    g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[k], dequant_word(wv[k], zlo, zhi, 0x000F000Fu, 0x00F000F0u, 0x64006400u), g, 0, 0, 0);
+  const float s = static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(sz)));
 #pragma unroll
-  for (int f = 0; f < kFrags; ++f)
-    if (f < frags) {  // uniform
-      f4 g = {0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < 4; ++i) sum[i] = __builtin_fmaf(s, g[i], sum[i]);
+}
+
+// Scales and zeros come four groups at a time, 16 lanes to a group: a load for each group would cost the CU's load
+// path as much as the group's weights (gate and up of 4 tokens, 4096 -> 14336: 92 us against 54 without them). Here
+// every lane gets them all.
+__device__ inline void spread4(uint32_t v, uint32_t (&o)[4]) {
+  const auto halves = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // groups 0 1 0 1, groups 2 3 2 3
+  const auto lo = __builtin_amdgcn_permlane16_swap(halves[0], halves[0], false, false);
+  const auto hi = __builtin_amdgcn_permlane16_swap(halves[1], halves[1], false, false);
+  o[0] = lo[0];
+  o[1] = lo[1];
+  o[2] = hi[0];
+  o[3] = hi[1];
+}
+
+template <class T>
+using gptr = const T __attribute__((address_space(1)))*;
+
+// A load from a uniform address plus a lane's own 32-bit offset, with the address in scalar registers. (The compiler is
+// kept from hoisting the lane's part into 64-bit sums of its own, a pair of registers each: the address by the empty
+// statement here, the offset by opaque() in the block of the load.)
+template <class T>
+__device__ inline T at(const void* base, uint32_t off, int more = 0) {
+  uintptr_t p = reinterpret_cast<uintptr_t>(base);
+  asm volatile("" : "+s"(p));
+  return *(gptr<T>)((gptr<char>)p + off + more);
+}
+__device__ inline void opaque(uint32_t& off) { asm volatile("" : "+v"(off)); }
+using u4 = uint32_t __attribute__((ext_vector_type(4)));
+__device__ inline uint4 load_weights(const void* w, uint32_t& wo) {
+  opaque(wo);
+  return __builtin_bit_cast(uint4, at<u4>(w, wo));
+}
+__device__ inline void load_scales(uint32_t& scale, uint32_t& zero, const void* sp, const void* zp, uint32_t& so) {
+  opaque(so);
+  scale = at<uint16_t>(sp, so);
+  zero = at<uint16_t>(zp, so);
+}
+__device__ inline void load_rows(Rows& r, const void* base, uint32_t& off) {
+  opaque(off);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[f][k], b[k], g, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[f][i] = __builtin_fmaf(s, g[i], acc[f][i]);
+  for (int k = 0; k < 4; ++k) r.v[k] = at<h8>(base, off, k * 16);
+}
+
+// All that is computed up to here comes before whatever is loaded later.
+__device__ inline void settled(f4& v) { asm volatile("" : "+v"(v) : : "memory"); }
+
+// Workgroups go through the tiles (16 gate and 16 up rows of a unit's expert), unit by unit, each a run of them. W waves
+// share out the groups of channels: wave w has GW of them from group GW w on, whose part of the unit's tokens it keeps
+// in registers (GW = 0: any number, w, w + W, ..., read again for each tile). Weights come straight into a ring of
+// registers, R groups ahead, from tile to tile without a break: a tile's gate rows, then its up rows. Every kPark
+// tiles, and where the unit ends, the waves' sums meet in LDS.
+constexpr int kPark = 4;
+template <int W, int GW>
+__global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
+  constexpr int R = GW == 1 ? 2 : GW == 3 ? 6 : 4;
+  constexpr int S = GW ? 2 * GW : R;  // steps of a tile
+  static_assert(S % R == 0, "a step's slot and its group are fixed");
+  __shared__ f4 red[kPark][2][W][64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), nl = lane & 15, h = lane >> 4;
+  const int G = c.D / PARO_GROUP, per_unit = c.F / 16;
+  const int total = *c.t.units * per_unit;
+  const int begin = int(size_t(total) * blockIdx.x / gridDim.x), end = int(size_t(total) * (blockIdx.x + 1) / gridDim.x);
+  if (begin == end) return;
+  auto group = [&](int i) { return min(GW ? wave * GW + i : wave + W * i, G - 1); };  // past the last one that one again
+  uint32_t wo = nl * 64 + h * 16;                                  // this lane's part of a group of 16 rows,
+  uint32_t so = (nl * G + (GW ? group(GW == 1 ? 0 : GW == 2 ? h & 1 : min(h, GW - 1)) : 0)) * 2;  // and its scale and zero
+  const size_t wup = size_t(c.F) * (c.D / 2), sup = size_t(c.F) * G * 2;  // from a gate row to its up row
+  // the tile that is loaded: its unit, its place in it, its first gate row's addresses
+  int lu = begin / per_unit, lt = begin - lu * per_unit, left = end - begin;
+  const char *wp, *sp, *zp;
+  auto aim = [&]() {
+    const size_t row = size_t(__builtin_amdgcn_readfirstlane(c.t.unit[lu].expert)) * 2 * c.F + lt * 16;
+    wp = reinterpret_cast<const char*>(c.gu_qw) + row * (c.D / 2);
+    sp = reinterpret_cast<const char*>(c.gu_sc) + row * G * 2;
+    zp = reinterpret_cast<const char*>(c.gu_zr) + row * G * 2;
+  };
+  aim();
+  auto next_tile = [&]() {  // past the end the last tile again
+    if (--left > 0) {
+      wp += size_t(8) * c.D;
+      sp += size_t(32) * G;
+      zp += size_t(32) * G;
+      if (++lt == per_unit) {
+        lt = 0;
+        ++lu;
+        aim();
+      }
     }
-}
-
-// A lane's part of a row's 128 channels, from its first one on.
-__device__ inline void load_rows(const uint16_t* p, h8 (&a)[4]) {
+  };
+  uint4 w[R];
+  uint32_t scale[GW ? 2 : R], zero[GW ? 2 : R], sz[4];
+  auto issue = [&](int q, int half, int i) {
+    const int g = group(i);
+    const size_t sa = (half ? sup : 0) + (GW ? 0 : uint32_t(g) * 2);
+    if (GW == 0 || i == 0) load_scales(scale[GW ? half : q], zero[GW ? half : q], sp + sa, zp + sa, so);
+    w[q] = load_weights(wp + (half ? wup : 0) + uint32_t(g) * 1024, wo);
+  };
+  auto spread = [&](int half) {
+    const uint32_t v = scale[half] | zero[half] << 16;
+    if constexpr (GW == 1) {
+      sz[0] = v;
+    } else if constexpr (GW == 2) {
+      const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+      sz[0] = r[0];
+      sz[1] = r[1];
+    } else {
+      spread4(v, sz);
+    }
+  };
+  // GW = 0: a step is a group's gate and up rows, in two slots of the ring, and a tile an even number of them
+  const int gw = ((G + W - 1) / W + 1) / 2 * 2;
+  int li = 0;
+  auto issue_both = [&](int p) {
+    issue(2 * p, 0, li);
+    issue(2 * p + 1, 1, li);
+    if (++li == gw) {
+      li = 0;
+      next_tile();
+    }
+  };
+  if constexpr (GW > 0) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) a[k] = decode_order(*reinterpret_cast<const h8*>(p + k * 8));
-}
-
-// A workgroup has 16 gate and 16 up rows of one expert; its waves take the groups of channels in turn.
-__global__ __launch_bounds__(256) void gate_up_kernel(const MoeCall c) {
-  __shared__ f4 red[4][2][kFrags][64];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nl = lane & 15, h = lane >> 4;
-  if (int(blockIdx.y) >= *c.t.active_count) return;
-  const MoeActive ex = c.t.active[blockIdx.y];
-  const int G = c.D / PARO_GROUP, frags = (ex.count + 15) / 16;
-  const uint16_t* xp[kFrags];
-#pragma unroll
-  for (int f = 0; f < kFrags; ++f) xp[f] = c.x + size_t(c.t.slot_token[ex.first + min(f * 16 + nl, ex.count - 1)]) * c.D + h * 32;
-  const size_t row = size_t(ex.expert) * 2 * c.F + blockIdx.x * 16 + nl;  // this lane's gate row; its up row is F further on
-  const uint8_t* const wp = c.gu_qw + qw_row_offset<size_t>(row, c.D) + h * 16;
-  const size_t up = size_t(c.F) * (c.D / 2), ups = size_t(c.F) * G;
-  f4 acc[2][kFrags] = {};
-  for (int g = wave; g < G; g += 4) {
-    h8 a[kFrags][4];
-#pragma unroll
-    for (int f = 0; f < kFrags; ++f)
-      if (f < frags) load_rows(xp[f] + g * PARO_GROUP, a[f]);
-    const size_t si = row * G + g;
-    group_product(*reinterpret_cast<const uint4*>(wp + size_t(g) * 1024), c.gu_sc[si], c.gu_zr[si], a, frags, acc[0]);
-    group_product(*reinterpret_cast<const uint4*>(wp + up + size_t(g) * 1024), c.gu_sc[si + ups], c.gu_zr[si + ups], a, frags, acc[1]);
+    for (int q = 0; q < R; ++q) issue(q, q / GW, q % GW);
+  } else {
+    issue_both(0);
+    issue_both(1);
   }
-#pragma unroll
-  for (int j = 0; j < 2; ++j)
-#pragma unroll
-    for (int f = 0; f < kFrags; ++f)
-      if (f < frags) red[wave][j][f][lane] = acc[j][f];
-  __syncthreads();
-  for (int o = tid; o < ex.count * 16; o += 256) {
-    const int m = o >> 4, n = o & 15, f = m >> 4, l = ((m & 15) >> 2) * 16 + n, i = m & 3;
-    float gate = 0, upv = 0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      gate += red[w][0][f][l][i];
-      upv += red[w][1][f][l][i];
-    }
-    const float v = gate / (1.0f + expf(-gate)) * upv;
-    c.a[size_t(ex.first + m) * c.F + blockIdx.x * 16 + n] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
-  }
-}
+  __builtin_amdgcn_sched_barrier(0);
 
-// A workgroup has 16 columns of y. Its waves share out the (expert, group) pairs, in order, each with sums of its own
-// for every token.
-__global__ __launch_bounds__(512) void down_kernel(const MoeCall c) {
-  __shared__ float sums[8][kMaxM][16];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nl = lane & 15, h = lane >> 4;
-  for (int i = lane; i < kMaxM * 16; i += 64) sums[wave][i / 16][i % 16] = 0;
-  const int G = c.F / PARO_GROUP, total = *c.t.active_count * G;
-  const int begin = int(size_t(total) * wave / 8), end = int(size_t(total) * (wave + 1) / 8);
-  int at = begin / G, g = begin % G;
-  for (int item = begin; item < end; ++at, g = 0) {
-    const MoeActive ex = c.t.active[at];
-    const int stop = min(G, g + end - item), frags = (ex.count + 15) / 16;
-    const uint16_t* ap[kFrags];
+  Rows a[GW ? GW : 2];
+  int unit = begin / per_unit, tile = begin - unit * per_unit, first = 0, count = 0;
+  uint32_t xo = 0;
+  // a group of the unit's tokens; past the last one zeros, so that its products are
+  auto rows = [&](int q, int i) { load_rows(a[q], c.x + size_t(group(i)) * PARO_GROUP, xo); };
+  auto settle = [&](int q, int i) {
+    const bool in = (GW ? wave * GW + i : wave + W * i) < G;
 #pragma unroll
-    for (int f = 0; f < kFrags; ++f) ap[f] = c.a_down + size_t(ex.first + min(f * 16 + nl, ex.count - 1)) * c.F + h * 32;
-    const size_t row = size_t(ex.expert) * c.D + blockIdx.x * 16 + nl;
-    const uint8_t* const wp = c.dn_qw + qw_row_offset<size_t>(row, c.F) + h * 16;
-    f4 acc[kFrags] = {};
-    item += stop - g;
-    for (; g < stop; ++g) {
-      h8 a[kFrags][4];
-#pragma unroll
-      for (int f = 0; f < kFrags; ++f)
-        if (f < frags) load_rows(ap[f] + g * PARO_GROUP, a[f]);
-      group_product(*reinterpret_cast<const uint4*>(wp + size_t(g) * 1024), c.dn_sc[row * G + g], c.dn_zr[row * G + g], a, frags, acc);
+    for (int k = 0; k < 4; ++k) {
+      const u4 v = __builtin_bit_cast(u4, c.x_nibble_order ? a[q].v[k] : decode_order(a[q].v[k]));
+      a[q].v[k] = __builtin_bit_cast(h8, in ? v : u4{0u, 0u, 0u, 0u});
     }
+  };
+  auto tokens = [&]() {
+    first = __builtin_amdgcn_readfirstlane(c.t.unit[unit].first);
+    count = __builtin_amdgcn_readfirstlane(c.t.unit[unit].count);
+    xo = uint32_t(c.t.slot[first + min(nl, count - 1)].token) * uint32_t(c.D) * 2 + h * 64;
+    if constexpr (GW > 0) {
 #pragma unroll
-    for (int f = 0; f < kFrags; ++f)
+      for (int i = 0; i < GW; ++i) rows(i, i);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = f * 16 + 4 * h + i;
-        if (r < ex.count) {
-          // (an expert has a token once: no two lanes meet)
-          float& s = sums[wave][c.t.slot_token[ex.first + r]][nl];
-          s = __builtin_fmaf(c.t.slot_weight[ex.first + r], acc[f][i], s);
+      for (int i = 0; i < GW; ++i) settle(i, i);
+    } else {
+      rows(0, 0);
+      rows(1, 1);
+    }
+  };
+  tokens();
+  f4 acc[2] = {};
+  int parked = 0;
+  auto park = [&](int half) {
+    red[parked][half][wave][lane] = acc[half];
+    acc[half] = f4{0.f, 0.f, 0.f, 0.f};
+  };
+  for (int t = begin;;) {
+    if constexpr (GW > 0) {
+#pragma unroll
+      for (int s = 0; s < S; ++s) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (s % GW == 0) spread(s / GW);
+        group_product(w[s % R], sz[s % GW], a[s % GW], acc[s / GW]);
+        settled(acc[s / GW]);
+        if (s % GW == GW - 1) park(s / GW);
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + R == S) next_tile();
+        issue(s % R, (s + R) % S / GW, (s + R) % GW);
+      }
+    } else {
+      for (int i = 0; i < gw; i += 2) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          __builtin_amdgcn_sched_barrier(0);
+          settle(p, i + p);
+          group_product(w[2 * p], scale[2 * p] | zero[2 * p] << 16, a[p], acc[0]);
+          group_product(w[2 * p + 1], scale[2 * p + 1] | zero[2 * p + 1] << 16, a[p], acc[1]);
+          settled(acc[0]);
+          settled(acc[1]);
+          __builtin_amdgcn_sched_barrier(0);
+          issue_both(p);
+          rows(p, i + p + 2 < gw ? i + p + 2 : i + p + 2 - gw);
         }
       }
-  }
-  __syncthreads();
-  for (int o = tid; o < c.M * 16; o += 512) {
-    const int m = o >> 4, n = o & 15;
-    float v = 0;
+      park(0);
+      park(1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    ++t;
+    ++tile;
+    ++parked;
+    if (parked < kPark && tile < per_unit && t < end) continue;
+    __syncthreads();
+    for (int o = tid; o < parked * 256; o += 64 * W) {
+      const int col = o & 15, m = o >> 4 & 15, j = o >> 8, l = (m >> 2) * 16 + col, i = m & 3;
+      if (m >= count) continue;
+      float gate = 0, upv = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += sums[w][m][n];
-    const size_t i = size_t(m) * c.D + blockIdx.x * 16 + n;
-    if (c.ydtype == PARO_F32)
-      static_cast<float*>(c.y)[i] = v;
-    else
-      static_cast<_Float16*>(c.y)[i] = static_cast<_Float16>(v);
+      for (int v = 0; v < W; ++v) {
+        gate += red[j][0][v][l][i];
+        upv += red[j][1][v][l][i];
+      }
+      const float v = gate / (1.0f + expf(-gate)) * upv;
+      const int to = c.a_nibble_order ? (col & 8) | (col & 3) << 1 | (col >> 2 & 1) : col;
+      c.a[size_t(c.t.slot[first + m].pair) * c.F + (tile - parked + j) * 16 + to] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+    }
+    if (t == end) break;
+    parked = 0;
+    if (tile == per_unit) {
+      tile = 0;
+      ++unit;
+      tokens();
+    }
+    __syncthreads();  // the sums have been read
   }
 }
 
-}  // namespace
+struct DownArgs {
+  MoeCall c;
+  int splits;
+};
 
-hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st) {
-  const dim3 grid(unsigned(c.F / 16), unsigned(std::min(c.E, c.M * c.top_k)));
-  hipLaunchKernelGGL(gate_up_kernel, grid, dim3(256), 0, st, c);
+// A workgroup has T times 16 columns of y and its share of the items, an item being four groups of a unit: the items in
+// order are cut into splits * W equal runs, one for each wave. A wave keeps sums of its own for every token in LDS, to
+// which it adds an expert's products times the tokens' weights where it leaves the expert. R groups are in flight.
+template <int W, int T, int R>
+__global__ __launch_bounds__(64 * W, 4) void down_kernel(const DownArgs args) {
+  static_assert(R == 2 || R == 4, "a group's slot is fixed");
+  extern __shared__ __attribute__((aligned(16))) char smem[];  // float [W][M][16 T], then the tables
+  const MoeCall& c = args.c;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), nl = lane & 15, h = lane >> 4;
+  const int pairs = c.M * c.top_k, tile = blockIdx.x / args.splits, split = blockIdx.x - tile * args.splits;
+  float* const all = reinterpret_cast<float*>(smem);
+  float* const sums = all + wave * c.M * 16 * T;
+  MoeSlot* const slot = reinterpret_cast<MoeSlot*>(all + W * c.M * 16 * T);
+  MoeUnit* const unit = reinterpret_cast<MoeUnit*>(slot + pairs);
+  const int units = *c.t.units;
+  for (int i = tid; i < pairs; i += 64 * W) slot[i] = c.t.slot[i];  // (those past the last one are not used)
+  for (int i = tid; i < units; i += 64 * W) unit[i] = c.t.unit[i];
+  for (int i = lane; i < c.M * 16 * T; i += 64) sums[i] = 0;
+  __syncthreads();
+  const int G = c.F / PARO_GROUP, Q = (G + 3) / 4, total = units * Q, runs = args.splits * W, run = split * W + wave;
+  const int begin = int(size_t(total) * run / runs), end = int(size_t(total) * (run + 1) / runs);
+  uint32_t wo = nl * 64 + h * 16, so = 0, ao = 0;  // this lane's part of a group of 16 rows, its scale and zero, its row of a
+  f4 acc[T] = {};
+  uint4 w[R][T];
+  Rows a[R];
+  uint32_t scale[T], zero[T], sz[T][4];
+  // the item that is loaded next: its unit, four groups and addresses; and the one that is used next
+  int lu = begin / Q, lq = begin - lu * Q, uu = lu, uq = lq, left = end - begin;
+  const char *wp = nullptr, *sp = nullptr, *zp = nullptr;
+  auto aim = [&]() {  // (no global access: the wait counts stay exact)
+    const MoeUnit k = unit[lu];
+    ao = uint32_t(slot[k.first + min(nl, k.count - 1)].pair) * uint32_t(c.F) * 2 + h * 64;
+    const size_t row = size_t(__builtin_amdgcn_readfirstlane(k.expert)) * c.D + tile * 16 * T;
+    wp = reinterpret_cast<const char*>(c.dn_qw) + row * (c.F / 2);
+    sp = reinterpret_cast<const char*>(c.dn_sc) + row * G * 2;
+    zp = reinterpret_cast<const char*>(c.dn_zr) + row * G * 2;
+  };
+  auto advance = [&]() {  // past the end the last item again
+    if (--left > 0 && ++lq == Q) {
+      lq = 0;
+      ++lu;
+      aim();
+    }
+  };
+  auto load = [&](int q, int p) {  // the item's group p; past the last one that one again
+    if (p == 0) {
+      so = (nl * G + min(4 * lq + h, G - 1)) * 2;
+#pragma unroll
+      for (int t = 0; t < T; ++t) load_scales(scale[t], zero[t], sp + size_t(t) * 32 * G, zp + size_t(t) * 32 * G, so);
+    }
+    const uint32_t g = min(4 * lq + p, G - 1);
+#pragma unroll
+    for (int t = 0; t < T; ++t) w[q][t] = load_weights(wp + size_t(t) * 8 * c.F + g * 1024, wo);
+    load_rows(a[q], c.a_down + g * PARO_GROUP, ao);
+  };
+  if (begin < end) {
+    aim();
+#pragma unroll
+    for (int q = 0; q < R; ++q) load(q, q);
+    for (int n = end - begin; n > 0; --n) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (p == 0) {
+#pragma unroll
+          for (int t = 0; t < T; ++t) spread4(scale[t] | zero[t] << 16, sz[t]);
+        }
+        if (p == 0 || 4 * uq + p < G) {  // uniform
+#pragma unroll
+          for (int t = 0; t < T; ++t) {
+            group_product(w[p % R][t], sz[t][p], a[p % R], acc[t]);
+            settled(acc[t]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (p + R == 4) advance();
+        load(p % R, (p + R) % 4);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (++uq == Q || n == 1) {
+        const MoeUnit k = unit[uu];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 4 * h + i;
+          if (r < k.count) {
+            // (an expert has a token once: no two lanes meet)
+            const MoeSlot o = slot[k.first + r];
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+              float& v = sums[(o.token * T + t) * 16 + nl];
+              v = __builtin_fmaf(o.weight, acc[t][i], v);
+            }
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
+        uq = 0;
+        ++uu;
+      }
+    }
+  }
+  __syncthreads();
+  for (int o = tid; o < c.M * 16 * T; o += 64 * W) {
+    const int m = o / (16 * T), n = o % (16 * T);
+    float v = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v += all[i * c.M * 16 * T + o];
+    const size_t to = size_t(m) * c.D + tile * 16 * T + n;
+    if (args.splits > 1)
+      c.part[size_t(split) * c.M * c.D + to] = v;
+    else if (c.ydtype == PARO_F32)
+      static_cast<float*>(c.y)[to] = v;
+    else
+      static_cast<_Float16*>(c.y)[to] = static_cast<_Float16>(v);
+  }
+}
+
+// y from the partial sums of the splits, in their order; 4 values a thread.
+__global__ __launch_bounds__(256) void sum_kernel(const float* part, int splits, int total, void* y, int ydtype) {
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= total) return;
+  f4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) v += *reinterpret_cast<const f4*>(part + size_t(s) * total + i);
+  if (ydtype == PARO_F32) {
+    *reinterpret_cast<f4*>(static_cast<float*>(y) + i) = v;
+  } else {
+    typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<h4*>(static_cast<_Float16*>(y) + i) = __builtin_convertvector(v, h4);
+  }
+}
+
+// Workgroups: as many as the GPU holds at once (16 waves on a CU), and no more than there can be tiles.
+template <int W, int GW>
+hipError_t launch_gate_up(const MoeCall& c, hipStream_t st) {
+  const long tiles = long(moe_units_max(c.M, c.E, c.top_k)) * (c.F / 16);
+  hipLaunchKernelGGL((gate_up_kernel<W, GW>), dim3(unsigned(std::min<long>(tiles, long(kCUs) * (16 / W)))), dim3(64 * W), 0, st, c);
   return hipGetLastError();
 }
 
+constexpr int kDownWaves = 8, kDownTiles = 2;
+static_assert(sizeof(MoeUnit) * (PARO_MOE_MAX_E + PARO_MOE_MAX_M) + sizeof(MoeSlot) * PARO_MOE_MAX_M * PARO_MOE_MAX_K +
+                      size_t(kDownWaves) * kDownTiles * PARO_MOE_MAX_M * 64 <= 80 * 1024, "two workgroups on a CU");
+
+}  // namespace
+
+int moe_units_max(int M, int E, int top_k) { return std::min(E, M * top_k) + M * top_k / 16; }
+
+// Workgroups of the down product that share their columns: what leaves the fewest items on the busiest place of the GPU
+// (two workgroups to a CU), where there are items enough to pay for another launch.
+int moe_down_splits(int M, int D, int F, int E, int top_k) {
+  const long items = long(std::min(E, M * top_k)) * ((F / PARO_GROUP + 3) / 4), tiles = D / 16 / kDownTiles, places = 2 * kCUs;
+  int best = 1;
+  double least = double(items) * ((tiles + places - 1) / places);
+  for (int s = 2; s <= 32; ++s) {
+    const double each = double(items) / s * ((tiles * s + places - 1) / places) + 15;
+    if (each < least) {
+      least = each;
+      best = s;
+    }
+  }
+  return best;
+}
+
+hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st) {
+  const int G = c.D / PARO_GROUP;
+  if (G <= 16) {
+    if (G <= 4) return launch_gate_up<4, 1>(c, st);
+    if (G <= 8) return launch_gate_up<4, 2>(c, st);
+    return G <= 12 ? launch_gate_up<4, 3>(c, st) : launch_gate_up<4, 4>(c, st);
+  }
+  if (G <= 32) return G <= 24 ? launch_gate_up<8, 3>(c, st) : launch_gate_up<8, 4>(c, st);
+  if (G <= 64) return G <= 48 ? launch_gate_up<16, 3>(c, st) : launch_gate_up<16, 4>(c, st);
+  return launch_gate_up<16, 0>(c, st);
+}
+
 hipError_t launch_moe_down(const MoeCall& c, hipStream_t st) {
-  hipLaunchKernelGGL(down_kernel, dim3(unsigned(c.D / 16)), dim3(512), 0, st, c);
+  constexpr int W = kDownWaves, T = kDownTiles;
+  const DownArgs a{c, moe_down_splits(c.M, c.D, c.F, c.E, c.top_k)};
+  const size_t lds = size_t(W) * T * c.M * 64 + sizeof(MoeSlot) * c.M * c.top_k + sizeof(MoeUnit) * moe_units_max(c.M, c.E, c.top_k);
+  const auto kernel = down_kernel<W, T, T == 1 ? 4 : 2>;
+  if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(lds))) return e;
+  hipLaunchKernelGGL(kernel, dim3(unsigned(c.D / 16 / T * a.splits)), dim3(64 * W), lds, st, a);
+  if (a.splits > 1) {
+    const int total = c.M * c.D;
+    hipLaunchKernelGGL(sum_kernel, dim3(unsigned((total / 4 + 255) / 256)), dim3(256), 0, st, c.part, a.splits, total, c.y, c.ydtype);
+  }
   return hipGetLastError();
 }
 

@@ -6,32 +6,38 @@
 
 namespace paro {
 
-// Which tokens go to which experts, made on the GPU from the ids. Slots are the (expert, token) pairs in the order
-// of experts, then tokens; a token that names an expert twice has one slot with both weights.
-struct MoeActive {
+// Which tokens go to which experts. Slots are the (expert, token) pairs in the order of the experts, then the tokens;
+// a token that names an expert twice has one slot with both weights. A unit is up to 16 slots of one expert.
+struct MoeUnit {
   int expert, first, count;  // its slots are first .. first + count - 1
 };
-struct MoeTables {
-  int* active_count;
-  MoeActive* active;   // the experts that have tokens, in their order
-  int* slot_token;     // [slots]
-  float* slot_weight;  // [slots]
+struct MoeSlot {
+  uint16_t pair, token;  // the first (token, choice) pair, whose row of a the slot has
+  float weight;
 };
+struct MoeTables {
+  int* units;  // how many
+  MoeUnit* unit;
+  MoeSlot* slot;
+};
+int moe_units_max(int M, int E, int top_k);
 
 struct MoeCall {
   int M, D, F, E, top_k;
   const uint16_t* x;  // [M][D], as the experts see it
+  bool x_nibble_order, a_nibble_order;  // 8-channel words of x, and of what goes to a, as [0,4,1,5,2,6,3,7]
   const uint8_t* gu_qw;
   const uint16_t* gu_sc;
   const uint16_t* gu_zr;
   const uint8_t* dn_qw;
   const uint16_t* dn_sc;
   const uint16_t* dn_zr;
-  uint16_t* a;             // [slots][F], what the gate and up products make
-  const uint16_t* a_down;  // the same as the down product sees it
+  uint16_t* a;             // [M top_k][F], what the gate and up products make: the rows of the pairs that have an expert
+  const uint16_t* a_down;  // the same as the down product sees it, in the nibble order
+  float* part;             // [splits][M][D], where the down product is split
+  MoeTables t;
   void* y;
   int ydtype;
-  MoeTables t;
 };
 
 struct MoeRoute {
@@ -51,6 +57,7 @@ hipError_t launch_moe_select(const MoeRoute& r, const MoeTables* t, hipStream_t 
 // The tables from given ids and weights.
 hipError_t launch_moe_group(int M, int E, int top_k, const int32_t* ids, const float* weights, const MoeTables& t, hipStream_t st);
 hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st);
+int moe_down_splits(int M, int D, int F, int E, int top_k);
 hipError_t launch_moe_down(const MoeCall& c, hipStream_t st);
 
 }  // namespace paro

@@ -1,29 +1,31 @@
-// The router of a mixture-of-experts layer: logits, the experts of each token, and the tables that the experts'
-// products go by.
+// The router of a mixture-of-experts layer: logits, then the experts of each token with their weights.
 //
 // Logits are float64 sums of products that are exact in it: which expert a token takes hangs on the order of two
 // logits, and a float32 sum turns close ones round.
 #include <algorithm>
 
-#include "moe_internal.h"
+#include "moe_tables.h"
 #include "w4_device.h"
 
 namespace paro {
 namespace {
 
-constexpr int kMaxM = PARO_MOE_MAX_M, kMaxE = PARO_MOE_MAX_E, kMaxK = PARO_MOE_MAX_K;
-constexpr int kTile = 4;  // a workgroup has 4 tokens and 4 experts
+constexpr int kMaxM = PARO_MOE_MAX_M, kMaxK = PARO_MOE_MAX_K;
+static_assert(PARO_MOE_MAX_E <= 512, "select_kernel<2> has room for 512 experts");
+constexpr int kWaves = 4;
 
-template <bool F32>
-__global__ __launch_bounds__(256) void logits_kernel(const MoeRoute r) {
-  __shared__ double part[4][kTile * kTile];
+// A workgroup has MT tokens and ET experts; its threads take 8 channels at a time.
+template <bool F32, int MT, int ET>
+__global__ __launch_bounds__(64 * kWaves) void logits_kernel(const MoeRoute r) {
+  constexpr int V = MT * ET;
+  __shared__ double part[kWaves][V];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int e0 = blockIdx.x * kTile, m0 = blockIdx.y * kTile;
-  double acc[kTile][kTile] = {};
-  for (int c = tid; c < r.D / 8; c += 256) {
-    double w[kTile][8];
+  const int e0 = blockIdx.x * ET, m0 = blockIdx.y * MT;
+  double acc[V] = {};
+  for (int c = tid; c < r.D / 8; c += 64 * kWaves) {
+    float w[ET][8];
 #pragma unroll
-    for (int i = 0; i < kTile; ++i) {
+    for (int i = 0; i < ET; ++i) {
       const size_t row = size_t(min(e0 + i, r.E - 1)) * r.D + c * 8;
       if constexpr (F32) {
         const float* const p = static_cast<const float*>(r.router) + row;
@@ -36,209 +38,201 @@ __global__ __launch_bounds__(256) void logits_kernel(const MoeRoute r) {
         for (int k = 0; k < 8; ++k) w[i][k] = float(v[k]);
       }
     }
+    h8 x[MT];
 #pragma unroll
-    for (int j = 0; j < kTile; ++j) {
-      const h8 v = *reinterpret_cast<const h8*>(r.x + size_t(min(m0 + j, r.M - 1)) * r.D + c * 8);
+    for (int j = 0; j < MT; ++j) x[j] = *reinterpret_cast<const h8*>(r.x + size_t(min(m0 + j, r.M - 1)) * r.D + c * 8);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const double x = float(v[k]);
+    for (int k = 0; k < 8; ++k) {
 #pragma unroll
-        for (int i = 0; i < kTile; ++i) acc[j][i] = __builtin_fma(x, w[i][k], acc[j][i]);
-      }
+      for (int j = 0; j < MT; ++j)
+#pragma unroll
+        for (int i = 0; i < ET; ++i) acc[j * ET + i] = __builtin_fma(double(float(x[j][k])), double(w[i][k]), acc[j * ET + i]);
     }
   }
+  // The wave's sums: while there are several, lanes whose indexes differ in one bit keep half of them each.
+  int n = V, at = 0, d = 32;
 #pragma unroll
-  for (int j = 0; j < kTile; ++j)
+  for (; n > 1; n /= 2, d /= 2) {
+    const bool high = lane & d;
 #pragma unroll
-    for (int i = 0; i < kTile; ++i) {
-      double v = acc[j][i];
+    for (int i = 0; i < V / 2; ++i)
+      if (i < n / 2) {
+        const double keep = high ? acc[n / 2 + i] : acc[i], give = high ? acc[i] : acc[n / 2 + i];
+        acc[i] = keep + __shfl_xor(give, d);
+      }
+    at += high ? n / 2 : 0;
+  }
 #pragma unroll
-      for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
-      if (lane == 0) part[wave][j * kTile + i] = v;
-    }
+  for (; d; d /= 2) acc[0] += __shfl_xor(acc[0], d);
+  if ((lane & (64 / V - 1)) == 0) part[wave][at] = acc[0];
   __syncthreads();
-  if (tid < kTile * kTile) {
-    const int m = m0 + tid / kTile, e = e0 + tid % kTile;
-    if (m < r.M && e < r.E) r.logits[size_t(m) * r.E + e] = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+  if (tid < V) {
+    const int m = m0 + tid / ET, e = e0 + tid % ET;
+    double v = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) v += part[i][tid];
+    if (m < r.M && e < r.E) r.logits[size_t(m) * r.E + e] = v;
   }
 }
 
-struct Shared {
-  unsigned long long mask[kMaxE];  // an expert's tokens
-  int first[kMaxE];                // its first slot
-  int ids[kMaxM * kMaxK];
-  float weights[kMaxM * kMaxK];
-};
-
-// The tables from s.ids and s.weights (all threads of the workgroup).
-__device__ inline void make_tables(Shared& s, int M, int E, int top_k, const MoeTables& t) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  for (int e = tid; e < kMaxE; e += nt) s.mask[e] = 0;
+// A workgroup has a token. An expert's rank is how many others go before it: the larger logits, the equal ones of a
+// lower index; the first top_k ranks are the token's choices. No rank waits for another, where top_k searches for
+// the largest one would go through the wave one after the other. PARTS threads share the comparisons of an expert.
+template <int PARTS>
+__global__ __launch_bounds__(1024) void select_kernel(const MoeRoute r) {
+  constexpr int kExperts = 1024 / PARTS;
+  __shared__ double key[kExperts], part[16], chosen[kMaxK];
+  __shared__ int id[kMaxK];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = blockIdx.x, e = tid / PARTS;
+  const double logit = e < r.E ? r.logits[size_t(m) * r.E + e] : 0.0;
+  const double mine = logit == logit ? logit : -__builtin_inf();  // a NaN ranks as minus infinity
+  if (tid % PARTS == 0) key[e] = mine;
   __syncthreads();
-  for (int p = tid; p < M * top_k; p += nt) {
-    const int e = s.ids[p];
-    if (e >= 0 && e < E) atomicOr(&s.mask[e], 1ull << (p / top_k));  // (an or: the same in any order)
+  int rank = 0;
+#pragma unroll 4
+  for (int o = tid % PARTS; o < r.E; o += PARTS) {
+    const double other = key[o];
+    rank += other > mine || (other == mine && o < e);
+  }
+#pragma unroll
+  for (int d = 1; d < PARTS; d *= 2) rank += __shfl_xor(rank, d);
+  if (tid % PARTS == 0 && e < r.E && rank < r.top_k) {
+    id[rank] = e;
+    chosen[rank] = logit;
   }
   __syncthreads();
-  if (tid < 64) {  // a lane has 8 experts in a row
-    constexpr int kEach = kMaxE / 64;
-    int slots = 0, active = 0;
-    for (int i = 0; i < kEach; ++i) {
-      const int n = __popcll(s.mask[tid * kEach + i]);
-      slots += n;
-      active += n > 0;
+  double sum = 0, top = 0;
+  if (!r.sigmoid) {
+    top = key[id[0]];
+    if (wave < (r.E * PARTS + 63) / 64) {
+      sum = e < r.E ? exp(logit - top) : 0.0;
+#pragma unroll
+      for (int d = 32; d >= PARTS; d /= 2) sum += __shfl_xor(sum, d);
     }
-    int slot = slots, at = active;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int a = __shfl_up(slot, d), b = __shfl_up(at, d);
-      if (tid >= d) {
-        slot += a;
-        at += b;
-      }
-    }
-    if (tid == 63) *t.active_count = at;
-    slot -= slots;
-    at -= active;
-    for (int i = 0; i < kEach; ++i) {
-      const int e = tid * kEach + i, n = __popcll(s.mask[e]);
-      s.first[e] = slot;
-      if (n) t.active[at++] = MoeActive{e, slot, n};
-      slot += n;
-    }
+    if (lane == 0) part[wave] = sum;
+    __syncthreads();
+    sum = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum += part[i];
   }
-  __syncthreads();
-  for (int p = tid; p < M * top_k; p += nt) {
-    const int e = s.ids[p], m = p / top_k;
-    if (e < 0 || e >= E) continue;
-    float w = 0;
-    bool again = false;
-    for (int j = 0; j < top_k; ++j)
-      if (s.ids[m * top_k + j] == e) {
-        again |= m * top_k + j < p;
-        w += s.weights[m * top_k + j];
-      }
-    if (again) continue;
-    const int slot = s.first[e] + __popcll(s.mask[e] & ((1ull << m) - 1));
-    t.slot_token[slot] = m;
-    t.slot_weight[slot] = w;
+  if (tid < 64) {
+    const double v = lane < r.top_k ? chosen[lane] : 0.0;
+    const double w = r.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - top) / sum;
+    double all = 0;
+    for (int j = 0; j < r.top_k; ++j) all += __shfl(w, j);
+    if (lane < r.top_k) {
+      r.ids[m * r.top_k + lane] = id[lane];
+      r.weights[m * r.top_k + lane] = float(r.renormalize ? w / all : w);
+    }
   }
 }
 
-__global__ __launch_bounds__(1024) void group_kernel(int M, int E, int top_k, const int32_t* ids, const float* weights, const MoeTables t) {
-  __shared__ Shared s;
-  for (int p = threadIdx.x; p < M * top_k; p += blockDim.x) {
-    s.ids[p] = ids[p];
-    s.weights[p] = weights[p];
-  }
-  make_tables(s, M, E, top_k, t);  // (its first barrier comes before any use of them)
-}
-
-// A wave takes a token: its logits, kMaxE / 64 to a lane, and top_k times the largest that is left.
+// The same in one workgroup, a thread to each (token, expert) pair, for up to kOneGroup of them; then, with t, the tables
+// of the experts' products: a launch less.
+constexpr int kOneGroup = 1024;
 template <bool TABLES>
-__global__ __launch_bounds__(1024) void select_kernel(const MoeRoute r, const MoeTables t) {
-  __shared__ Shared s;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  constexpr int kEach = kMaxE / 64;
-  for (int m = wave; m < r.M; m += 16) {
-    const double* const row = r.logits + size_t(m) * r.E;
-    double v[kEach];
-    double top = -__builtin_inf();
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int e = lane + i * 64;
-      v[i] = e < r.E ? row[e] : -__builtin_inf();
-      top = v[i] > top ? v[i] : top;
+__global__ __launch_bounds__(1024) void select_one_kernel(const MoeRoute r, const MoeTables t) {
+  __shared__ union {
+    struct {
+      double key[kOneGroup], share[kOneGroup];
+    };
+    TableWork work;
+  } s;
+  __shared__ int ids[kMaxM * kMaxK];
+  __shared__ double chosen[kMaxM * kMaxK];
+  __shared__ float weights[kMaxM * kMaxK];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = tid / r.E, e = tid - m * r.E;
+  const bool live = m < r.M;
+  const double logit = live ? r.logits[tid] : 0.0;
+  const double mine = logit == logit ? logit : -__builtin_inf();  // a NaN ranks as minus infinity
+  s.key[tid] = mine;
+  __syncthreads();
+  if (live) {
+    int rank = 0;
+    const double* const row = s.key + m * r.E;
+#pragma unroll 8
+    for (int o = 0; o < r.E; ++o) rank += row[o] > mine || (row[o] == mine && o < e);
+    if (rank < r.top_k) {
+      ids[m * r.top_k + rank] = e;
+      chosen[m * r.top_k + rank] = logit;
     }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) {
-      const double o = __shfl_xor(top, d);
-      top = o > top ? o : top;
-    }
+  }
+  __syncthreads();
+  if (live && !r.sigmoid) s.share[tid] = exp(logit - s.key[m * r.E + ids[m * r.top_k]]);
+  __syncthreads();
+  for (int at = wave; at < r.M; at += 16) {  // a wave for each token
     double sum = 0;
     if (!r.sigmoid) {
+      for (int o = lane; o < r.E; o += 64) sum += s.share[at * r.E + o];
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (lane + i * 64 < r.E) sum += exp(v[i] - top);
-#pragma unroll
-      for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+      for (int d = 32; d; d /= 2) sum += __shfl_xor(sum, d);
     }
-    uint32_t taken = 0;
-    double mine = 0, chosen = 0;  // lane j holds the j-th weight
-    int id = 0;
-    for (int j = 0; j < r.top_k; ++j) {
-      double best = 0;
-      int at = kMaxE;  // none yet
-#pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int e = lane + i * 64;
-        if (e < r.E && !(taken >> i & 1)) {
-          const double key = v[i] == v[i] ? v[i] : -__builtin_inf();
-          if (at == kMaxE || key > best) {
-            best = key;
-            at = e;
-          }
-        }
-      }
-#pragma unroll
-      for (int d = 32; d; d >>= 1) {
-        const double o = __shfl_xor(best, d);
-        const int oe = __shfl_xor(at, d);
-        if (oe != kMaxE && (at == kMaxE || o > best || (o == best && oe < at))) {
-          best = o;
-          at = oe;
-        }
-      }
-      // the logit itself (a NaN stays one)
-      double logit = 0;
-#pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (lane == (at & 63) && i == at / 64) {
-          logit = v[i];
-          taken |= 1u << i;
-        }
-      logit = __shfl(logit, at & 63);
-      const double w = r.sigmoid ? 1.0 / (1.0 + exp(-logit)) : exp(logit - top) / sum;
-      chosen += w;
-      if (lane == j) {
-        mine = w;
-        id = at;
-      }
-    }
-    if (lane < r.top_k) {
-      const float w = float(r.renormalize ? mine / chosen : mine);
-      const int p = m * r.top_k + lane;
-      r.ids[p] = id;
-      r.weights[p] = w;
-      if constexpr (TABLES) {
-        s.ids[p] = id;
-        s.weights[p] = w;
-      }
-    }
+    const int p = at * r.top_k + lane;
+    double w = 0;
+    if (lane < r.top_k) w = r.sigmoid ? 1.0 / (1.0 + exp(-chosen[p])) : s.share[at * r.E + ids[p]] / sum;
+    double all = 0;
+    for (int j = 0; j < r.top_k; ++j) all += __shfl(w, j);
+    if (lane < r.top_k) weights[p] = float(r.renormalize ? w / all : w);
   }
-  if constexpr (TABLES) make_tables(s, r.M, r.E, r.top_k, t);
+  __syncthreads();
+  const int pairs = r.M * r.top_k;
+  for (int p = tid; p < pairs; p += 1024) {
+    r.ids[p] = ids[p];
+    r.weights[p] = weights[p];
+  }
+  if constexpr (TABLES) make_tables(s.work, r.M, r.E, r.top_k, ids, weights, t);
+}
+
+__global__ __launch_bounds__(512) void group_kernel(int M, int E, int top_k, const int32_t* given_ids, const float* given_weights,
+                                                    const MoeTables t) {
+  __shared__ TableWork work;
+  __shared__ int ids[kMaxM * kMaxK];
+  __shared__ float weights[kMaxM * kMaxK];
+  for (int p = threadIdx.x; p < M * top_k; p += 512) {
+    ids[p] = given_ids[p];
+    weights[p] = given_weights[p];
+  }
+  make_tables(work, M, E, top_k, ids, weights, t);  // (which begins with a barrier)
+}
+
+template <int MT, int ET>
+hipError_t launch_logits(const MoeRoute& r, hipStream_t st) {
+  const dim3 grid(unsigned((r.E + ET - 1) / ET), unsigned((r.M + MT - 1) / MT));
+  if (r.router_f32)
+    hipLaunchKernelGGL((logits_kernel<true, MT, ET>), grid, dim3(64 * kWaves), 0, st, r);
+  else
+    hipLaunchKernelGGL((logits_kernel<false, MT, ET>), grid, dim3(64 * kWaves), 0, st, r);
+  return hipGetLastError();
 }
 
 }  // namespace
 
+// A single token: a workgroup for each expert. Few pairs of tokens and experts: as many workgroups as tiles of 4 by 1
+// give; many: tiles of 4 by 4, which read half as much.
 hipError_t launch_moe_logits(const MoeRoute& r, hipStream_t st) {
-  const dim3 grid(unsigned((r.E + kTile - 1) / kTile), unsigned((r.M + kTile - 1) / kTile));
-  if (r.router_f32)
-    hipLaunchKernelGGL(logits_kernel<true>, grid, dim3(256), 0, st, r);
-  else
-    hipLaunchKernelGGL(logits_kernel<false>, grid, dim3(256), 0, st, r);
-  return hipGetLastError();
+  if (r.M == 1) return launch_logits<1, 1>(r, st);
+  return r.M * r.E <= 2048 ? launch_logits<4, 1>(r, st) : launch_logits<4, 4>(r, st);
 }
 
+// t: the tables too, or nullptr.
 hipError_t launch_moe_select(const MoeRoute& r, const MoeTables* t, hipStream_t st) {
-  if (t)
-    hipLaunchKernelGGL(select_kernel<true>, dim3(1), dim3(1024), 0, st, r, *t);
-  else
-    hipLaunchKernelGGL(select_kernel<false>, dim3(1), dim3(1024), 0, st, r, MoeTables{});
-  return hipGetLastError();
+  if (r.M * r.E <= kOneGroup) {
+    if (t)
+      hipLaunchKernelGGL(select_one_kernel<true>, dim3(1), dim3(1024), 0, st, r, *t);
+    else
+      hipLaunchKernelGGL(select_one_kernel<false>, dim3(1), dim3(1024), 0, st, r, MoeTables{});
+    return hipGetLastError();
+  }
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned(r.M)), dim3(1024), 0, st, r);
+    return hipGetLastError();
+  };
+  if (hipError_t e = r.E <= 64 ? go(select_kernel<16>) : r.E <= 256 ? go(select_kernel<4>) : go(select_kernel<2>)) return e;
+  return t ? launch_moe_group(r.M, r.E, r.top_k, r.ids, r.weights, *t, st) : hipSuccess;
 }
 
 hipError_t launch_moe_group(int M, int E, int top_k, const int32_t* ids, const float* weights, const MoeTables& t, hipStream_t st) {
-  hipLaunchKernelGGL(group_kernel, dim3(1), dim3(1024), 0, st, M, E, top_k, ids, weights, t);
+  hipLaunchKernelGGL(group_kernel, dim3(1), dim3(512), 0, st, M, E, top_k, ids, weights, t);
   return hipGetLastError();
 }
 
