@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import F16, F32, GROUP, _i, _lib, _on_gpu, _ptr, _sz, _vp, _want, _want_ws
-from .w8a8 import _DTYPE, _call, _channels, _f, _forward_only, _rot_p, _rows, paro_w8a8_workspace_bytes
+from .w8a8 import _DTYPE, _binding, _call, _channels, _f, _forward_only, _rot_p, _rows, paro_w8a8_workspace_bytes
 
 MOE_MAX_M, MOE_MAX_E, MOE_MAX_K = 64, 512, 16
 ACTIVATIONS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
@@ -39,6 +39,7 @@ for _name, (_res, _args) in _SIGNATURES.items():
     getattr(_lib, _name).restype = _res
     getattr(_lib, _name).argtypes = _args
 EXPORTS_BLOCK = tuple(_SIGNATURES)
+_binding.bind_block(*(ctypes.cast(getattr(_lib, _name), _vp).value for _name in EXPORTS_BLOCK))
 
 
 def _one_of(table, name, what):
@@ -53,6 +54,9 @@ def paro_w8a8_linear_epilogue(x, x_scales, qweight, w_scales, bias=None, activat
     y's type (each optional), activation one of "none", "relu", "relu2" (its square), "silu", "gelu", "gelu_tanh". The
     type of y is out_dtype, or that of out, residual or bias, or float16. ``out`` may be ``residual`` itself."""
     act = _one_of(ACTIVATIONS, activation, "activation")
+    y = _binding.linear_epilogue(x, x_scales, qweight, w_scales, bias, act, residual, out_dtype, out, ws)
+    if y is not None:
+        return y
     for t, what in ((x, "x"), (qweight, "qweight")):
         if not isinstance(t, torch.Tensor) or t.dim() != 2:
             raise ValueError(f"{what} must be a torch.Tensor with two dimensions")
@@ -83,6 +87,9 @@ def paro_w8a8_linear_epilogue(x, x_scales, qweight, w_scales, bias=None, activat
 
 
 def _block_norm(q8, x, residual, gamma, eps, post_gamma, gate, residual_scale, residual_out, outs):
+    r = _binding.block_norm(q8, x, residual, gamma, eps, post_gamma, gate, residual_scale, residual_out, outs[0], outs[-1])
+    if r is not None:
+        return r
     M, D = _rows(x, "x")
     _want(residual, x.dtype, (M, D), "residual")
     _want(gamma, x.dtype, (D,), "gamma")
@@ -182,6 +189,9 @@ def paro_moe_route(x, router, top_k, scoring="softmax", renormalize=True, out=No
     float32 [E][D]; scoring "softmax" (over all experts) or "sigmoid", divided by its sum over the top_k with
     ``renormalize``. ``out``: an optional (ids, weights) pair to write."""
     how = _one_of(SCORINGS, scoring, "scoring")
+    r = _binding.route(x, router, top_k, how, bool(renormalize), *((None, None) if out is None else out), ws)
+    if r is not None:
+        return r
     M, D, E = _router(x, router, top_k)
     ids, weights = given = _routing(out, M, top_k)
     _want_ws(ws)
@@ -239,18 +249,26 @@ def _rot(rot):
     return None if rot is None else rot.ptr
 
 
+def _compiled(x, router, top_k, how, renormalize, ids, weights, gate_up, down, rot_x, rot_a, out_dtype, out, ws):
+    rots = [v for r in (rot_x, rot_a) for v in ((0, None) if r is None else (ctypes.addressof(r.handle), r.desc))]
+    return _binding.moe(x, router, top_k, how, renormalize, ids, weights, gate_up, down, *rots, out_dtype, out, ws)
+
+
 def paro_moe_w4a16(x, ids, weights, gate_up, down, rot_x=None, rot_a=None, out_dtype=None, out=None, ws=None):
     """The experts of up to 64 tokens on INT4 weights: y[m] = sum_j weights[m][j] * down_e(silu(gate_e x) * up_e x) with
     e = ids[m][j]; an id outside 0..E-1 takes no expert. x float16 [M][D]; ids int32, weights float32 [M][top_k];
     gate_up a (qweight uint8 [E][2F][D/2], scales, zeros float16 [E][2F][D/128]) triple, gate rows first, as
     paro_pack_weights packs the E * 2F rows; down the same [E][D][F]. rot_x, rot_a: the transforms (of D and of F
     channels) that gate_up's and down's rows were packed with. y float16 (default) or float32 [M][D]."""
+    y = _compiled(x, None, None, None, None, ids, weights, gate_up, down, rot_x, rot_a, out_dtype, out, ws)
+    if y is not None:
+        return y
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids must be a torch.Tensor with two dimensions")
     top_k = ids.shape[1]
     M, D = _tokens(x, top_k)
-    if ids is None or weights is None:
-        raise ValueError("ids and weights are required")
+    if weights is None:
+        raise ValueError("weights are required")
     _routing((ids, weights), M, top_k)
     E, F, (gu, dn), y, ydtype, ws, dev = _experts(M, D, None, top_k, gate_up, down, rot_x, rot_a, out_dtype, out, ws,
                                                   {"x": x, "ids": ids, "weights": weights})
@@ -265,6 +283,10 @@ def paro_moe_layer_w4a16(x, router, top_k, gate_up, down, rot_x=None, rot_a=None
     one call: (y, ids, weights). The router sees x itself, not its transform. ``routing``: an optional (ids, weights)
     pair to write."""
     how = _one_of(SCORINGS, scoring, "scoring")
+    r = _compiled(x, router, top_k, how, bool(renormalize), *((None, None) if routing is None else routing), gate_up, down, rot_x, rot_a,
+                  out_dtype, out, ws)
+    if r is not None:
+        return r
     M, D, E = _router(x, router, top_k)
     ids, weights = given = _routing(routing, M, top_k)
     E, F, (gu, dn), y, ydtype, ws, dev = _experts(M, D, E, top_k, gate_up, down, rot_x, rot_a, out_dtype, out, ws,

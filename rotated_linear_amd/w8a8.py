@@ -25,6 +25,8 @@ try:
     _for = getattr(_binding, "torch_version", "another version")
     if re.match(r"\d+\.\d+\.\d+", torch.__version__)[0] != _for:  # (its headers name no pre-release)
         raise ImportError(f"it was built for torch {_for}, this is {torch.__version__}")
+    if not hasattr(_binding, "bind_block"):
+        raise ImportError("it was built from older sources")
 except ImportError as e:
     warnings.warn(f"rotated_linear_amd runs without its compiled binding ({e}): the 8-bit calls take more host time. "
                   "Build it with `python -m rotated_linear_amd._build`.", RuntimeWarning, stacklevel=2)
@@ -35,6 +37,7 @@ except ImportError as e:
             return None
 
         bind = linear = quantize = dequantize = rmsnorm = _declines
+        bind_block = linear_epilogue = block_norm = route = moe = _declines
 
 BF16 = 2
 _DTYPE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}

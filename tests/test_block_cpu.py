@@ -271,6 +271,22 @@ def test_binding_refusals():
     raises(ValueError, "gate_up has 513 experts, it must have 1 to 512", "moe", **{"gate_up qweight": t(513, 256, 128, dtype=torch.uint8)})
 
 
+def test_compiled_binding_declines_what_it_does_not_take():
+    """It returns None, having done nothing, for CPU tensors, other objects and wrong counts; bind_block() takes eight
+    addresses, none of them zero."""
+    b = pytest.importorskip("rotated_linear_amd._binding")
+    x, q, s = torch.zeros(2, 256, dtype=torch.float16), torch.zeros(2, 256, dtype=torch.int8), torch.zeros(2)
+    for f, args in ((b.linear_epilogue, (q, s, q, s, None, 0, None, None, None, None)), (b.route, (x, x, 1, 0, True, None, None, None)),
+                    (b.block_norm, (True, x, x, x[0], 1e-6, None, None, 1.0, None, None, None)),
+                    (b.moe, (x, x, 1, 0, True, None, None, (q, s, s), (q, s, s), 0, None, 0, None, None, None, None)),
+                    (b.moe, (x, None, None, None, None, q, s, (q, s, s), (q, s, s), 0, None, 0, None, None, None, None))):
+        assert f(*args) is None and f(*args[1:]) is None and f() is None
+        assert f(*("x" if isinstance(a, torch.Tensor) else a for a in args)) is None
+    for bad in ((), (1,) * 7, (1,) * 7 + (0,), (1,) * 7 + ("x",)):
+        with pytest.raises((TypeError, ValueError)):
+            b.bind_block(*bad)
+
+
 # ---- the oracle against hand-worked values ----
 
 def test_oracle_activations():
