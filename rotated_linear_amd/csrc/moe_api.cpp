@@ -29,7 +29,7 @@ Layout layout(int M, int D, int F, int E, int top_k) {
   l.x = take(size_t(M) * D * 2);
   l.a = take(pairs * F * 2);
   l.a_rotated = take(pairs * F * 2);
-  const int splits = moe_down_splits(M, D, F, E, top_k);
+  const int splits = moe_down_plan(M, D, F, E, top_k).splits;
   l.part = take(splits > 1 ? size_t(splits) * M * D * 4 : 0);
   l.units = take(4);
   l.unit = take(size_t(moe_units_max(M, E, top_k)) * sizeof(MoeUnit));
@@ -98,7 +98,7 @@ paro_status experts(int M, int D, int F, int E, int top_k, const void* x, const 
   c.dn_zr = static_cast<const uint16_t*>(down->zeros);
   c.a = reinterpret_cast<uint16_t*>(base + l.a);
   c.a_down = c.a;
-  c.a_nibble_order = rot_a == nullptr;
+  c.a_fragments = rot_a == nullptr;
   c.part = reinterpret_cast<float*>(base + l.part);
   c.t = MoeTables{reinterpret_cast<int*>(base + l.units), reinterpret_cast<MoeUnit*>(base + l.unit), reinterpret_cast<MoeSlot*>(base + l.slot)};
   c.y = y;

@@ -1,6 +1,7 @@
 // The experts' products of a mixture-of-experts layer for a few tokens, on INT4 weights: gate and up with their
 // activation, then down with the sum over a token's experts.
 #include <algorithm>
+#include <cmath>
 
 #include "moe_internal.h"
 #include "w4_device.h"
@@ -67,7 +68,13 @@ __device__ inline void load_scales(uint32_t& scale, uint32_t& zero, const void* 
   scale = at<uint16_t>(sp, so);
   zero = at<uint16_t>(zp, so);
 }
-__device__ inline void load_rows(Rows& r, const void* base, uint32_t& off) {
+// step: from a lane's 8 channels to its next 8.
+__device__ inline void load_rows(Rows& r, const void* base, uint32_t& off, uint32_t step) {
+  opaque(off);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) r.v[k] = at<h8>(static_cast<const char*>(base) + k * step, off);
+}
+__device__ inline void load_rows(Rows& r, const void* base, uint32_t& off) {  // (16: as offsets of the instructions)
   opaque(off);
 #pragma unroll
   for (int k = 0; k < 4; ++k) r.v[k] = at<h8>(base, off, k * 16);
@@ -75,6 +82,13 @@ __device__ inline void load_rows(Rows& r, const void* base, uint32_t& off) {
 
 // All that is computed up to here comes before whatever is loaded later.
 __device__ inline void settled(f4& v) { asm volatile("" : "+v"(v) : : "memory"); }
+
+// Where channel n of a row lies in the order of fragments: within its group the lanes' first 8 channels, then their
+// second 8, ..., so that each load of a row takes 64 bytes that follow each other; within 8 the order of dequant_word.
+__device__ inline int fragment_place(int n) {
+  const int h = n >> 5 & 3, k = n >> 3 & 3, j = n & 7;
+  return (n & ~127) | k << 5 | h << 3 | (j & 3) << 1 | j >> 2;
+}
 
 // Workgroups go through the tiles (16 gate and 16 up rows of a unit's expert), unit by unit, each a run of them. W waves
 // share out the groups of channels: wave w has GW of them from group GW w on, whose part of the unit's tokens it keeps
@@ -240,8 +254,9 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
         upv += red[j][1][v][l][i];
       }
       const float v = gate / (1.0f + expf(-gate)) * upv;
-      const int to = c.a_nibble_order ? (col & 8) | (col & 3) << 1 | (col >> 2 & 1) : col;
-      c.a[size_t(c.t.slot[first + m].pair) * c.F + (tile - parked + j) * 16 + to] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+      int to = (tile - parked + j) * 16 + col;
+      if (c.a_fragments) to = fragment_place(to);
+      c.a[size_t(c.t.slot[first + m].pair) * c.F + to] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
     }
     if (t == end) break;
     parked = 0;
@@ -262,8 +277,11 @@ struct DownArgs {
 // A workgroup has T times 16 columns of y and its share of the items, an item being four groups of a unit: the items in
 // order are cut into splits * W equal runs, one for each wave. A wave keeps sums of its own for every token in LDS, to
 // which it adds an expert's products times the tokens' weights where it leaves the expert. R groups are in flight.
+//
+// What bounds it is the CU's load path: a group of 16 rows of a takes four times the loads of 16 columns' weights, so
+// more columns to a workgroup cost less, as long as there is a workgroup for each CU.
 template <int W, int T, int R>
-__global__ __launch_bounds__(64 * W, 4) void down_kernel(const DownArgs args) {
+__global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const DownArgs args) {
   static_assert(R == 2 || R == 4, "a group's slot is fixed");
   extern __shared__ __attribute__((aligned(16))) char smem[];  // float [W][M][16 T], then the tables
   const MoeCall& c = args.c;
@@ -290,7 +308,7 @@ __global__ __launch_bounds__(64 * W, 4) void down_kernel(const DownArgs args) {
   const char *wp = nullptr, *sp = nullptr, *zp = nullptr;
   auto aim = [&]() {  // (no global access: the wait counts stay exact)
     const MoeUnit k = unit[lu];
-    ao = uint32_t(slot[k.first + min(nl, k.count - 1)].pair) * uint32_t(c.F) * 2 + h * 64;
+    ao = uint32_t(slot[k.first + min(nl, k.count - 1)].pair) * uint32_t(c.F) * 2 + h * (c.a_fragments ? 16 : 64);
     const size_t row = size_t(__builtin_amdgcn_readfirstlane(k.expert)) * c.D + tile * 16 * T;
     wp = reinterpret_cast<const char*>(c.dn_qw) + row * (c.F / 2);
     sp = reinterpret_cast<const char*>(c.dn_sc) + row * G * 2;
@@ -312,7 +330,7 @@ __global__ __launch_bounds__(64 * W, 4) void down_kernel(const DownArgs args) {
     const uint32_t g = min(4 * lq + p, G - 1);
 #pragma unroll
     for (int t = 0; t < T; ++t) w[q][t] = load_weights(wp + size_t(t) * 8 * c.F + g * 1024, wo);
-    load_rows(a[q], c.a_down + g * PARO_GROUP, ao);
+    load_rows(a[q], c.a_down + g * PARO_GROUP, ao, c.a_fragments ? 64 : 16);
   };
   if (begin < end) {
     aim();
@@ -399,27 +417,34 @@ hipError_t launch_gate_up(const MoeCall& c, hipStream_t st) {
   return hipGetLastError();
 }
 
-constexpr int kDownWaves = 8, kDownTiles = 2;
-static_assert(sizeof(MoeUnit) * (PARO_MOE_MAX_E + PARO_MOE_MAX_M) + sizeof(MoeSlot) * PARO_MOE_MAX_M * PARO_MOE_MAX_K +
-                      size_t(kDownWaves) * kDownTiles * PARO_MOE_MAX_M * 64 <= 80 * 1024, "two workgroups on a CU");
+constexpr int kDownWaves = 8;
+constexpr size_t down_lds(int T, int M, int units, int pairs) {
+  return size_t(kDownWaves) * T * M * 64 + sizeof(MoeSlot) * pairs + sizeof(MoeUnit) * units;
+}
+static_assert(down_lds(4, PARO_MOE_MAX_M, PARO_MOE_MAX_E + PARO_MOE_MAX_M, PARO_MOE_MAX_M * PARO_MOE_MAX_K) <= 160 * 1024, "a CU's LDS");
 
 }  // namespace
 
 int moe_units_max(int M, int E, int top_k) { return std::min(E, M * top_k) + M * top_k / 16; }
 
-// Workgroups of the down product that share their columns: what leaves the fewest items on the busiest place of the GPU
-// (two workgroups to a CU), where there are items enough to pay for another launch.
-int moe_down_splits(int M, int D, int F, int E, int top_k) {
-  const long items = long(std::min(E, M * top_k)) * ((F / PARO_GROUP + 3) / 4), tiles = D / 16 / kDownTiles, places = 2 * kCUs;
-  int best = 1;
-  double least = double(items) * ((tiles + places - 1) / places);
-  for (int s = 2; s <= 32; ++s) {
-    const double each = double(items) / s * ((tiles * s + places - 1) / places) + 15;
-    if (each < least) {
-      least = each;
-      best = s;
+// 16, 32 or 64 columns to a workgroup, and how many workgroups share them, by an estimate in microseconds of what a CU
+// has to do: its items, four groups each, and the kernel that adds the parts. Measured (16, 32, 64 columns, workgroups
+// for each CU): 64 tokens, 8 of 64 experts, 1408 -> 4096 80, 54 and 46 us; 32 tokens, 4 of 16, 2048 -> 4096 27, 22 and
+// 22; 4 tokens, 2 of 8, 14336 -> 4096 45, 38 and 38; 13 tokens, 4 of 60, 1408 -> 1536 19, 14 and 16.
+MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {
+  constexpr double kItem[2][3] = {{0.22, 0.36, 0.75}, {0.39, 0.51, 0.86}};  // up to 32 tokens, and more
+  const double items = double(std::min(E, M * top_k)) * ((F / PARO_GROUP + 3) / 4);
+  MoeDownPlan best{1, 1};
+  double least = 1e30;
+  for (int i = 0; i < 3; ++i)
+    for (int s = 1; s <= 32; ++s) {
+      const double rounds = double((long(D / 16 >> i) * s + kCUs - 1) / kCUs);
+      const double us = rounds * std::ceil(items / s) * kItem[M > 32][i] * (0.92 + 0.08 * rounds) + (s > 1 ? 4.0 : 0.0);
+      if (us < least) {
+        least = us;
+        best = MoeDownPlan{1 << i, s};
+      }
     }
-  }
   return best;
 }
 
@@ -436,15 +461,22 @@ hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st) {
 }
 
 hipError_t launch_moe_down(const MoeCall& c, hipStream_t st) {
-  constexpr int W = kDownWaves, T = kDownTiles;
-  const DownArgs a{c, moe_down_splits(c.M, c.D, c.F, c.E, c.top_k)};
-  const size_t lds = size_t(W) * T * c.M * 64 + sizeof(MoeSlot) * c.M * c.top_k + sizeof(MoeUnit) * moe_units_max(c.M, c.E, c.top_k);
-  const auto kernel = down_kernel<W, T, T == 1 ? 4 : 2>;
-  if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(lds))) return e;
-  hipLaunchKernelGGL(kernel, dim3(unsigned(c.D / 16 / T * a.splits)), dim3(64 * W), lds, st, a);
-  if (a.splits > 1) {
+  constexpr int W = kDownWaves;
+  const MoeDownPlan p = moe_down_plan(c.M, c.D, c.F, c.E, c.top_k);
+  const DownArgs a{c, p.splits};
+  const size_t lds = down_lds(p.tiles, c.M, moe_units_max(c.M, c.E, c.top_k), c.M * c.top_k);
+  auto go = [&](auto kernel) {
+    if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, int(lds))) return e;
+    hipLaunchKernelGGL(kernel, dim3(unsigned(c.D / 16 / p.tiles * p.splits)), dim3(64 * W), lds, st, a);
+    return hipGetLastError();
+  };
+  if (hipError_t e = p.tiles == 1   ? go(down_kernel<W, 1, 4>)
+                     : p.tiles == 2 ? go(down_kernel<W, 2, 2>)
+                                    : go(down_kernel<W, 4, 2>))
+    return e;
+  if (p.splits > 1) {
     const int total = c.M * c.D;
-    hipLaunchKernelGGL(sum_kernel, dim3(unsigned((total / 4 + 255) / 256)), dim3(256), 0, st, c.part, a.splits, total, c.y, c.ydtype);
+    hipLaunchKernelGGL(sum_kernel, dim3(unsigned((total / 4 + 255) / 256)), dim3(256), 0, st, c.part, p.splits, total, c.y, c.ydtype);
   }
   return hipGetLastError();
 }

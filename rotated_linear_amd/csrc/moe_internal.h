@@ -25,7 +25,9 @@ int moe_units_max(int M, int E, int top_k);
 struct MoeCall {
   int M, D, F, E, top_k;
   const uint16_t* x;  // [M][D], as the experts see it
-  bool x_nibble_order, a_nibble_order;  // 8-channel words of x, and of what goes to a, as [0,4,1,5,2,6,3,7]
+  bool x_nibble_order;  // 8-channel words of x as [0,4,1,5,2,6,3,7]
+  bool a_fragments;     // a is written, and read, in the order of fragments; else it is written as it is and read in the
+                        // nibble order, with a transform in between
   const uint8_t* gu_qw;
   const uint16_t* gu_sc;
   const uint16_t* gu_zr;
@@ -33,7 +35,7 @@ struct MoeCall {
   const uint16_t* dn_sc;
   const uint16_t* dn_zr;
   uint16_t* a;             // [M top_k][F], what the gate and up products make: the rows of the pairs that have an expert
-  const uint16_t* a_down;  // the same as the down product sees it, in the nibble order
+  const uint16_t* a_down;  // the same as the down product sees it
   float* part;             // [splits][M][D], where the down product is split
   MoeTables t;
   void* y;
@@ -57,7 +59,10 @@ hipError_t launch_moe_select(const MoeRoute& r, const MoeTables* t, hipStream_t 
 // The tables from given ids and weights.
 hipError_t launch_moe_group(int M, int E, int top_k, const int32_t* ids, const float* weights, const MoeTables& t, hipStream_t st);
 hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st);
-int moe_down_splits(int M, int D, int F, int E, int top_k);
+struct MoeDownPlan {
+  int tiles, splits;  // 16-column tiles of a workgroup, and the workgroups that share them
+};
+MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k);
 hipError_t launch_moe_down(const MoeCall& c, hipStream_t st);
 
 }  // namespace paro

@@ -12,7 +12,7 @@ namespace {
 
 constexpr int kMaxM = PARO_MOE_MAX_M, kMaxK = PARO_MOE_MAX_K;
 static_assert(PARO_MOE_MAX_E <= 512, "select_kernel<2> has room for 512 experts");
-constexpr int kWaves = 4;
+constexpr int kWaves = 8;
 
 // A workgroup has MT tokens and ET experts; its threads take 8 channels at a time.
 template <bool F32, int MT, int ET>
