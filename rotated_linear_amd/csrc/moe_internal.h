@@ -66,3 +66,6 @@ MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k);
 hipError_t launch_moe_down(const MoeCall& c, hipStream_t st);
 
 }  // namespace paro
+
+// For tests, and in no header of the library: how a call's down product is cut.
+extern "C" void paro_internal_moe_down_plan(int M, int D, int F, int E, int top_k, int* tiles, int* splits);

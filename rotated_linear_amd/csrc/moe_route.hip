@@ -11,7 +11,7 @@ namespace paro {
 namespace {
 
 constexpr int kMaxM = PARO_MOE_MAX_M, kMaxK = PARO_MOE_MAX_K;
-static_assert(PARO_MOE_MAX_E <= 512, "select_kernel<2> has room for 512 experts");
+static_assert(PARO_MOE_MAX_E == 512, "a thread for each expert; select_kernel<2> has room for 512");
 constexpr int kWaves = 8;
 
 // A workgroup has MT tokens and ET experts; its threads take 8 channels at a time.
@@ -127,72 +127,97 @@ __global__ __launch_bounds__(1024) void select_kernel(const MoeRoute r) {
   }
 }
 
-// The same in one workgroup, a thread to each (token, expert) pair, for up to kOneGroup of them; then, with t, the tables
-// of the experts' products: a launch less.
+// The same in one workgroup, a thread to each (token, expert) pair, for up to kOneGroup of them; and, with TABLES, the
+// tables of the experts' products: a launch less. While some waves work out the weights, others count.
 constexpr int kOneGroup = 1024;
 template <bool TABLES>
-__global__ __launch_bounds__(1024) void select_one_kernel(const MoeRoute r, const MoeTables t) {
-  __shared__ union {
-    struct {
-      double key[kOneGroup], share[kOneGroup];
-    };
-    TableWork work;
-  } s;
+__global__ __launch_bounds__(kOneGroup) void select_one_kernel(const MoeRoute r, const MoeTables t) {
+  __shared__ double key[kOneGroup], share[kOneGroup];
+  __shared__ TableWork work;
   __shared__ int ids[kMaxM * kMaxK];
   __shared__ double chosen[kMaxM * kMaxK];
   __shared__ float weights[kMaxM * kMaxK];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = tid / r.E, e = tid - m * r.E;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = tid / r.E, e = tid - m * r.E, pairs = r.M * r.top_k;
   const bool live = m < r.M;
   const double logit = live ? r.logits[tid] : 0.0;
   const double mine = logit == logit ? logit : -__builtin_inf();  // a NaN ranks as minus infinity
-  s.key[tid] = mine;
+  key[tid] = mine;
+  if (TABLES && tid < PARO_MOE_MAX_E) work.mask[tid] = 0;
   __syncthreads();
   if (live) {
     int rank = 0;
-    const double* const row = s.key + m * r.E;
+    const double* const row = key + m * r.E;
 #pragma unroll 8
     for (int o = 0; o < r.E; ++o) rank += row[o] > mine || (row[o] == mine && o < e);
     if (rank < r.top_k) {
       ids[m * r.top_k + rank] = e;
       chosen[m * r.top_k + rank] = logit;
+      if (TABLES) atomicOr(&work.mask[e], 1ull << m);  // (in any order the same)
     }
   }
   __syncthreads();
-  if (live && !r.sigmoid) s.share[tid] = exp(logit - s.key[m * r.E + ids[m * r.top_k]]);
+  if (live && !r.sigmoid) share[tid] = exp(logit - key[m * r.E + ids[m * r.top_k]]);
   __syncthreads();
-  for (int at = wave; at < r.M; at += 16) {  // a wave for each token
-    double sum = 0;
-    if (!r.sigmoid) {
-      for (int o = lane; o < r.E; o += 64) sum += s.share[at * r.E + o];
+  TablePlace place{};
+  if (TABLES && tid < PARO_MOE_MAX_E) {
+    place = tables_count(work);
+  } else {
+    constexpr int kFirst = TABLES ? PARO_MOE_MAX_E / 64 : 0;
+    for (int at = wave - kFirst; at < r.M; at += kOneGroup / 64 - kFirst) {  // a wave for each token
+      double sum = 0;
+      if (!r.sigmoid) {
+        for (int o = lane; o < r.E; o += 64) sum += share[at * r.E + o];
 #pragma unroll
-      for (int d = 32; d; d /= 2) sum += __shfl_xor(sum, d);
+        for (int d = 32; d; d /= 2) sum += __shfl_xor(sum, d);
+      }
+      const int p = at * r.top_k + lane;
+      double w = 0;
+      if (lane < r.top_k) w = r.sigmoid ? 1.0 / (1.0 + exp(-chosen[p])) : share[at * r.E + ids[p]] / sum;
+      double all = 0;
+      for (int j = 0; j < r.top_k; ++j) all += __shfl(w, j);
+      if (lane < r.top_k) weights[p] = float(r.renormalize ? w / all : w);
     }
-    const int p = at * r.top_k + lane;
-    double w = 0;
-    if (lane < r.top_k) w = r.sigmoid ? 1.0 / (1.0 + exp(-chosen[p])) : s.share[at * r.E + ids[p]] / sum;
-    double all = 0;
-    for (int j = 0; j < r.top_k; ++j) all += __shfl(w, j);
-    if (lane < r.top_k) weights[p] = float(r.renormalize ? w / all : w);
   }
   __syncthreads();
-  const int pairs = r.M * r.top_k;
-  for (int p = tid; p < pairs; p += 1024) {
+  if (TABLES && tid < PARO_MOE_MAX_E) tables_units(work, place, t);
+  for (int p = tid; p < pairs; p += kOneGroup) {
     r.ids[p] = ids[p];
     r.weights[p] = weights[p];
   }
-  if constexpr (TABLES) make_tables(s.work, r.M, r.E, r.top_k, ids, weights, t);
+  if constexpr (TABLES) {
+    __syncthreads();
+    tables_slots(work, r.M, r.E, r.top_k, ids, weights, t);
+  }
 }
 
-__global__ __launch_bounds__(512) void group_kernel(int M, int E, int top_k, const int32_t* given_ids, const float* given_weights,
-                                                    const MoeTables t) {
+__global__ __launch_bounds__(PARO_MOE_MAX_E) void group_kernel(int M, int E, int top_k, const int32_t* given_ids,
+                                                               const float* given_weights, const MoeTables t) {
   __shared__ TableWork work;
   __shared__ int ids[kMaxM * kMaxK];
   __shared__ float weights[kMaxM * kMaxK];
-  for (int p = threadIdx.x; p < M * top_k; p += 512) {
-    ids[p] = given_ids[p];
-    weights[p] = given_weights[p];
+  const int tid = threadIdx.x;
+  constexpr int kEach = kMaxM * kMaxK / PARO_MOE_MAX_E;
+  int id[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int p = tid + i * PARO_MOE_MAX_E;
+    id[i] = -1;
+    if (p < M * top_k) {
+      ids[p] = id[i] = given_ids[p];
+      weights[p] = given_weights[p];
+    }
   }
-  make_tables(work, M, E, top_k, ids, weights, t);  // (which begins with a barrier)
+  work.mask[tid] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kEach; ++i)
+    if (uint32_t(id[i]) < uint32_t(E)) atomicOr(&work.mask[id[i]], 1ull << ((tid + i * PARO_MOE_MAX_E) / top_k));  // (in any order the same)
+  __syncthreads();
+  const TablePlace place = tables_count(work);
+  __syncthreads();
+  tables_units(work, place, t);
+  __syncthreads();
+  tables_slots(work, M, E, top_k, ids, weights, t);
 }
 
 template <int MT, int ET>
@@ -232,7 +257,7 @@ hipError_t launch_moe_select(const MoeRoute& r, const MoeTables* t, hipStream_t 
 }
 
 hipError_t launch_moe_group(int M, int E, int top_k, const int32_t* ids, const float* weights, const MoeTables& t, hipStream_t st) {
-  hipLaunchKernelGGL(group_kernel, dim3(1), dim3(512), 0, st, M, E, top_k, ids, weights, t);
+  hipLaunchKernelGGL(group_kernel, dim3(1), dim3(PARO_MOE_MAX_E), 0, st, M, E, top_k, ids, weights, t);
   return hipGetLastError();
 }
 

@@ -1,4 +1,5 @@
-// Which tokens go to which experts, made by one workgroup from the ids.
+// Which tokens go to which experts, made by one workgroup from masks of the experts' tokens, in three steps with a
+// barrier of all its threads before each.
 #pragma once
 
 #include "moe_internal.h"
@@ -8,54 +9,47 @@ namespace paro {
 struct TableWork {
   unsigned long long mask[PARO_MOE_MAX_E];  // an expert's tokens
   int first[PARO_MOE_MAX_E];                // its first slot
-  int slots[8], units[8];                   // of 64 experts each
+  uint32_t totals[PARO_MOE_MAX_E / 64];     // of 64 experts each: slots, and units in the upper half
 };
 
-// All threads of the workgroup (512 at least); ids and weights [M][top_k] in LDS.
-__device__ inline void make_tables(TableWork& s, int M, int E, int top_k, const int* ids, const float* weights, const MoeTables& t) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 63, wave = tid >> 6, pairs = M * top_k;
-  __syncthreads();
-  if (tid < PARO_MOE_MAX_E) s.mask[tid] = 0;
-  __syncthreads();
-  for (int p = tid; p < pairs; p += nt)
-    if (uint32_t(ids[p]) < uint32_t(E)) atomicOr(&s.mask[ids[p]], 1ull << (p / top_k));  // (in any order the same)
-  __syncthreads();
-  int n = 0, slot = 0, unit = 0;  // of the thread's expert, then what lies before it in its 64
-  if (tid < PARO_MOE_MAX_E) {
-    n = int(__popcll(s.mask[tid]));
-    slot = n;
-    unit = (n + 15) / 16;
+// Threads 0..511, one for each expert: what it and those before it in its 64 have.
+struct TablePlace {
+  int count;
+  uint32_t before;  // slots, and units in the upper half
+};
+__device__ inline TablePlace tables_count(TableWork& s) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  TablePlace p;
+  p.count = int(__popcll(s.mask[tid]));
+  const uint32_t own = uint32_t(p.count) | uint32_t((p.count + 15) / 16) << 16;
+  uint32_t sum = own;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int a = __shfl_up(slot, d), b = __shfl_up(unit, d);
-      if (lane >= d) {
-        slot += a;
-        unit += b;
-      }
-    }
-    if (lane == 63) {
-      s.slots[wave] = slot;
-      s.units[wave] = unit;
-    }
-    slot -= n;
-    unit -= (n + 15) / 16;
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(sum, d);
+    if (lane >= d) sum += o;
   }
-  __syncthreads();
-  if (tid < PARO_MOE_MAX_E) {
-    int all = unit;
-    for (int w = 0; w < PARO_MOE_MAX_E / 64; ++w) {
-      if (w < wave) {
-        slot += s.slots[w];
-        unit += s.units[w];
-      }
-      all = w == 0 ? s.units[0] : all + s.units[w];
-    }
-    s.first[tid] = slot;
-    for (int f = 0; f < n; f += 16) t.unit[unit++] = MoeUnit{tid, slot + f, min(16, n - f)};
-    if (tid == 0) *t.units = all;
+  if (lane == 63) s.totals[wave] = sum;
+  p.before = sum - own;
+  return p;
+}
+// The same threads: units, and the experts' first slots.
+__device__ inline void tables_units(TableWork& s, const TablePlace& p, const MoeTables& t) {
+  const int tid = threadIdx.x, wave = tid >> 6;
+  uint32_t before = p.before, all = 0;
+#pragma unroll
+  for (int w = 0; w < PARO_MOE_MAX_E / 64; ++w) {
+    if (w < wave) before += s.totals[w];
+    all += s.totals[w];
   }
-  __syncthreads();
-  for (int p = tid; p < pairs; p += nt) {
+  const int slot = int(before & 0xFFFFu);
+  int unit = int(before >> 16);
+  s.first[tid] = slot;
+  for (int f = 0; f < p.count; f += 16) t.unit[unit++] = MoeUnit{tid, slot + f, min(16, p.count - f)};
+  if (tid == 0) *t.units = int(all >> 16);
+}
+// All threads: the slots.
+__device__ inline void tables_slots(const TableWork& s, int M, int E, int top_k, const int* ids, const float* weights, const MoeTables& t) {
+  for (int p = threadIdx.x; p < M * top_k; p += blockDim.x) {
     const int e = ids[p], m = p / top_k;
     if (uint32_t(e) >= uint32_t(E)) continue;
     float w = 0;

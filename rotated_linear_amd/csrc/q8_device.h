@@ -177,17 +177,14 @@ __device__ inline float load_element(const void* p, size_t i, int ydtype) {
   const uint32_t h = static_cast<const uint16_t*>(p)[i];
   return ydtype == PARO_F16 ? from_bits16<PARO_F16>(h) : from_bits16<PARO_BF16>(h);
 }
-// y[m][n] of a call with an epilogue, from its product.
-__device__ inline float epilogue(const W8A8Call& c, float v, int m, int n) {
-  if (c.bias) v = plus(v, load_element(c.bias, n, c.ydtype));
-  float o[1] = {v};
+// An output of a call with an epilogue, from its product, its bias (0 without one) and what there is of a residual.
+__device__ inline float epilogue(const W8A8Call& c, float v, float bias, float residual) {
+  float o[1] = {plus(v, bias)};
   if (c.ydtype == PARO_F32)
     activate<PARO_F32>(o, c.act);
   else
     activate<PARO_F16>(o, c.act);
-  v = o[0];
-  if (c.residual) v = plus(v, load_element(c.residual, size_t(m) * c.N + n, c.ydtype));
-  return v;
+  return c.residual ? plus(o[0], residual) : o[0];
 }
 
 }  // namespace paro

@@ -55,6 +55,18 @@ __global__ __launch_bounds__(64 * W) void w8a8_column_kernel(const W8A8Call c) {
       dma16(lds + buf * STAGE + i * 1024, voff[i], (i < 2 * FM ? xb : i < 2 * FM + 2 ? wb : ub) + k);
   };
 
+  // An epilogue's operands, on their way while the sums are formed.
+  constexpr int OUTS = (FM * 256 + 64 * W - 1) / (64 * W);  // outputs of a thread
+  float bias[OUTS], res[OUTS];
+  if constexpr (KIND == kEpilogue) {
+#pragma unroll
+    for (int i = 0; i < OUTS; ++i) {
+      const int o = threadIdx.x + i * 64 * W, n = n0 + o % 16, m = o / 16;
+      bias[i] = c.bias && n < c.N ? load_element(c.bias, n, c.ydtype) : 0.0f;
+      res[i] = c.residual && n < c.N && m < c.M ? load_element(c.residual, size_t(m) * c.N + n, c.ydtype) : 0.0f;
+    }
+  }
+
   i32x4 acc[WN][FM];
 #pragma unroll
   for (int j = 0; j < WN; ++j)
@@ -105,9 +117,10 @@ __global__ __launch_bounds__(64 * W) void w8a8_column_kernel(const W8A8Call c) {
     for (int f = 0; f < FM; ++f) red[(j * FM * 16 + f * 16 + (lane & 15)) * 4 + (lane >> 4)] = acc[j][f];
   __syncthreads();
   const int* const sums = reinterpret_cast<const int*>(smem);
-  for (int o = threadIdx.x; o < 16 * c.M; o += 64 * W) {
-    const int n = n0 + o % 16, m = o / 16;
-    if (n >= c.N) continue;
+#pragma unroll
+  for (int i = 0; i < OUTS; ++i) {
+    const int o = threadIdx.x + i * 64 * W, n = n0 + o % 16, m = o / 16;
+    if (n >= c.N || m >= c.M) continue;
     int v[WN];
 #pragma unroll
     for (int j = 0; j < WN; ++j) {
@@ -121,7 +134,7 @@ __global__ __launch_bounds__(64 * W) void w8a8_column_kernel(const W8A8Call c) {
       const float u = scaled(v[1], xs, c.ws[size_t(c.N) + n]);
       y = c.ydtype == PARO_F32 ? silu_mul<PARO_F32>(y, u) : silu_mul<PARO_F16>(y, u);
     }
-    if constexpr (KIND == kEpilogue) y = epilogue(c, y, m, n);
+    if constexpr (KIND == kEpilogue) y = epilogue(c, y, bias[i], res[i]);
     const size_t at = size_t(m) * c.N + n;
     if (c.ydtype == PARO_F32)
       static_cast<float*>(c.y)[at] = y;

@@ -17,6 +17,8 @@
 // The steps, at 8192^3: 256 x 256 tiles in four waves 575 us; in eight, reads between the products 507;
 // results through LDS and the scales read from there 481; stages of 128 channels, two of them, instead
 // of four of 64 464; loads that pass the ends of tiles 457; the 16 x 16 x 64 product 417.
+#include <stddef.h>
+
 #include <algorithm>
 #include <cmath>
 
@@ -69,6 +71,10 @@ struct Tile {
   static constexpr int XS = BM < 64 ? 64 : BM;    // scales of x rows (64 at least: they come 64 a load)
   static constexpr int LDS = SCALES + (XS + BN) * 4;
   static_assert(XS % 64 == 0 && BN % 64 == 0 && LDS <= 160 * 1024, "scales 64 a load; one CU's LDS");
+  // With an epilogue, each wave's bias in float32 behind the scales.
+  static constexpr int BIAS = LDS, WCOLS = FN * 16;
+  static constexpr int LDS_EPILOGUE = BIAS + NW * WCOLS * 4;
+  static_assert(WCOLS <= 64 && 160 * 1024 / LDS_EPILOGUE == 160 * 1024 / LDS, "a lane to each; no workgroup less on a CU");
 };
 
 // Where a tile lies.
@@ -238,11 +244,13 @@ __device__ inline void store_tile(const GemmArgs& a, const Place& p, const i32x4
   }
 }
 
-// The same for a call with an epilogue. The residual is read as the lanes hold their sums, four columns of a row
-// each, a piece ahead of the one that is worked on. One copy of the activations serves every piece (unrolled over
-// the pieces they would not fit the instruction cache), so a piece's sums are first moved to registers of their own.
-template <class T, int DT>
-__device__ inline void store_tile_epilogue(const W8A8Call& c, const Place& p, const i32x4 (&acc)[T::FM][T::FN], char* smem, int wave) {
+// The same for a call with an epilogue. The residual is read as the lanes hold their sums, four columns of a row each, a
+// piece ahead of the one that is worked on. With one tile for each CU this code runs once, from a cold instruction cache,
+// so that its length counts (4096 x 14336 -> 4096 with a residual: 234 us with the pieces unrolled, 223 with the
+// activations in the way): one copy of it serves all pieces, whose sums are first moved to registers of their own, and
+// ACT, with an activation, is another. bias: of the wave's column `lane`.
+template <class T, int DT, bool ACT>
+__device__ inline void store_tile_epilogue(const W8A8Call& c, const Place& p, const i32x4 (&acc)[T::FM][T::FN], char* smem, int wave, float bias) {
   const int lane = fresh_lane();
   constexpr int EB = DT == PARO_F32 ? 4 : 2;
   constexpr int CF = T::FN < 4 / EB ? T::FN : 4 / EB;  // column and row fragments of a piece
@@ -251,8 +259,9 @@ __device__ inline void store_tile_epilogue(const W8A8Call& c, const Place& p, co
   const int wm = wave / T::WN, wn = wave % T::WN;
   char* const buf = smem + T::OUT + wave * T::PR * T::EP;
   const float* const sc = reinterpret_cast<const float*>(smem + T::SCALES);
+  float* const bs = reinterpret_cast<float*>(smem + T::BIAS) + wave * T::WCOLS;
   const bool whole = c.N % (16 / EB) == 0;
-  const int mw = wm * T::FM * 16, nw = wn * T::FN * 16;  // the wave's first row and column in the tile
+  const int mw = wm * T::FM * 16, nw = wn * T::WCOLS;  // the wave's first row and column in the tile
   Four<DT> res[RF][CF], next[RF][CF];
   // (only elements of y: in place of the residual, the others are another workgroup's to write)
   auto fetch = [&](int piece) {
@@ -266,6 +275,9 @@ __device__ inline void store_tile_epilogue(const W8A8Call& c, const Place& p, co
       }
   };
   if (c.residual) fetch(0);
+  if (lane < T::WCOLS) bs[lane] = bias;  // (0 without one)
+  // one wave's LDS accesses are carried out in order; the compiler keeps them in order too
+  asm volatile("" ::: "memory");
 #pragma unroll 1
   for (int piece = 0; piece < PIECES; ++piece) {
     i32x4 sum[RF][CF];
@@ -277,12 +289,6 @@ __device__ inline void store_tile_epilogue(const W8A8Call& c, const Place& p, co
 #pragma unroll
           for (int k = 0; k < CF; ++k) sum[u][k] = acc[q / ROW * RF + u][q % ROW * CF + k];
       }
-    const int mf = mw + piece / ROW * RF * 16, nf = nw + piece % ROW * CF * 16;
-    Four<DT> bias[CF];
-    if (c.bias) {
-#pragma unroll
-      for (int k = 0; k < CF; ++k) bias[k] = load4<DT>(c.bias, 0, p.n0 + nf + k * 16 + 4 * (lane >> 4), c.N);
-    }
     if (c.residual) {
 #pragma unroll
       for (int u = 0; u < RF; ++u)
@@ -290,48 +296,69 @@ __device__ inline void store_tile_epilogue(const W8A8Call& c, const Place& p, co
         for (int k = 0; k < CF; ++k) res[u][k] = next[u][k];
       if (piece + 1 < PIECES) fetch(piece + 1);
     }
+    const int mf = mw + piece / ROW * RF * 16, nf = piece % ROW * CF * 16;
     float v[RF * CF * 4];
 #pragma unroll
     for (int k = 0; k < CF; ++k) {
-      const float4 w4 = *reinterpret_cast<const float4*>(sc + T::XS + nf + k * 16 + 4 * (lane >> 4));
-      const float ws[4] = {w4.x, w4.y, w4.z, w4.w};
+      const int at = nf + k * 16 + 4 * (lane >> 4);
+      const float4 w4 = *reinterpret_cast<const float4*>(sc + T::XS + nw + at), b4 = *reinterpret_cast<const float4*>(bs + at);
+      const float ws[4] = {w4.x, w4.y, w4.z, w4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int u = 0; u < RF; ++u) {
         const float xs = sc[mf + u * 16 + (lane & 15)];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float& o = v[(u * CF + k) * 4 + e];
-          o = scaled(sum[u][k][e], xs, ws[e]);
-          if (c.bias) o = plus(o, element<DT>(bias[k], e));
-        }
+        for (int e = 0; e < 4; ++e) v[(u * CF + k) * 4 + e] = plus(scaled(sum[u][k][e], xs, ws[e]), b[e]);
       }
     }
-    activate<DT>(v, c.act);
+    if constexpr (ACT) activate<DT>(v, c.act);
+    if (c.residual) {
+#pragma unroll
+      for (int u = 0; u < RF; ++u)
+#pragma unroll
+        for (int k = 0; k < CF; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[(u * CF + k) * 4 + e] = plus(v[(u * CF + k) * 4 + e], element<DT>(res[u][k], e));
+    }
 #pragma unroll
     for (int u = 0; u < RF; ++u)
 #pragma unroll
       for (int k = 0; k < CF; ++k) {
-        float o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          o[e] = v[(u * CF + k) * 4 + e];
-          if (c.residual) o[e] = plus(o[e], element<DT>(res[u][k], e));
-        }
-        put4<DT>(buf + (u * 16 + (lane & 15)) * T::EP + (16 * k + 4 * (lane >> 4)) * EB, o);
+        const float* const o = v + (u * CF + k) * 4;
+        const float o4[4] = {o[0], o[1], o[2], o[3]};
+        put4<DT>(buf + (u * 16 + (lane & 15)) * T::EP + (16 * k + 4 * (lane >> 4)) * EB, o4);
       }
-    // one wave's LDS accesses are carried out in order; the compiler keeps them in order too
     asm volatile("" ::: "memory");
-    store_piece<EB, T::EP, CF * 16 * EB, T::PR>(buf, static_cast<char*>(c.y) + (size_t(p.m0 + mf) * c.N + p.n0 + nf) * EB,
-                                                size_t(c.N) * EB, c.M - p.m0 - mf, c.N - p.n0 - nf, whole, lane);
+    store_piece<EB, T::EP, CF * 16 * EB, T::PR>(buf, static_cast<char*>(c.y) + (size_t(p.m0 + mf) * c.N + p.n0 + nw + nf) * EB,
+                                                size_t(c.N) * EB, c.M - p.m0 - mf, c.N - p.n0 - nw - nf, whole, lane);
     asm volatile("" ::: "memory");
   }
 }
 
+// The kernel's arguments, read again here: kept from the start, those that only the epilogue wants would take scalar
+// registers from the main loop, which then keeps its own in lanes of vector registers.
+__device__ inline W8A8Call call_again() {
+  uintptr_t p = uintptr_t(__builtin_amdgcn_kernarg_segment_ptr());
+  asm volatile("" : "+s"(p));
+  const auto k = (const __attribute__((address_space(4))) W8A8Call*)p;
+  W8A8Call c{};
+  c.M = k->M;
+  c.N = k->N;
+  c.y = k->y;
+  c.act = k->act;
+  c.residual = k->residual;
+  return c;
+}
+static_assert(offsetof(GemmArgs, c) == 0, "the call lies where the arguments begin");
+
 template <class T, Output KIND, int DT>
-__device__ inline void store_outputs(const GemmArgs& a, const Place& p, const i32x4 (&acc)[T::FM][T::FN], char* smem, int wave) {
-  if constexpr (KIND == kEpilogue)
-    store_tile_epilogue<T, DT>(a.c, p, acc, smem, wave);
-  else
+__device__ inline void store_outputs(const GemmArgs& a, const Place& p, const i32x4 (&acc)[T::FM][T::FN], char* smem, int wave, float bias) {
+  if constexpr (KIND == kEpilogue) {
+    const W8A8Call c = call_again();
+    if (c.act == PARO_ACT_NONE)
+      store_tile_epilogue<T, DT, false>(c, p, acc, smem, wave, bias);
+    else
+      store_tile_epilogue<T, DT, true>(c, p, acc, smem, wave, bias);
+  } else
     store_tile<T, KIND, DT, false>(a, p, acc, smem, wave);
 }
 
@@ -452,6 +479,11 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
     for (int i = 0; i < T::FM; ++i)
 #pragma unroll
       for (int j = 0; j < T::FN; ++j) acc[i][j] = i32x4{};
+    float bias = 0;  // asked for long before it is used
+    if constexpr (KIND == kEpilogue) {
+      const int col = wn * T::WCOLS + fresh_lane();
+      if (c.bias && !a.part && col < (wn + 1) * T::WCOLS && p.n0 + col < c.N) bias = load_element(c.bias, p.n0 + col, c.ydtype);
+    }
     for (int t = 0; t < p.steps; ++t) {
       const uint32_t nbuf = buf + 1 == T::S ? 0 : buf + 1;
 #pragma unroll
@@ -492,11 +524,15 @@ __global__ __launch_bounds__(T::NT) void w8a8_gemm_kernel(const GemmArgs a) {
     if (a.part)
       store_tile<T, KIND, PARO_F32, true>(a, p, acc, smem, wave);
     else if (c.ydtype == PARO_F32)
-      store_outputs<T, KIND, PARO_F32>(a, p, acc, smem, wave);
+      store_outputs<T, KIND, PARO_F32>(a, p, acc, smem, wave, bias);
     else if (c.ydtype == PARO_F16)
-      store_outputs<T, KIND, PARO_F16>(a, p, acc, smem, wave);
+      store_outputs<T, KIND, PARO_F16>(a, p, acc, smem, wave, bias);
     else
-      store_outputs<T, KIND, PARO_BF16>(a, p, acc, smem, wave);
+      store_outputs<T, KIND, PARO_BF16>(a, p, acc, smem, wave, bias);
+    if constexpr (KIND == kEpilogue) {  // read again: not kept in registers across the epilogue, which wants them
+      read_w(buf, 0);
+      read_x(buf, 0);
+    }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // loads past the last stage land before the LDS is given up
 }
@@ -539,12 +575,10 @@ __global__ __launch_bounds__(256) void reduce_kernel(const W8A8Call c, const int
       if constexpr (GATED) v[e] = silu_mul<DT>(v[e], scaled(u[e], xs, c.ws[size_t(c.N) + n + e]));
     }
     if constexpr (KIND == kEpilogue) {
-      float w[V];
-      if (c.bias) {
-        load_elements<DT, V>(c.bias, n, w);
+      float w[V] = {};
+      if (c.bias) load_elements<DT, V>(c.bias, n, w);
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = plus(v[e], w[e]);
-      }
+      for (int e = 0; e < V; ++e) v[e] = plus(v[e], w[e]);
       activate<DT>(v, c.act);
       if (c.residual) {
         load_elements<DT, V>(c.residual, m * c.N + n, w);
@@ -593,9 +627,10 @@ hipError_t launch_tile(const W8A8Call& c, int* part, int splits, hipStream_t st)
   a.splits = (steps + a.steps_per_split - 1) / a.steps_per_split;  // every split has steps
   a.part = a.splits > 1 ? part : nullptr;
   const void* fn = reinterpret_cast<const void*>(&w8a8_gemm_kernel<T, KIND>);
-  if (hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, T::LDS)) return e;
+  constexpr int lds = KIND == kEpilogue ? T::LDS_EPILOGUE : T::LDS;
+  if (hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds)) return e;
   const long total = long(a.tiles_m) * a.tiles_n * a.splits;
-  hipLaunchKernelGGL((w8a8_gemm_kernel<T, KIND>), dim3(unsigned(std::min<long>(total, tiling<T>().workgroups))), dim3(T::NT), T::LDS, st, a);
+  hipLaunchKernelGGL((w8a8_gemm_kernel<T, KIND>), dim3(unsigned(std::min<long>(total, tiling<T>().workgroups))), dim3(T::NT), lds, st, a);
   if (hipError_t e = hipGetLastError()) return e;
   return a.part ? launch_reduce<KIND>(c, part, a.splits, st) : hipSuccess;
 }

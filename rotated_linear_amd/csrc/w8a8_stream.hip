@@ -97,7 +97,9 @@ __global__ __launch_bounds__(64 * W) void w8a8_stream_kernel(const W8A8Call c) {
       const float u = scaled(sum(t + YT), xs, c.ws[size_t(c.N) + n]);
       v = c.ydtype == PARO_F32 ? silu_mul<PARO_F32>(v, u) : silu_mul<PARO_F16>(v, u);
     }
-    if constexpr (KIND == kEpilogue) v = epilogue(c, v, m, n);
+    if constexpr (KIND == kEpilogue)
+      v = epilogue(c, v, c.bias ? load_element(c.bias, n, c.ydtype) : 0.0f,
+                   c.residual ? load_element(c.residual, size_t(m) * c.N + n, c.ydtype) : 0.0f);
     const size_t at = size_t(m) * c.N + n;
     if (c.ydtype == PARO_F32)
       static_cast<float*>(c.y)[at] = v;

@@ -1,6 +1,8 @@
 """The mixture-of-experts calls on the GPU against their float64 oracle: the router with its ties and odd rows, the
 experts over token counts, ids and sizes, the layer as a whole, and a decoder block's run of all of it.
 """
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -49,7 +51,22 @@ def check(y, want, bound, half):
 SIZES = [  # M, D, F, E, top_k
     (1, 128, 128, 1, 1), (1, 2048, 1024, 64, 8), (2, 256, 384, 4, 2), (3, 1152, 128, 7, 3), (5, 128, 2176, 5, 5), (13, 640, 256, 60, 4),
     (16, 512, 512, 3, 2), (17, 256, 128, 2, 1), (33, 384, 640, 4, 3), (48, 256, 256, 512, 16), (64, 256, 384, 16, 8), (64, 128, 128, 1, 1),
-    (64, 1024, 128, 2, 2), (7, 4096, 1408, 9, 2), (4, 256, 14336, 3, 2), (4, 16384, 256, 3, 2), (31, 768, 896, 40, 6)]
+    (64, 1024, 128, 2, 2), (7, 4096, 1408, 9, 2), (4, 256, 14336, 3, 2), (4, 16384, 256, 3, 2), (31, 768, 896, 40, 6),
+    (3, 2560, 256, 5, 2), (9, 5120, 256, 3, 2), (5, 8192, 128, 3, 1), (40, 10368, 128, 3, 2), (64, 768, 1408, 24, 6), (50, 2048, 640, 30, 4)]
+
+
+def down_plan(*size):
+    """(16-column tiles of a workgroup, workgroups that share them) of the down product."""
+    out = [ctypes.c_int() for _ in range(2)]
+    rl.lib().paro_internal_moe_down_plan(*size, *map(ctypes.byref, out))
+    return tuple(v.value for v in out)
+
+
+def test_the_sizes_reach_every_kernel():
+    plans = {down_plan(*s) for s in SIZES}
+    assert {t for t, s in plans if s == 1} >= {1, 4} and {t for t, s in plans if s > 1} == {1, 2, 4}
+    # the gate and up product: four, eight or sixteen waves by the groups of channels, one to four of them to a wave, or any number
+    assert {min(65, D // 128) for _, D, _, _, _ in SIZES} >= {1, 2, 4, 5, 6, 8, 9, 16, 20, 32, 40, 64, 65}
 
 
 @pytest.mark.parametrize("M,D,F,E,k", SIZES)
