@@ -26,8 +26,8 @@ Layout layout(int M, int D, int F, int E, int top_k) {
   };
   const size_t pairs = size_t(M) * top_k;
   l.logits = take(size_t(M) * E * 8);
-  l.x = take(size_t(M) * D * 2);
-  l.a = take(pairs * F * 2);
+  l.x = take(size_t(M) * D * 4);
+  l.a = take(pairs * F * 4);  // (float32 where a transform follows)
   l.a_rotated = take(pairs * F * 2);
   const int splits = moe_down_plan(M, D, F, E, top_k).splits;
   l.part = take(splits > 1 ? size_t(splits) * M * D * 4 : 0);
@@ -96,8 +96,8 @@ paro_status experts(int M, int D, int F, int E, int top_k, const void* x, const 
   c.dn_qw = down->qweight;
   c.dn_sc = static_cast<const uint16_t*>(down->scales);
   c.dn_zr = static_cast<const uint16_t*>(down->zeros);
-  c.a = reinterpret_cast<uint16_t*>(base + l.a);
-  c.a_down = c.a;
+  c.a = base + l.a;
+  c.a_down = reinterpret_cast<const uint16_t*>(c.a);
   c.a_fragments = rot_a == nullptr;
   c.part = reinterpret_cast<float*>(base + l.part);
   c.t = MoeTables{reinterpret_cast<int*>(base + l.units), reinterpret_cast<MoeUnit*>(base + l.unit), reinterpret_cast<MoeSlot*>(base + l.slot)};
@@ -115,15 +115,15 @@ paro_status experts(int M, int D, int F, int E, int top_k, const void* x, const 
   }
   if (e == hipSuccess && rot_x) {
     uint16_t* const xr = reinterpret_cast<uint16_t*>(base + l.x);
-    e = launch_rotate(rx, M, c.x, xr, true, st);
+    e = launch_rotate_parts(rx, M, c.x, xr, st);
     c.x = xr;
-    c.x_nibble_order = true;
+    c.x_parts = true;
   }
   if (e == hipSuccess) e = launch_moe_gate_up(c, st);
   if (e == hipSuccess && rot_a) {
     // (every row there may be: those of pairs without an expert hold what they held, and no product reads them)
     uint16_t* const ar = reinterpret_cast<uint16_t*>(base + l.a_rotated);
-    e = launch_rotate(ra, M * top_k, c.a, ar, true, st);
+    e = launch_rotate_f32(ra, M * top_k, static_cast<const float*>(c.a), ar, st);
     c.a_down = ar;
   }
   if (e == hipSuccess) e = launch_moe_down(c, st);

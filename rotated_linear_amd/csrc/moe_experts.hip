@@ -18,15 +18,20 @@ struct Rows {
 };
 
 // sum[row of x][row of w] += the group's products. sz: the scale and, in the upper half, the zero of the lane's row.
-__device__ inline void group_product(const uint4& w, uint32_t sz, const Rows& a, f4& sum) {
+// PARTS: a[0] and a[PARTS - 1] are the rows' upper and lower parts, else there is a[0] alone.
+template <int PARTS = 1>
+__device__ inline void group_product(const uint4& w, uint32_t sz, const Rows* a, f4& sum) {
   const _Float16 z = __builtin_bit_cast(_Float16, uint16_t(sz >> 16));
   const _Float16 zl = -(static_cast<_Float16>(1024.0f) + z), zh = -(static_cast<_Float16>(64.0f) + z);
   const h2 zlo = {zl, zl}, zhi = {zh, zh};
   const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
   f4 g = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[k], dequant_word(wv[k], zlo, zhi, 0x000F000Fu, 0x00F000F0u, 0x64006400u), g, 0, 0, 0);
+  for (int k = 0; k < 4; ++k) {
+    const h8 b = dequant_word(wv[k], zlo, zhi, 0x000F000Fu, 0x00F000F0u, 0x64006400u);
+    g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0].v[k], b, g, 0, 0, 0);
+    if constexpr (PARTS == 2) g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1].v[k], b, g, 0, 0, 0);
+  }
   const float s = static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(sz)));
 #pragma unroll
   for (int i = 0; i < 4; ++i) sum[i] = __builtin_fmaf(s, g[i], sum[i]);
@@ -95,8 +100,9 @@ __device__ inline int fragment_place(int n) {
 // in registers (GW = 0: any number, w, w + W, ..., read again for each tile). Weights come straight into a ring of
 // registers, R groups ahead, from tile to tile without a break: a tile's gate rows, then its up rows. Every kPark
 // tiles, and where the unit ends, the waves' sums meet in LDS.
+// PARTS = 2: the tokens' rows come from a transform, in two float16 parts, and take twice the registers and products.
 constexpr int kPark = 4;
-template <int W, int GW>
+template <int W, int GW, int PARTS>
 __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
   constexpr int R = GW == 1 ? 2 : GW == 3 ? 6 : 4;
   constexpr int S = GW ? 2 * GW : R;  // steps of a tile
@@ -173,18 +179,23 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
   }
   __builtin_amdgcn_sched_barrier(0);
 
-  Rows a[GW ? GW : 2];
+  Rows a[GW ? GW : 2][PARTS];
   int unit = begin / per_unit, tile = begin - unit * per_unit, first = 0, count = 0;
   uint32_t xo = 0;
   // a group of the unit's tokens; past the last one zeros, so that its products are
-  auto rows = [&](int q, int i) { load_rows(a[q], c.x + size_t(group(i)) * PARO_GROUP, xo); };
+  auto rows = [&](int q, int i) {
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) load_rows(a[q][p], c.x + size_t(p) * c.M * c.D + size_t(group(i)) * PARO_GROUP, xo);
+  };
   auto settle = [&](int q, int i) {
     const bool in = (GW ? wave * GW + i : wave + W * i) < G;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const u4 v = __builtin_bit_cast(u4, c.x_nibble_order ? a[q].v[k] : decode_order(a[q].v[k]));
-      a[q].v[k] = __builtin_bit_cast(h8, in ? v : u4{0u, 0u, 0u, 0u});
-    }
+    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const u4 v = __builtin_bit_cast(u4, PARTS == 2 ? a[q][p].v[k] : decode_order(a[q][p].v[k]));
+        a[q][p].v[k] = __builtin_bit_cast(h8, in ? v : u4{0u, 0u, 0u, 0u});
+      }
   };
   auto tokens = [&]() {
     first = __builtin_amdgcn_readfirstlane(c.t.unit[unit].first);
@@ -213,7 +224,7 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
       for (int s = 0; s < S; ++s) {
         __builtin_amdgcn_sched_barrier(0);
         if (s % GW == 0) spread(s / GW);
-        group_product(w[s % R], sz[s % GW], a[s % GW], acc[s / GW]);
+        group_product<PARTS>(w[s % R], sz[s % GW], a[s % GW], acc[s / GW]);
         settled(acc[s / GW]);
         if (s % GW == GW - 1) park(s / GW);
         __builtin_amdgcn_sched_barrier(0);
@@ -226,8 +237,8 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
         for (int p = 0; p < 2; ++p) {
           __builtin_amdgcn_sched_barrier(0);
           settle(p, i + p);
-          group_product(w[2 * p], scale[2 * p] | zero[2 * p] << 16, a[p], acc[0]);
-          group_product(w[2 * p + 1], scale[2 * p + 1] | zero[2 * p + 1] << 16, a[p], acc[1]);
+          group_product<PARTS>(w[2 * p], scale[2 * p] | zero[2 * p] << 16, a[p], acc[0]);
+          group_product<PARTS>(w[2 * p + 1], scale[2 * p + 1] | zero[2 * p + 1] << 16, a[p], acc[1]);
           settled(acc[0]);
           settled(acc[1]);
           __builtin_amdgcn_sched_barrier(0);
@@ -254,9 +265,12 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
         upv += red[j][1][v][l][i];
       }
       const float v = gate / (1.0f + expf(-gate)) * upv;
-      int to = (tile - parked + j) * 16 + col;
-      if (c.a_fragments) to = fragment_place(to);
-      c.a[size_t(c.t.slot[first + m].pair) * c.F + to] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+      const size_t row = size_t(c.t.slot[first + m].pair) * c.F;
+      const int n = (tile - parked + j) * 16 + col;
+      if (c.a_fragments)
+        static_cast<_Float16*>(c.a)[row + fragment_place(n)] = static_cast<_Float16>(v);
+      else
+        static_cast<float*>(c.a)[row + n] = v;
     }
     if (t == end) break;
     parked = 0;
@@ -347,7 +361,7 @@ __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const Down
         if (p == 0 || 4 * uq + p < G) {  // uniform
 #pragma unroll
           for (int t = 0; t < T; ++t) {
-            group_product(w[p % R][t], sz[t][p], a[p % R], acc[t]);
+            group_product(w[p % R][t], sz[t][p], &a[p % R], acc[t]);
             settled(acc[t]);
           }
         }
@@ -410,10 +424,10 @@ __global__ __launch_bounds__(256) void sum_kernel(const float* part, int splits,
 }
 
 // Workgroups: as many as the GPU holds at once (16 waves on a CU), and no more than there can be tiles.
-template <int W, int GW>
+template <int W, int GW, int PARTS = 1>
 hipError_t launch_gate_up(const MoeCall& c, hipStream_t st) {
   const long tiles = long(moe_units_max(c.M, c.E, c.top_k)) * (c.F / 16);
-  hipLaunchKernelGGL((gate_up_kernel<W, GW>), dim3(unsigned(std::min<long>(tiles, long(kCUs) * (16 / W)))), dim3(64 * W), 0, st, c);
+  hipLaunchKernelGGL((gate_up_kernel<W, GW, PARTS>), dim3(unsigned(std::min<long>(tiles, long(kCUs) * (16 / W)))), dim3(64 * W), 0, st, c);
   return hipGetLastError();
 }
 
@@ -450,6 +464,11 @@ MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {
 
 hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st) {
   const int G = c.D / PARO_GROUP;
+  if (c.x_parts) {  // twice the registers for a group of the tokens' rows
+    if (G <= 8) return G <= 4 ? launch_gate_up<4, 1, 2>(c, st) : launch_gate_up<4, 2, 2>(c, st);
+    if (G <= 32) return G <= 16 ? launch_gate_up<8, 2, 2>(c, st) : launch_gate_up<16, 2, 2>(c, st);
+    return launch_gate_up<16, 0, 2>(c, st);
+  }
   if (G <= 16) {
     if (G <= 4) return launch_gate_up<4, 1>(c, st);
     if (G <= 8) return launch_gate_up<4, 2>(c, st);

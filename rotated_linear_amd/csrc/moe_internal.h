@@ -25,16 +25,16 @@ int moe_units_max(int M, int E, int top_k);
 struct MoeCall {
   int M, D, F, E, top_k;
   const uint16_t* x;  // [M][D], as the experts see it
-  bool x_nibble_order;  // 8-channel words of x as [0,4,1,5,2,6,3,7]
-  bool a_fragments;     // a is written, and read, in the order of fragments; else it is written as it is and read in the
-                        // nibble order, with a transform in between
+  bool x_parts;  // a transform's rows: 8-channel words as [0,4,1,5,2,6,3,7], and [M][D] more, what their rounding took away
+  bool a_fragments;     // a is float16 in the order of fragments; else, with a transform behind it, float32 as it is, and
+                        // a_down float16 in the nibble order
   const uint8_t* gu_qw;
   const uint16_t* gu_sc;
   const uint16_t* gu_zr;
   const uint8_t* dn_qw;
   const uint16_t* dn_sc;
   const uint16_t* dn_zr;
-  uint16_t* a;             // [M top_k][F], what the gate and up products make: the rows of the pairs that have an expert
+  void* a;                 // [M top_k][F], what the gate and up products make: the rows of the pairs that have an expert
   const uint16_t* a_down;  // the same as the down product sees it
   float* part;             // [splits][M][D], where the down product is split
   MoeTables t;

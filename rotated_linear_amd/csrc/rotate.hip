@@ -61,7 +61,27 @@ struct RotJobs {
   int n, D;
 };
 
-template <int NT, int R, int PPT, int PD, bool EXACT, bool PERM>
+// Two adjacent channels as they are read.
+template <bool F32>
+struct ChannelPair {
+  using T = uint32_t;
+  static __device__ inline float low(T v) { return static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(v))); }
+  static __device__ inline float high(T v) { return static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(v >> 16))); }
+};
+template <>
+struct ChannelPair<true> {
+  using T = float __attribute__((ext_vector_type(2)));
+  static __device__ inline float low(T v) { return v[0]; }
+  static __device__ inline float high(T v) { return v[1]; }
+};
+
+// What the rounding of v to h takes away, as float16 (0 where v has no number, and where h has none, past 65504).
+__device__ inline uint16_t rest16(float v, _Float16 h) {
+  const float d = v - static_cast<float>(h);
+  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(fabsf(d) < 65504.0f ? d : 0.0f));
+}
+
+template <int NT, int R, int PPT, int PD, bool EXACT, bool PERM, bool F32, bool LO>
 __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
   extern __shared__ __attribute__((aligned(16))) float lds[];  // [D][R]
   const int tid = threadIdx.x;
@@ -104,14 +124,16 @@ __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
   // memory (not generic), so the accesses are global_* and an LDS wait or barrier never waits
   // for them; the bases are made opaque where the accesses issue, so their addresses are
   // formed there and not kept live (or spilled) across the stages.
-  uint32_t hv[PPT][R];
+  using Pair = ChannelPair<F32>;
+  typename Pair::T hv[PPT][R];
   auto load_rows = [&](int b) {
     const int tl = fresh_tid();
     uintptr_t xb = reinterpret_cast<uintptr_t>(x);
     asm volatile("" : "+s"(xb));
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const gptr<const uint32_t> xr = (gptr<const uint32_t>)(xb + size_t(min(b * R + r, M - 1)) * D * sizeof(uint16_t));
+      const gptr<const typename Pair::T> xr =
+          (gptr<const typename Pair::T>)(xb + size_t(min(b * R + r, M - 1)) * D * (sizeof(typename Pair::T) / 2));
 #pragma unroll
       for (int u = 0; u < PPT; ++u) hv[u][r] = xr[min(tl + u * NT, P - 1)];
     }
@@ -125,8 +147,8 @@ __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
         float f0[R], f1[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          f0[r] = static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(hv[u][r])));
-          f1[r] = static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(hv[u][r] >> 16)));
+          f0[r] = Pair::low(hv[u][r]);
+          f1[r] = Pair::high(hv[u][r]);
         }
         // lanes with bit 32/R set write their odd channel first: every aligned run of 16 (R = 4),
         // 32 or 64 lanes then hits distinct bank slots in each of the two writes
@@ -155,7 +177,7 @@ __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
 
     // LDS -> fp16(rows * (1/s)) packed in registers
     if constexpr (!kHoldS) load_s();
-    uint32_t ov[PPT][R];
+    uint32_t ov[PPT][R], ol[LO ? PPT : 1][R];
     const int to = fresh_tid();
 #pragma unroll
     for (int u = 0; u < PPT; ++u) {
@@ -167,9 +189,10 @@ __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
       const V va = sw ? w2 : w1, vb = sw ? w1 : w2;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const uint32_t lo = __builtin_bit_cast(uint16_t, static_cast<_Float16>(vec_at<R>(va, r) * isa[u]));
-        const uint32_t hi = __builtin_bit_cast(uint16_t, static_cast<_Float16>(vec_at<R>(vb, r) * isc[u]));
-        ov[u][r] = lo | (hi << 16);
+        const float fa = vec_at<R>(va, r) * isa[u], fb = vec_at<R>(vb, r) * isc[u];
+        const _Float16 ha = static_cast<_Float16>(fa), hb = static_cast<_Float16>(fb);
+        ov[u][r] = __builtin_bit_cast(uint16_t, ha) | uint32_t(__builtin_bit_cast(uint16_t, hb)) << 16;
+        if constexpr (LO) ol[u][r] = rest16(fa, ha) | uint32_t(rest16(fb, hb)) << 16;
       }
     }
     __syncthreads();  // every read of this block's rows is done
@@ -188,6 +211,12 @@ __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
 #pragma unroll
           for (int u = 0; u < PPT; ++u)
             if (ts + u * NT < P) orow[ts + u * NT] = ov[u][r];
+          if constexpr (LO) {
+            const gptr<uint32_t> lrow = orow + size_t(M) * P;
+#pragma unroll
+            for (int u = 0; u < PPT; ++u)
+              if (ts + u * NT < P) lrow[ts + u * NT] = ol[u][r];
+          }
         }
       }
     }
@@ -200,10 +229,10 @@ __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
 // One launch over J (jobs of one D): `grid` workgroups, or with grid = -T persistent workgroups
 // over T blocks, as many as the CUs hold at once (registers and LDS, from the runtime's occupancy
 // query: a workgroup that only starts when another ends would serve its blocks last).
-template <int NT, int R, int PPT, int PD, bool EXACT, bool PERM>
+template <int NT, int R, int PPT, int PD, bool EXACT, bool PERM, bool F32, bool LO>
 hipError_t launch_rows(const RotJobs& J, int grid, hipStream_t st) {
   const size_t lds = size_t(J.D) * R * sizeof(float);
-  const void* fn = reinterpret_cast<const void*>(&rotate_rows_kernel<NT, R, PPT, PD, EXACT, PERM>);
+  const void* fn = reinterpret_cast<const void*>(&rotate_rows_kernel<NT, R, PPT, PD, EXACT, PERM, F32, LO>);
   if (lds > 64 * 1024) {
     hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
     if (e != hipSuccess) return e;
@@ -213,28 +242,27 @@ hipError_t launch_rows(const RotJobs& J, int grid, hipStream_t st) {
     if (hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&per_cu, fn, NT, lds)) return e;
     grid = int(std::min<long>(-long(grid), long(std::max(per_cu, 1)) * kCUs));
   }
-  hipLaunchKernelGGL((rotate_rows_kernel<NT, R, PPT, PD, EXACT, PERM>), dim3(grid), dim3(NT), lds, st, J);
+  hipLaunchKernelGGL((rotate_rows_kernel<NT, R, PPT, PD, EXACT, PERM, F32, LO>), dim3(grid), dim3(NT), lds, st, J);
   return hipGetLastError();
 }
 
-// PD: ring depth when the pairs divide evenly over the threads (EXACT), PDN otherwise (the
-// range checks take registers).
-template <int NT, int R, int PPT, int PD, bool PERM, int PDN = PD>
+// PD: ring depth.
+template <int NT, int R, int PPT, int PD, bool PERM, bool F32, bool LO>
 hipError_t launch_exact(const RotJobs& J, int grid, hipStream_t st) {
-  if (J.D / 2 == PPT * NT) return launch_rows<NT, R, PPT, PD, true, PERM>(J, grid, st);
-  return launch_rows<NT, R, PPT, PDN, false, PERM>(J, grid, st);
+  if (J.D / 2 == PPT * NT) return launch_rows<NT, R, PPT, PD, true, PERM, F32, LO>(J, grid, st);
+  return launch_rows<NT, R, PPT, PD, false, PERM, F32, LO>(J, grid, st);
 }
 
 // Threads, pairs per thread per stage (PPT) and ring depth by row width (the ring is shallower
 // for wide rows, whose records and row vectors take more registers).
-template <int R, bool PERM>
+template <int R, bool PERM, bool F32 = false, bool LO = false>
 hipError_t launch_ppt(const RotJobs& J, int grid, hipStream_t st) {
   const int P = J.D / 2;
-  if (P <= 512) return launch_exact<512, R, 1, 4, PERM>(J, grid, st);
-  if (P <= 1024) return launch_exact<512, R, 2, 4, PERM>(J, grid, st);
-  if (P <= 1536) return launch_exact<512, R, 3, (R == 4 ? 2 : 4), PERM>(J, grid, st);
-  if (P <= 2048) return launch_exact<512, R, 4, (R == 1 ? 4 : 2), PERM>(J, grid, st);
-  if (P <= 3072) return launch_exact<512, R, 6, (R == 2 ? 1 : 2), PERM>(J, grid, st);
+  if (P <= 512) return launch_exact<512, R, 1, 4, PERM, F32, LO>(J, grid, st);
+  if (P <= 1024) return launch_exact<512, R, 2, 4, PERM, F32, LO>(J, grid, st);
+  if (P <= 1536) return launch_exact<512, R, 3, (R == 4 ? 2 : 4), PERM, F32, LO>(J, grid, st);
+  if (P <= 2048) return launch_exact<512, R, 4, (R == 1 ? 4 : 2), PERM, F32, LO>(J, grid, st);
+  if (P <= 3072) return launch_exact<512, R, 6, (R == 2 ? 1 : 2), PERM, F32, LO>(J, grid, st);
   // Wider rows: a workgroup's rows fill most of the LDS, so one workgroup runs per CU; 1024
   // threads (half the pairs each) give that CU twice the waves to overlap the stages' LDS
   // round trips. Measured on MI355X, K = 8: 64 x 14336 18.2 -> 14.3 us (one row per workgroup),
@@ -243,17 +271,17 @@ hipError_t launch_ppt(const RotJobs& J, int grid, hipStream_t st) {
   // threads a deeper ring spills, which was slower still (2048 x 8960: 58.7 us).
   // Past 14336 channels 8 pairs per thread would spill at 1024 threads: 512 threads, 16 pairs each.
   if constexpr (R == 1) {
-    if (P <= 4608) return launch_exact<1024, R, 5, 2, PERM>(J, grid, st);
-    if (P <= 6144) return launch_exact<1024, R, 6, 2, PERM>(J, grid, st);
-    if (P <= 7168) return launch_exact<1024, R, 7, 2, PERM>(J, grid, st);
-    return launch_exact<512, R, 16, 1, PERM>(J, grid, st);
+    if (P <= 4608) return launch_exact<1024, R, 5, 2, PERM, F32, LO>(J, grid, st);
+    if (P <= 6144) return launch_exact<1024, R, 6, 2, PERM, F32, LO>(J, grid, st);
+    if (P <= 7168) return launch_exact<1024, R, 7, 2, PERM, F32, LO>(J, grid, st);
+    return launch_exact<512, R, 16, 1, PERM, F32, LO>(J, grid, st);
   } else if constexpr (R == 2) {
-    if (P <= 4608) return launch_exact<1024, R, 5, 2, PERM>(J, grid, st);
-    if (P <= 6144) return launch_exact<1024, R, 6, 1, PERM>(J, grid, st);
-    if (P <= 7168) return launch_exact<1024, R, 7, 1, PERM>(J, grid, st);
-    return launch_exact<512, R, 16, 1, PERM>(J, grid, st);
+    if (P <= 4608) return launch_exact<1024, R, 5, 2, PERM, F32, LO>(J, grid, st);
+    if (P <= 6144) return launch_exact<1024, R, 6, 1, PERM, F32, LO>(J, grid, st);
+    if (P <= 7168) return launch_exact<1024, R, 7, 1, PERM, F32, LO>(J, grid, st);
+    return launch_exact<512, R, 16, 1, PERM, F32, LO>(J, grid, st);
   } else {  // 4-row blocks only up to 9216 channels
-    if (P <= 4608) return launch_exact<1024, R, 5, 1, PERM>(J, grid, st);
+    if (P <= 4608) return launch_exact<1024, R, 5, 1, PERM, F32, LO>(J, grid, st);
   }
   return hipErrorInvalidValue;
 }
@@ -273,7 +301,7 @@ int rows_per_block(int D, long T) {
 // Launch jobs[0, n) (same D, 1 <= n <= kRotMaxJobs) with R rows per block: one job on
 // persistent workgroups, several jobs one block per workgroup (the caller keeps their total
 // within what the GPU holds at once).
-hipError_t launch_jobs(const RotateJob* jobs, int n, int R, bool perm, hipStream_t st) {
+RotJobs table(const RotateJob* jobs, int n, int R) {
   RotJobs J;
   memset(&J, 0, sizeof(J));
   J.n = n;
@@ -290,6 +318,11 @@ hipError_t launch_jobs(const RotateJob* jobs, int n, int R, bool perm, hipStream
     total += (jobs[i].M + R - 1) / R;
   }
   J.blk0[n] = total;
+  return J;
+}
+hipError_t launch_jobs(const RotateJob* jobs, int n, int R, bool perm, hipStream_t st) {
+  const RotJobs J = table(jobs, n, R);
+  const int total = J.blk0[n];
   const int grid = n == 1 ? -total : total;  // one job: persistent workgroups (see launch_rows)
   if (R == 4) return perm ? launch_ppt<4, true>(J, grid, st) : launch_ppt<4, false>(J, grid, st);
   if (R == 2) return perm ? launch_ppt<2, true>(J, grid, st) : launch_ppt<2, false>(J, grid, st);
@@ -303,6 +336,22 @@ hipError_t launch_rotate(const DevRot& R, int M, const uint16_t* x, uint16_t* xo
   if (R.D / 2 > 8 * 1024) return hipErrorInvalidValue;
   const RotateJob job{&R, M, x, xout};
   return launch_jobs(&job, 1, rows_per_block(R.D, M), nibble_order, st);
+}
+
+hipError_t launch_rotate_parts(const DevRot& R, int M, const uint16_t* x, uint16_t* xout, hipStream_t st) {
+  if (R.D / 2 > 8 * 1024) return hipErrorInvalidValue;
+  const RotateJob job{&R, M, x, xout};
+  const RotJobs J = table(&job, 1, 1);
+  return launch_ppt<1, true, false, true>(J, -J.blk0[1], st);
+}
+
+// (Blocks of two rows hold twice the registers of float32 rows: only where a thread has few pairs.)
+hipError_t launch_rotate_f32(const DevRot& R, int M, const float* x, uint16_t* xout, hipStream_t st) {
+  if (R.D / 2 > 8 * 1024) return hipErrorInvalidValue;
+  const RotateJob job{&R, M, reinterpret_cast<const uint16_t*>(x), xout};
+  const int rows = R.D <= 4096 && M > kCUs ? 2 : 1;
+  const RotJobs J = table(&job, 1, rows);
+  return rows == 2 ? launch_ppt<2, true, true>(J, -J.blk0[1], st) : launch_ppt<1, true, true>(J, -J.blk0[1], st);
 }
 
 hipError_t launch_rotate_batch(const RotateJob* jobs, int n, bool nibble_order, hipStream_t st) {
