@@ -14,6 +14,49 @@ constexpr int kMaxM = PARO_MOE_MAX_M, kMaxK = PARO_MOE_MAX_K;
 static_assert(PARO_MOE_MAX_E == 512, "a thread for each expert; select_kernel<2> has room for 512");
 constexpr int kWaves = 8;
 
+// Moves of a double between lanes without LDS, in its two halves.
+template <class F>
+__device__ inline double by_halves(double v, F move) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, uint64_t(move(uint32_t(b))) | uint64_t(move(uint32_t(b >> 32))) << 32);
+}
+// v plus what a data-parallel move brings; lanes without a source add 0.
+template <int CTRL, int ROWS>
+__device__ inline double plus_moved(double v) {
+  return v + by_halves(v, [](uint32_t h) { return uint32_t(__builtin_amdgcn_update_dpp(0, int(h), CTRL, ROWS, 0xF, false)); });
+}
+// In lane 15 of each row of 16 lanes: the row's sum.
+__device__ inline double row_sum(double v) {
+  v = plus_moved<0x111, 0xF>(v);  // row_shr:1, 2, 4, 8
+  v = plus_moved<0x112, 0xF>(v);
+  v = plus_moved<0x114, 0xF>(v);
+  return plus_moved<0x118, 0xF>(v);
+}
+__device__ inline double lane_of(double v, int lane) {
+  return by_halves(v, [lane](uint32_t h) { return uint32_t(__builtin_amdgcn_readlane(int(h), lane)); });
+}
+// In every lane: the wave's sum.
+__device__ inline double wave_sum(double v) {
+  v = row_sum(v);
+  v = plus_moved<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+  v = plus_moved<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+  return lane_of(v, 63);
+}
+// D = 32 (16): in the wave's first half (its even rows) a plus the other half's (the next row's) a, in the others b plus b.
+template <int D>
+__device__ inline double traded_sum(double a, double b) {
+  const uint64_t x = __builtin_bit_cast(uint64_t, a), y = __builtin_bit_cast(uint64_t, b);
+  uint64_t lo = 0, hi = 0;
+#pragma unroll
+  for (int s = 0; s < 64; s += 32) {
+    const auto r = D == 32 ? __builtin_amdgcn_permlane32_swap(uint32_t(x >> s), uint32_t(y >> s), false, false)
+                           : __builtin_amdgcn_permlane16_swap(uint32_t(x >> s), uint32_t(y >> s), false, false);
+    lo |= uint64_t(uint32_t(r[0])) << s;
+    hi |= uint64_t(uint32_t(r[1])) << s;
+  }
+  return __builtin_bit_cast(double, lo) + __builtin_bit_cast(double, hi);
+}
+
 // A workgroup has MT tokens and ET experts; its threads take 8 channels at a time.
 template <bool F32, int MT, int ET>
 __global__ __launch_bounds__(64 * kWaves) void logits_kernel(const MoeRoute r) {
@@ -49,22 +92,21 @@ __global__ __launch_bounds__(64 * kWaves) void logits_kernel(const MoeRoute r) {
         for (int i = 0; i < ET; ++i) acc[j * ET + i] = __builtin_fma(double(float(x[j][k])), double(w[i][k]), acc[j * ET + i]);
     }
   }
-  // The wave's sums: while there are several, lanes whose indexes differ in one bit keep half of them each.
-  int n = V, at = 0, d = 32;
+  // The wave's sums. While there are several, halves of the wave (then its rows of 16 lanes) trade them, so that each
+  // goes on with half of them; what is left is summed over the row, or over the wave.
+  if constexpr (V == 1) {
+    const double v = wave_sum(acc[0]);
+    if (lane == 0) part[wave][0] = v;
+  } else {
+    constexpr int H = V / 2, Q = V / 4;
 #pragma unroll
-  for (; n > 1; n /= 2, d /= 2) {
-    const bool high = lane & d;
+    for (int i = 0; i < H; ++i) acc[i] = traded_sum<32>(acc[i], acc[H + i]);  // lanes 32..63: sums H + i
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i)
-      if (i < n / 2) {
-        const double keep = high ? acc[n / 2 + i] : acc[i], give = high ? acc[i] : acc[n / 2 + i];
-        acc[i] = keep + __shfl_xor(give, d);
-      }
-    at += high ? n / 2 : 0;
+    for (int i = 0; i < Q; ++i) {
+      const double v = row_sum(traded_sum<16>(acc[i], acc[Q + i]));  // odd rows: sums Q + i
+      if ((lane & 15) == 15) part[wave][(lane >> 5) * H + (lane >> 4 & 1) * Q + i] = v;
+    }
   }
-#pragma unroll
-  for (; d; d /= 2) acc[0] += __shfl_xor(acc[0], d);
-  if ((lane & (64 / V - 1)) == 0) part[wave][at] = acc[0];
   __syncthreads();
   if (tid < V) {
     const int m = m0 + tid / ET, e = e0 + tid % ET;
@@ -104,11 +146,7 @@ __global__ __launch_bounds__(1024) void select_kernel(const MoeRoute r) {
   double sum = 0, top = 0;
   if (!r.sigmoid) {
     top = key[id[0]];
-    if (wave < (r.E * PARTS + 63) / 64) {
-      sum = e < r.E ? exp(logit - top) : 0.0;
-#pragma unroll
-      for (int d = 32; d >= PARTS; d /= 2) sum += __shfl_xor(sum, d);
-    }
+    if (wave < (r.E * PARTS + 63) / 64) sum = wave_sum(e < r.E && tid % PARTS == 0 ? exp(logit - top) : 0.0);
     if (lane == 0) part[wave] = sum;
     __syncthreads();
     sum = 0;
@@ -119,7 +157,7 @@ __global__ __launch_bounds__(1024) void select_kernel(const MoeRoute r) {
     const double v = lane < r.top_k ? chosen[lane] : 0.0;
     const double w = r.sigmoid ? 1.0 / (1.0 + exp(-v)) : exp(v - top) / sum;
     double all = 0;
-    for (int j = 0; j < r.top_k; ++j) all += __shfl(w, j);
+    for (int j = 0; j < r.top_k; ++j) all += lane_of(w, j);
     if (lane < r.top_k) {
       r.ids[m * r.top_k + lane] = id[lane];
       r.weights[m * r.top_k + lane] = float(r.renormalize ? w / all : w);
@@ -147,7 +185,7 @@ __global__ __launch_bounds__(kOneGroup) void select_one_kernel(const MoeRoute r,
   if (live) {
     int rank = 0;
     const double* const row = key + m * r.E;
-#pragma unroll 8
+#pragma unroll 16
     for (int o = 0; o < r.E; ++o) rank += row[o] > mine || (row[o] == mine && o < e);
     if (rank < r.top_k) {
       ids[m * r.top_k + rank] = e;
@@ -167,14 +205,13 @@ __global__ __launch_bounds__(kOneGroup) void select_one_kernel(const MoeRoute r,
       double sum = 0;
       if (!r.sigmoid) {
         for (int o = lane; o < r.E; o += 64) sum += share[at * r.E + o];
-#pragma unroll
-        for (int d = 32; d; d /= 2) sum += __shfl_xor(sum, d);
+        sum = wave_sum(sum);
       }
       const int p = at * r.top_k + lane;
       double w = 0;
       if (lane < r.top_k) w = r.sigmoid ? 1.0 / (1.0 + exp(-chosen[p])) : share[at * r.E + ids[p]] / sum;
       double all = 0;
-      for (int j = 0; j < r.top_k; ++j) all += __shfl(w, j);
+      for (int j = 0; j < r.top_k; ++j) all += lane_of(w, j);
       if (lane < r.top_k) weights[p] = float(r.renormalize ? w / all : w);
     }
   }

@@ -17,17 +17,22 @@ struct TablePlace {
   int count;
   uint32_t before;  // slots, and units in the upper half
 };
+template <int CTRL, int ROWS>
+__device__ inline uint32_t up(uint32_t v) {  // what a data-parallel move brings, 0 to lanes without a source
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, ROWS, 0xF, false));
+}
 __device__ inline TablePlace tables_count(TableWork& s) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   TablePlace p;
   p.count = int(__popcll(s.mask[tid]));
   const uint32_t own = uint32_t(p.count) | uint32_t((p.count + 15) / 16) << 16;
   uint32_t sum = own;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_up(sum, d);
-    if (lane >= d) sum += o;
-  }
+  sum += up<0x111, 0xF>(sum);  // row_shr:1, 2, 4, 8: sums up to the lane within its row of 16
+  sum += up<0x112, 0xF>(sum);
+  sum += up<0x114, 0xF>(sum);
+  sum += up<0x118, 0xF>(sum);
+  sum += up<0x142, 0xA>(sum);  // row_bcast:15 into rows 1 and 3
+  sum += up<0x143, 0xC>(sum);  // row_bcast:31 into rows 2 and 3
   if (lane == 63) s.totals[wave] = sum;
   p.before = sum - own;
   return p;
