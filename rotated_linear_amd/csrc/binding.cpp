@@ -1,6 +1,6 @@
-// The Python calls of the 8-bit path and of what surrounds a block's products, without ctypes: checks, outputs and the C call in one step. A decode
-// step's kernels take 3 to 6 us each; through ctypes a call costs 7 to 10 us of host time, here 3.7 to 4.9
-// (2.5 of it the runtime's launch).
+// The Python calls of the 8-bit path and of what surrounds a block's products, without ctypes: checks, outputs and the
+// C call in one step. A decode step's kernels take 3 to 6 us each; through ctypes a call costs 7 to 10 us of host time,
+// here 3.7 to 4.9 (2.5 of it the runtime's launch).
 //
 // Every function here returns None, having done nothing, when an argument is not what the call takes
 // (another type, shape, device, stride or a tensor subclass, or a gradient asked for), when another GPU is current, or when the

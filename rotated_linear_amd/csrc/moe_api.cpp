@@ -27,8 +27,8 @@ Layout layout(int M, int D, int F, int E, int top_k) {
   const size_t pairs = size_t(M) * top_k;
   l.logits = take(size_t(M) * E * 8);
   l.x = take(size_t(M) * D * 4);
-  l.a = take(pairs * F * 4);  // (float32 where a transform follows)
-  l.a_rotated = take(pairs * F * 2);
+  l.a = take(pairs * F * 4);  // two float16 parts, or float32 where a transform follows
+  l.a_rotated = take(pairs * F * 4);
   const int splits = moe_down_plan(M, D, F, E, top_k).splits;
   l.part = take(splits > 1 ? size_t(splits) * M * D * 4 : 0);
   l.units = take(4);
@@ -123,7 +123,7 @@ paro_status experts(int M, int D, int F, int E, int top_k, const void* x, const 
   if (e == hipSuccess && rot_a) {
     // (every row there may be: those of pairs without an expert hold what they held, and no product reads them)
     uint16_t* const ar = reinterpret_cast<uint16_t*>(base + l.a_rotated);
-    e = launch_rotate_f32(ra, M * top_k, static_cast<const float*>(c.a), ar, st);
+    e = launch_rotate_f32_parts(ra, M * top_k, static_cast<const float*>(c.a), ar, st);
     c.a_down = ar;
   }
   if (e == hipSuccess) e = launch_moe_down(c, st);

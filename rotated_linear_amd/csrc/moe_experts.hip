@@ -267,9 +267,11 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
       const float v = gate / (1.0f + expf(-gate)) * upv;
       const size_t row = size_t(c.t.slot[first + m].pair) * c.F;
       const int n = (tile - parked + j) * 16 + col;
-      if (c.a_fragments)
-        static_cast<_Float16*>(c.a)[row + fragment_place(n)] = static_cast<_Float16>(v);
-      else
+      if (c.a_fragments) {
+        _Float16* const to = static_cast<_Float16*>(c.a) + row + fragment_place(n);
+        *to = static_cast<_Float16>(v);
+        if (count <= kTwoParts) to[size_t(c.M) * c.top_k * c.F] = __builtin_bit_cast(_Float16, rest16(v, static_cast<_Float16>(v)));
+      } else
         static_cast<float*>(c.a)[row + n] = v;
     }
     if (t == end) break;
@@ -291,6 +293,9 @@ struct DownArgs {
 // A workgroup has T times 16 columns of y and its share of the items, an item being four groups of a unit: the items in
 // order are cut into splits * W equal runs, one for each wave. A wave keeps sums of its own for every token in LDS, to
 // which it adds an expert's products times the tokens' weights where it leaves the expert. R groups are in flight.
+// a is float16, but a unit of up to 8 tokens has 8 rows of the matrix products to spare: there they take what a's rounding
+// took away, at no cost in loads or products (error of y, float16, one token, 8 of 64 experts 1024 -> 2048: 3.2e-4 -> 2.1e-4 of
+// y, of which its own rounding is 2.1e-4; the fuller units' a is off by 2^-12 of each value).
 //
 // What bounds it is the CU's load path: a group of 16 rows of a takes four times the loads of 16 columns' weights, so
 // more columns to a workgroup cost less, as long as there is a workgroup for each CU.
@@ -322,7 +327,9 @@ __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const Down
   const char *wp = nullptr, *sp = nullptr, *zp = nullptr;
   auto aim = [&]() {  // (no global access: the wait counts stay exact)
     const MoeUnit k = unit[lu];
-    ao = uint32_t(slot[k.first + min(nl, k.count - 1)].pair) * uint32_t(c.F) * 2 + h * (c.a_fragments ? 16 : 64);
+    const bool both = k.count <= kTwoParts;
+    const int r = min(both ? nl % kTwoParts : nl, k.count - 1);
+    ao = (uint32_t(slot[k.first + r].pair) + (both && nl >= kTwoParts ? pairs : 0)) * uint32_t(c.F) * 2 + h * (c.a_fragments ? 16 : 64);
     const size_t row = size_t(__builtin_amdgcn_readfirstlane(k.expert)) * c.D + tile * 16 * T;
     wp = reinterpret_cast<const char*>(c.dn_qw) + row * (c.F / 2);
     sp = reinterpret_cast<const char*>(c.dn_sc) + row * G * 2;
@@ -372,6 +379,12 @@ __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const Down
       __builtin_amdgcn_sched_barrier(0);
       if (++uq == Q || n == 1) {
         const MoeUnit k = unit[uu];
+        if (k.count <= kTwoParts) {  // lanes 32..63 have the lower parts' sums
+#pragma unroll
+          for (int t = 0; t < T; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] += __shfl_xor(acc[t][i], 32);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = 4 * h + i;
@@ -441,24 +454,30 @@ static_assert(down_lds(4, PARO_MOE_MAX_M, PARO_MOE_MAX_E + PARO_MOE_MAX_M, PARO_
 
 int moe_units_max(int M, int E, int top_k) { return std::min(E, M * top_k) + M * top_k / 16; }
 
-// 16, 32 or 64 columns to a workgroup, and how many workgroups share them, by an estimate in microseconds of what a CU
-// has to do: its items, four groups each, and the kernel that adds the parts. Measured (16, 32, 64 columns, workgroups
-// for each CU): 64 tokens, 8 of 64 experts, 1408 -> 4096 80, 54 and 46 us; 32 tokens, 4 of 16, 2048 -> 4096 27, 22 and
-// 22; 4 tokens, 2 of 8, 14336 -> 4096 45, 38 and 38; 13 tokens, 4 of 60, 1408 -> 1536 19, 14 and 16.
+// 16, 32 or 64 columns to a workgroup, and how many workgroups share them, by an estimate in microseconds: a CU's time for
+// an item (four groups of an expert's rows), fitted to ten calls of 1 to 64 tokens at 27 cuts each, and the kernel that adds
+// the parts. The experts are as many as are reached where each token's choice is as good as any other. The shares are
+// those that fill the GPU once, or one. Measured, a layer with 16 columns to a workgroup and no shares, with 32, 64 and
+// as many shares as fill the GPU: 4 tokens, 2 of 8 experts, 4096 -> 14336 112, 107 and 106 us; 8 tokens, 4 of 16, 4096 ->
+// 2048 48, 48 and 47; 64 tokens, 8 of 64, 4096 -> 1408 174, 150 and 142; one token, 8 of 64, 2048 -> 1024 21.5, 21.2 and 22.9.
 MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {
-  constexpr double kItem[2][3] = {{0.22, 0.36, 0.75}, {0.39, 0.51, 0.86}};  // up to 32 tokens, and more
-  const double items = double(std::min(E, M * top_k)) * ((F / PARO_GROUP + 3) / 4);
+  constexpr double kItem[3] = {0.28, 0.39, 0.62}, kSum = 4.0;
+  const double reached = E * (1.0 - std::pow(1.0 - std::min(1.0, double(top_k) / E), M));
+  const double items = reached * ((F / PARO_GROUP + 3) / 4);
   MoeDownPlan best{1, 1};
   double least = 1e30;
-  for (int i = 0; i < 3; ++i)
-    for (int s = 1; s <= 32; ++s) {
-      const double rounds = double((long(D / 16 >> i) * s + kCUs - 1) / kCUs);
-      const double us = rounds * std::ceil(items / s) * kItem[M > 32][i] * (0.92 + 0.08 * rounds) + (s > 1 ? 4.0 : 0.0);
+  for (int i = 0; i < 3; ++i) {
+    const int columns = D / 16 >> i, rounds = (columns + kCUs - 1) / kCUs;
+    const int shares = std::min({32, kCUs / columns, int(items / 3)});
+    auto take = [&](int s, double us) {
       if (us < least) {
         least = us;
         best = MoeDownPlan{1 << i, s};
       }
-    }
+    };
+    take(1, rounds * items * kItem[i]);
+    if (shares > 1) take(shares, items / shares * kItem[i] + kSum);
+  }
   return best;
 }
 

@@ -146,8 +146,8 @@ hipError_t launch_rotate(const DevRot& R, int M, const uint16_t* x, uint16_t* xo
                          hipStream_t st);
 // For few rows, in the nibble order: float16 rows [M][D], and behind them [M][D] what their rounding took away.
 hipError_t launch_rotate_parts(const DevRot& R, int M, const uint16_t* x, uint16_t* xout, hipStream_t st);
-// From float32 rows to float16, in the nibble order.
-hipError_t launch_rotate_f32(const DevRot& R, int M, const float* x, uint16_t* xout, hipStream_t st);
+// The same from float32 rows.
+hipError_t launch_rotate_f32_parts(const DevRot& R, int M, const float* x, uint16_t* xout, hipStream_t st);
 // Several transforms of the same D (each with its own descriptor, x and output) in as few
 // launches as the GPU holds at once (up to kRotMaxJobs per launch).
 constexpr int kRotMaxJobs = 16;

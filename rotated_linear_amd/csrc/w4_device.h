@@ -5,6 +5,12 @@
 
 namespace paro {
 
+// What the rounding of v to h takes away, as float16 (0 where v has no number, and where h has none, past 65504).
+__device__ inline uint16_t rest16(float v, _Float16 h) {
+  const float d = v - static_cast<float>(h);
+  return __builtin_bit_cast(uint16_t, static_cast<_Float16>(fabsf(d) < 65504.0f ? d : 0.0f));
+}
+
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef float f4 __attribute__((ext_vector_type(4)));
