@@ -3,7 +3,9 @@
 // in registers between its statistics and its output. Measured (graph replays, cold rows): rmsnorm_q8 with
 // residual 4096 x 4096 bf16 25.4 us (7 bytes a channel, 4.6 TB/s; a copy of 1 GiB runs at 4.7), rmsnorm
 // 26.1 us (8 bytes, 5.1 TB/s), quantiser 13.0 us (3.9 TB/s), read-back 12.3 us (4.1 TB/s); a single row of
-// 4096 2.7, 2.4, 2.1 and 1.9 us, a launch.
+// 4096 2.7, 2.4, 2.1 and 1.9 us, a launch. The norms around a block (in a trace): 4096 x 4096 bf16 with post_gamma, eight
+// gates and 8-bit rows 27.0 us (7 bytes a channel, 4.4 TB/s), 1021 x 8960 float16 with a gate 16.7 us (8 bytes, 4.4
+// TB/s), a row of 4096 3.3 us.
 #include <algorithm>
 
 #include "q8_device.h"
