@@ -488,7 +488,9 @@ MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {
 hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st) {
   const int G = c.D / PARO_GROUP;
   if (c.x_parts) {  // twice the registers for a group of the tokens' rows
-    if (G <= 8) return G <= 4 ? launch_gate_up<4, 1, 2>(c, st) : launch_gate_up<4, 2, 2>(c, st);
+    // (eight waves for 5 to 8 groups: half as many workgroups load the tokens; against four of two groups each, a layer of 50
+    // tokens, 2 of 6 experts, 896 -> 2688 43 us against 47, of 64, 4 of 60, 1024 -> 1408 69 against 67)
+    if (G <= 8) return G <= 4 ? launch_gate_up<4, 1, 2>(c, st) : launch_gate_up<8, 1, 2>(c, st);
     if (G <= 32) return G <= 16 ? launch_gate_up<8, 2, 2>(c, st) : launch_gate_up<16, 2, 2>(c, st);
     return launch_gate_up<16, 0, 2>(c, st);
   }

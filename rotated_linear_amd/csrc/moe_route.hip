@@ -171,7 +171,11 @@ __global__ __launch_bounds__(1024) void select_kernel(const MoeRoute r) {
 constexpr int kOneGroup = 1024;
 template <bool TABLES>
 __global__ __launch_bounds__(kOneGroup) void select_one_kernel(const MoeRoute r, const MoeTables t) {
-  __shared__ double key[kOneGroup], share[kOneGroup];
+  // Logits as whole numbers of the same order, in two halves, each token's upper halves from a multiple of four on, with
+  // zeros behind them (no logit's): four are compared at a time, and the lower ones only where upper ones are equal.
+  __shared__ __attribute__((aligned(16))) uint32_t upper[kOneGroup + 3 * kMaxM];
+  __shared__ uint32_t lower[kOneGroup];
+  __shared__ double share[kOneGroup];
   __shared__ TableWork work;
   __shared__ int ids[kMaxM * kMaxK];
   __shared__ double chosen[kMaxM * kMaxK];
@@ -179,15 +183,32 @@ __global__ __launch_bounds__(kOneGroup) void select_one_kernel(const MoeRoute r,
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = tid / r.E, e = tid - m * r.E, pairs = r.M * r.top_k;
   const bool live = m < r.M;
   const double logit = live ? r.logits[tid] : 0.0;
-  const double mine = logit == logit ? logit : -__builtin_inf();  // a NaN ranks as minus infinity
-  key[tid] = mine;
+  const double mine = logit == logit ? logit + 0.0 : -__builtin_inf();  // a NaN ranks as minus infinity, -0 as 0
+  const uint64_t bits = __builtin_bit_cast(uint64_t, mine), key = bits ^ (bits >> 63 ? ~0ull : 1ull << 63);
+  const uint32_t high = uint32_t(key >> 32), low = uint32_t(key);
+  const int stride = (r.E + 3) & ~3;
+  const uint32_t* const row = upper + m * stride;
+  if (live) {
+    upper[m * stride + e] = high;
+    lower[tid] = low;
+    if (e == 0)
+      for (int o = r.E; o < stride; ++o) upper[m * stride + o] = 0;
+  }
   if (TABLES && tid < PARO_MOE_MAX_E) work.mask[tid] = 0;
   __syncthreads();
   if (live) {
-    int rank = 0;
-    const double* const row = key + m * r.E;
-#pragma unroll 16
-    for (int o = 0; o < r.E; ++o) rank += row[o] > mine || (row[o] == mine && o < e);
+    int rank = 0, equal = 0;
+#pragma unroll 4
+    for (int o = 0; o < r.E; o += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + o);
+      rank += (v.x > high) + (v.y > high) + (v.z > high) + (v.w > high);
+      equal += (v.x == high) + (v.y == high) + (v.z == high) + (v.w == high);
+    }
+    if (equal > 1)
+      for (int o = 0; o < r.E; ++o) {
+        const uint32_t other = lower[tid - e + o];
+        rank += row[o] == high && (other > low || (other == low && o < e));
+      }
     if (rank < r.top_k) {
       ids[m * r.top_k + rank] = e;
       chosen[m * r.top_k + rank] = logit;
@@ -195,7 +216,7 @@ __global__ __launch_bounds__(kOneGroup) void select_one_kernel(const MoeRoute r,
     }
   }
   __syncthreads();
-  if (live && !r.sigmoid) share[tid] = exp(logit - key[m * r.E + ids[m * r.top_k]]);
+  if (live && !r.sigmoid) share[tid] = exp(logit - chosen[m * r.top_k]);
   __syncthreads();
   TablePlace place{};
   if (TABLES && tid < PARO_MOE_MAX_E) {

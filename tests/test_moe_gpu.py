@@ -230,6 +230,20 @@ def test_route_ties_and_odd_rows():
     assert ids[0].tolist()[2] == 0 and bool(w[0, 2].isnan()) and bool(w[0, :2].isfinite().all())
 
 
+@pytest.mark.parametrize("M,E,k", [(1, 2, 2), (3, 61, 16), (25, 40, 7), (64, 15, 15), (64, 300, 9)])
+def test_route_close_logits(M, E, k):
+    """Logits a float32's last digit apart, of either sign, some of them equal."""
+    D = 128
+    r = np.random.default_rng([M, E, k])
+    x = np.zeros((M, D), np.float16)
+    x[:, 0] = r.choice([1, -1, 0.5, -0.25], M)
+    router = np.zeros((E, D), np.float32)
+    router[:, 0] = 1 + r.integers(0, 2 * E, E) * 2.0 ** -23
+    want, w64 = B.route(x.astype(np.float64), router.astype(np.float64), k)
+    ids, w = rl.paro_moe_route(torch.from_numpy(x).cuda(), torch.from_numpy(router).cuda(), k)
+    assert np.array_equal(ids.cpu().numpy(), want) and over(w.double().cpu().numpy() - w64, w64 * U * 1.0001) <= 1
+
+
 @pytest.mark.parametrize("M,E,k,rotated", [(1, 64, 8, False), (4, 8, 2, True), (64, 24, 3, False), (23, 7, 7, True)])
 def test_layer_is_its_parts(M, E, k, rotated):
     D, F = 512, 384
