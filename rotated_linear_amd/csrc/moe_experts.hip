@@ -67,9 +67,17 @@ __device__ inline T at(const void* base, uint32_t off, int more = 0) {
 }
 __device__ inline void opaque(uint32_t& off) { asm volatile("" : "+v"(off)); }
 using u4 = uint32_t __attribute__((ext_vector_type(4)));
+// ONCE: past the caches (see kOnceGateUp).
+template <bool ONCE>
 __device__ inline uint4 load_weights(const void* w, uint32_t& wo) {
   opaque(wo);
-  return __builtin_bit_cast(uint4, at<u4>(w, wo));
+  if constexpr (ONCE) {
+    uintptr_t p = reinterpret_cast<uintptr_t>(w);
+    asm volatile("" : "+s"(p));
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load((gptr<u4>)((gptr<char>)p + wo)));
+  } else {
+    return __builtin_bit_cast(uint4, at<u4>(w, wo));
+  }
 }
 __device__ inline void load_scales(uint32_t& scale, uint32_t& zero, const void* sp, const void* zp, uint32_t& so) {
   opaque(so);
@@ -106,7 +114,7 @@ __device__ inline int fragment_place(int n) {
 // PARTS = 2: the tokens' rows come from a transform, in two float16 parts, and take twice the registers and products.
 // How many waves, and so how many groups to each, is a matter of registers: 16 waves on a CU leave each 128.
 constexpr int kPark = 4;
-template <int W, int GW, int PARTS>
+template <int W, int GW, int PARTS, bool ONCE>
 __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
   constexpr int R = GW == 1 ? 2 : GW == 3 ? 6 : 4;
   constexpr int S = GW ? 2 * GW : R;  // steps of a tile
@@ -149,7 +157,7 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
     const int g = group(i);
     const size_t sa = (half ? sup : 0) + (GW ? 0 : uint32_t(g) * 2);
     if (GW == 0 || i == 0) load_scales(scale[GW ? half : q], zero[GW ? half : q], sp + sa, zp + sa, so);
-    w[q] = load_weights(wp + (half ? wup : 0) + uint32_t(g) * 1024, wo);
+    w[q] = load_weights<ONCE>(wp + (half ? wup : 0) + uint32_t(g) * 1024, wo);
   };
   auto spread = [&](int half) {
     const uint32_t v = scale[half] | zero[half] << 16;
@@ -303,7 +311,7 @@ struct DownArgs {
 //
 // What bounds it is the CU's load path: a group of 16 rows of a takes four times the loads of 16 columns' weights, so
 // more columns to a workgroup cost less, as long as there is a workgroup for each CU.
-template <int W, int T, int R>
+template <int W, int T, int R, bool ONCE>
 __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const DownArgs args) {
   static_assert(R == 2 || R == 4, "a group's slot is fixed");
   extern __shared__ __attribute__((aligned(16))) char smem[];  // float [W][M][16 T], then the tables
@@ -354,7 +362,7 @@ __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const Down
     }
     const uint32_t g = min(4 * lq + p, G - 1);
 #pragma unroll
-    for (int t = 0; t < T; ++t) w[q][t] = load_weights(wp + size_t(t) * 8 * c.F + g * 1024, wo);
+    for (int t = 0; t < T; ++t) w[q][t] = load_weights<ONCE>(wp + size_t(t) * 8 * c.F + g * 1024, wo);
     load_rows(a[q], c.a_down + g * PARO_GROUP, ao, c.a_fragments ? 64 : 16);
   };
   if (begin < end) {
@@ -440,12 +448,25 @@ __global__ __launch_bounds__(256) void sum_kernel(const float* part, int splits,
   }
 }
 
+// The experts that a call reaches, where each choice of a token is as good as any other.
+double reached(int M, int E, int top_k) { return E * (1.0 - std::pow(1.0 - std::min(1.0, double(top_k) / E), M)); }
+
+// From so many bytes of the reached experts' weights on they are loaded past the caches, and leave those to what is read
+// again. A layer with both products' loads in the caches, gate and up's past them, both: 4 tokens, 2 of 8 experts, 4096 ->
+// 14336 106, 103 and 100 us; 64 tokens, 8 of 64, 4096 -> 1408 143, 141 and 135; 13 tokens, 4 of 60, 1536 -> 1408 65, 62 and 65
+// (82 and 41 MB); one token, 8 of 64, 2048 -> 1024 22.0, 23.0 and 23.1 (18 and 9 MB, which were still in the caches).
+constexpr double kOnceGateUp = 32e6, kOnceDown = 128e6;
+
 // Workgroups: as many as the GPU holds at once (16 waves on a CU), and no more than there can be tiles.
 template <int W, int GW, int PARTS = 1>
 hipError_t launch_gate_up(const MoeCall& c, hipStream_t st) {
   const long tiles = long(moe_units_max(c.M, c.E, c.top_k)) * (c.F / 16);
-  hipLaunchKernelGGL((gate_up_kernel<W, GW, PARTS>), dim3(unsigned(std::min<long>(tiles, long(kCUs) * (16 / W)))), dim3(64 * W), 0, st, c);
-  return hipGetLastError();
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(unsigned(std::min<long>(tiles, long(kCUs) * (16 / W)))), dim3(64 * W), 0, st, c);
+    return hipGetLastError();
+  };
+  const bool once = reached(c.M, c.E, c.top_k) * c.F * c.D >= kOnceGateUp;  // (two rows of half a byte)
+  return once ? go(gate_up_kernel<W, GW, PARTS, true>) : go(gate_up_kernel<W, GW, PARTS, false>);
 }
 
 constexpr int kDownWaves = 8;
@@ -460,14 +481,12 @@ int moe_units_max(int M, int E, int top_k) { return std::min(E, M * top_k) + M *
 
 // 16, 32 or 64 columns to a workgroup, and how many workgroups share them, by an estimate in microseconds: a CU's time for
 // an item (four groups of an expert's rows), fitted to ten calls of 1 to 64 tokens at 27 cuts each, and the kernel that adds
-// the parts. The experts are as many as are reached where each token's choice is as good as any other. The shares are
-// those that fill the GPU once, or one. Measured, a layer with 16 columns to a workgroup and no shares, with 32, 64 and
+// the parts. The shares are those that fill the GPU once, or one. Measured, a layer with 16 columns to a workgroup and no shares, with 32, 64 and
 // as many shares as fill the GPU: 4 tokens, 2 of 8 experts, 4096 -> 14336 112, 107 and 106 us; 8 tokens, 4 of 16, 4096 ->
 // 2048 48, 48 and 47; 64 tokens, 8 of 64, 4096 -> 1408 174, 150 and 142; one token, 8 of 64, 2048 -> 1024 21.5, 21.2 and 22.9.
 MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {
   constexpr double kItem[3] = {0.28, 0.39, 0.62}, kSum = 4.0;
-  const double reached = E * (1.0 - std::pow(1.0 - std::min(1.0, double(top_k) / E), M));
-  const double items = reached * ((F / PARO_GROUP + 3) / 4);
+  const double items = reached(M, E, top_k) * ((F / PARO_GROUP + 3) / 4);
   MoeDownPlan best{1, 1};
   double least = 1e30;
   for (int i = 0; i < 3; ++i) {
@@ -514,9 +533,11 @@ hipError_t launch_moe_down(const MoeCall& c, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(c.D / 16 / p.tiles * p.splits)), dim3(64 * W), lds, st, a);
     return hipGetLastError();
   };
-  if (hipError_t e = p.tiles == 1   ? go(down_kernel<W, 1, 4>)
-                     : p.tiles == 2 ? go(down_kernel<W, 2, 2>)
-                                    : go(down_kernel<W, 4, 2>))
+  const bool once = reached(c.M, c.E, c.top_k) * c.F * c.D / 2 >= kOnceDown;  // (so much is cut into wide columns, nearly always)
+  if (hipError_t e = p.tiles == 1   ? go(down_kernel<W, 1, 4, false>)
+                     : p.tiles == 2 ? go(down_kernel<W, 2, 2, false>)
+                     : once         ? go(down_kernel<W, 4, 2, true>)
+                                    : go(down_kernel<W, 4, 2, false>))
     return e;
   if (p.splits > 1) {
     const int total = c.M * c.D;

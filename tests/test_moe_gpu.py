@@ -175,6 +175,68 @@ def test_rotated_experts(M, D, F, E, k, K):
     assert np.linalg.norm(got - want) <= 2.0 ** -12 * np.linalg.norm(want)
 
 
+LARGE = [  # M, D, F, E, top_k, K
+    (64, 4096, 1408, 64, 8, 0), (8, 512, 16384, 8, 4, 0), (8, 1024, 8192, 8, 4, 0), (8, 1536, 8192, 8, 4, 0), (8, 2048, 4096, 8, 4, 0),
+    (8, 2560, 2048, 16, 4, 0), (8, 5120, 2048, 8, 4, 0), (8, 8192, 1024, 8, 4, 0), (2, 16384, 1024, 4, 2, 0), (8, 512, 16384, 8, 4, 2),
+    (8, 1024, 8192, 8, 4, 2), (8, 1536, 8192, 8, 4, 2), (8, 4096, 2048, 8, 4, 2), (2, 16384, 1024, 4, 2, 2)]
+
+
+@pytest.mark.parametrize("M,D,F,E,k,K", LARGE)
+def test_large_experts(M, D, F, E, k, K):
+    """Experts of tens of megabytes, whose weights go past the caches, against the formulas in float64 on the GPU."""
+    C.log(f"large experts M={M} D={D} F={F} E={E} k={k} K={K}")
+    r = np.random.default_rng([M, D, F, E, k, K])
+    torch.manual_seed(M + D + F)
+
+    def packed(N, n):
+        q = torch.randint(0, 256, (E, N, n // 2), dtype=torch.uint8, device="cuda")
+        sc = ((torch.rand(E, N, n // 128, device="cuda") * 0.6 + 0.7) / (4.6 * n ** 0.5)).half()
+        return q, sc, torch.randint(5, 11, (E, N, n // 128), device="cuda").half()
+
+    def expert(p, e):
+        q, sc, z = (t[e] for t in p)
+        N, half = q.shape
+        q = q.view(N // 16, half // 64, 16, 64).transpose(1, 2).reshape(N, half)
+        q = torch.stack([q & 15, q >> 4], -1).view(N, half // 64, 128).double()
+        return ((q - z.double()[..., None]) * sc.double()[..., None]).view(N, 2 * half)
+
+    gu, dn = packed(2 * F, D), packed(D, F)
+    x, x64 = tokens(r, M, D)
+    ids, w = choose(r, M, E, k)
+    rots = None, None
+    if K:
+        Lx, La = W.custom_linear(51, 1, D, 16, K), W.custom_linear(52, 1, F, 16, K)
+        rots = [rl.paro_rotation_prepare(L.pairs, L.theta, L.scale) for L in (Lx, La)]
+        x64 = O.transform_activations(x64.astype(np.float16), Lx.pairs, Lx.theta, Lx.scale)
+    xd = torch.from_numpy(np.asarray(x64, np.float64)).cuda()
+    want, bound = (torch.zeros(M, D, dtype=torch.float64, device="cuda") for _ in range(2))
+    for e in range(E):
+        at = np.nonzero((ids == e).any(axis=1))[0]
+        if not len(at):
+            continue
+        we = torch.from_numpy(np.where(ids[at] == e, w[at], 0).sum(axis=1).astype(np.float64)).cuda()[:, None]
+        g, d, xe = expert(gu, e), expert(dn, e), xd[at]
+        p, off = xe @ g.T, (140 + D // 128) * U * (xe.abs() @ g.abs().T)
+        a = p[:, :F] * torch.sigmoid(p[:, :F]) * p[:, F:]
+        # block_oracle.experts derives the bound
+        gate, up, og, ou = p[:, :F].abs(), p[:, F:].abs(), off[:, :F], off[:, F:]
+        da = 1.1 * up * og + gate * ou + 1.1 * og * ou + (4 + gate) * U * a.abs()
+        da = da + (2.0 ** -11 * (a.abs() + da)).clamp(min=2.0 ** -25)
+        if K:
+            a = torch.from_numpy(np.asarray(O.transform_activations(a.cpu().numpy(), La.pairs, La.theta, La.scale), np.float64)).cuda()
+        want[at] += we * (a @ d.T)
+        bound[at] += we * (da @ d.abs().T + (160 + k + F // 128) * U * ((a.abs() + da) @ d.abs().T))
+    y, ok = guarded((M, D), torch.float32)
+    rl.paro_moe_w4a16(x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), gu, dn, *rots, out=y)
+    assert ok()
+    if K:
+        # a is off by half a float16 step of each value, 2^-11 of it at most and 2^-11 / sqrt(3) in the mean of squares; the
+        # sums turn that into as much of y, with float32's errors far below
+        assert float((y.double() - want).norm()) <= 2.0 ** -11 * float(want.norm())
+    else:
+        check(y, want.cpu().numpy(), bound.cpu().numpy(), U)
+
+
 ROUTES = [(1, 128, 1, 1), (1, 2048, 64, 8), (3, 256, 5, 5), (64, 4096, 128, 8), (17, 384, 60, 4), (64, 128, 512, 16), (33, 16384, 3, 2),
           (2, 1536, 257, 16)]
 
