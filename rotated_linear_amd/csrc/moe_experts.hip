@@ -1,8 +1,8 @@
 // The experts' products of a mixture-of-experts layer for a few tokens, on INT4 weights: gate and up with their
 // activation, then down with the sum over a token's experts. Bound by the weights' way from HBM where the experts are
 // large, and by launches where they are not. Measured (in a trace; a copy runs at 4.95 TB/s), gate and up, then down: 4
-// tokens, 2 of 8 experts, 4096 -> 14336 58 us (5.9 TB/s) and 39 us (4.4); 64 tokens, 8 of 64, 4096 -> 1408 80 (4.9) and
-// 48 (4.0); 32 tokens, 4 of 16, 4096 -> 2048 32 (4.4) and 22 (3.2); one token, 8 of 64, 2048 -> 1024 8.0 and 7.8.
+// tokens, 2 of 8 experts, 4096 -> 14336 53 us (6.4 TB/s) and 38 us (4.5); 64 tokens, 8 of 64, 4096 -> 1408 74 (5.3) and
+// 48 (4.0); 32 tokens, 4 of 16, 4096 -> 2048 31 (4.6) and 22 (3.2); one token, 8 of 64, 2048 -> 1024 7.7 and 7.7.
 #include <algorithm>
 #include <cmath>
 
@@ -41,7 +41,7 @@ __device__ inline void group_product(const uint4& w, uint32_t sz, const Rows* a,
 }
 
 // Scales and zeros come four groups at a time, 16 lanes to a group: a load for each group would cost the CU's load
-// path as much as the group's weights (gate and up of 4 tokens, 4096 -> 14336: 92 us against 54 without them, 58 so). Here
+// path as much as the group's weights (gate and up of 4 tokens, 4096 -> 14336: 92 us against 54 without them, 53 now). Here
 // every lane gets them all.
 __device__ inline void spread4(uint32_t v, uint32_t (&o)[4]) {
   const auto halves = __builtin_amdgcn_permlane32_swap(v, v, false, false);  // groups 0 1 0 1, groups 2 3 2 3
@@ -309,8 +309,9 @@ struct DownArgs {
 // took away, at no cost in loads or products (error of y, float16, one token, 8 of 64 experts 1024 -> 2048: 3.2e-4 -> 2.1e-4 of
 // y, of which its own rounding is 2.1e-4; the fuller units' a is off by 2^-12 of each value).
 //
-// What bounds it is the CU's load path: a group of 16 rows of a takes four times the loads of 16 columns' weights, so
-// more columns to a workgroup cost less, as long as there is a workgroup for each CU.
+// What bounds it is what a CU takes in, some 38 KB a microsecond here (weights from HBM and a from the L2 cache; more
+// groups in flight change nothing): a group of 16 rows of a is four times the bytes of 16 columns' weights, so more
+// columns to a workgroup cost less, as long as there is a workgroup for each CU.
 template <int W, int T, int R, bool ONCE>
 __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const DownArgs args) {
   static_assert(R == 2 || R == 4, "a group's slot is fixed");
