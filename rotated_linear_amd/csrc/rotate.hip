@@ -257,8 +257,7 @@ hipError_t launch_ppt(const RotJobs& J, int grid, hipStream_t st) {
   if (P <= 1024) return launch_exact<512, R, 2, 4, PERM, F32, LO>(J, grid, st);
   if (P <= 1536) return launch_exact<512, R, 3, (R == 4 ? 2 : 4), PERM, F32, LO>(J, grid, st);
   if (P <= 2048) return launch_exact<512, R, 4, (R == 1 ? 4 : 2), PERM, F32, LO>(J, grid, st);
-  if constexpr (!(F32 && R == 2))  // (see launch_rotate_f32_parts; so too below)
-    if (P <= 3072) return launch_exact<512, R, 6, (R == 2 ? 1 : 2), PERM, F32, LO>(J, grid, st);
+  if (P <= 3072) return launch_exact<512, R, 6, (R == 2 ? 1 : 2), PERM, F32, LO>(J, grid, st);
   // Wider rows: a workgroup's rows fill most of the LDS, so one workgroup runs per CU; 1024
   // threads (half the pairs each) give that CU twice the waves to overlap the stages' LDS
   // round trips. Measured on MI355X, K = 8: 64 x 14336 18.2 -> 14.3 us (one row per workgroup),
@@ -271,12 +270,12 @@ hipError_t launch_ppt(const RotJobs& J, int grid, hipStream_t st) {
     if (P <= 6144) return launch_exact<1024, R, 6, 2, PERM, F32, LO>(J, grid, st);
     if (P <= 7168) return launch_exact<1024, R, 7, 2, PERM, F32, LO>(J, grid, st);
     return launch_exact<512, R, 16, 1, PERM, F32, LO>(J, grid, st);
-  } else if constexpr (R == 2 && !F32) {
+  } else if constexpr (R == 2) {
     if (P <= 4608) return launch_exact<1024, R, 5, 2, PERM, F32, LO>(J, grid, st);
     if (P <= 6144) return launch_exact<1024, R, 6, 1, PERM, F32, LO>(J, grid, st);
     if (P <= 7168) return launch_exact<1024, R, 7, 1, PERM, F32, LO>(J, grid, st);
     return launch_exact<512, R, 16, 1, PERM, F32, LO>(J, grid, st);
-  } else if constexpr (R == 4) {  // only up to 9216 channels
+  } else {  // 4-row blocks only up to 9216 channels
     if (P <= 4608) return launch_exact<1024, R, 5, 1, PERM, F32, LO>(J, grid, st);
   }
   return hipErrorInvalidValue;
@@ -345,9 +344,14 @@ hipError_t launch_rotate_parts(const DevRot& R, int M, const uint16_t* x, uint16
 hipError_t launch_rotate_f32_parts(const DevRot& R, int M, const float* x, uint16_t* xout, hipStream_t st) {
   if (R.D / 2 > 8 * 1024) return hipErrorInvalidValue;
   const RotateJob job{&R, M, reinterpret_cast<const uint16_t*>(x), xout};
-  const int rows = R.D <= 4096 && M > kCUs ? 2 : 1;
-  const RotJobs J = table(&job, 1, rows);
-  return rows == 2 ? launch_ppt<2, true, true, true>(J, -J.blk0[1], st) : launch_ppt<1, true, true, true>(J, -J.blk0[1], st);
+  if (R.D > 4096 || M <= kCUs) {
+    const RotJobs J = table(&job, 1, 1);
+    return launch_ppt<1, true, true, true>(J, -J.blk0[1], st);
+  }
+  const RotJobs J = table(&job, 1, 2);
+  if (R.D <= 1024) return launch_exact<512, 2, 1, 4, true, true, true>(J, -J.blk0[1], st);
+  if (R.D <= 2048) return launch_exact<512, 2, 2, 4, true, true, true>(J, -J.blk0[1], st);
+  return launch_exact<512, 2, 4, 2, true, true, true>(J, -J.blk0[1], st);
 }
 
 hipError_t launch_rotate_batch(const RotateJob* jobs, int n, bool nibble_order, hipStream_t st) {
