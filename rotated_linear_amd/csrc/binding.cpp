@@ -394,12 +394,12 @@ bool transform(PyObject* address, PyObject* desc, int device, const paro_rotatio
   return t && t->is_cuda() && t->get_device() == device && (*r)->dev == t->const_data_ptr();
 }
 
-// (x, router or None, top_k, scoring, renormalize, ids, weights, gate_up, down, rot_x, its descriptor, rot_a, its descriptor,
-// out_dtype, out, ws) -> y, or with a router (y, ids, weights)
+// (x, router, top_k, scoring, renormalize, ids, weights, gate_up, down, rot_x, its descriptor, rot_a, its descriptor,
+// out_dtype, out, ws) -> (y, ids, weights) of the layer, or with None for the four behind x, y of the experts alone
 PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (n != 16) Py_RETURN_NONE;
-  const bool layer = a[1] != Py_None;
+  const bool layer = a[3] != Py_None;  // (not by the router: a layer without one is refused)
   const Tensor *x = tensor(a[0]), *router = nullptr, *out = a[14] == Py_None ? nullptr : tensor(a[14]);
   const Tensor* ws = a[15] == Py_None ? nullptr : tensor(a[15]);
   int device, M, D, E, k, how = 0;
