@@ -102,8 +102,8 @@ typedef struct {
  * paro_moe_w4a16 -- the experts of a few tokens, ids and weights given:
  *     y[m] = sum over j of weights[m][j] * down_e(a),  e = ids[m][j],
  *     a = silu(gate_e x'[m]) * (up_e x'[m]),
- * each product as in paro_w4a16_linear (products of float16 values exact, float32 sums). a is rounded to float16, and where
- * few tokens share an expert to two float16 parts, which leave 2^-22 of it; past float16's range it is an infinity. y is
+ * each product as in paro_w4a16_linear (products of float16 values exact, float32 sums). a is rounded to two
+ * float16 parts, which leave 2^-22 of it, or 2^-25 where that is more; past float16's range it is an infinity. y is
  * rounded once to ydtype (PARO_F16 or PARO_F32). An id outside 0..E-1 takes no expert (its weight is not read into the sum): a hole in a padded batch,
  * or an expert on another GPU; a token without experts has y = 0. An id that a token names twice counts twice.
  * x float16 [M][D]; ids int32 [M][top_k], weights float32 [M][top_k], 1 <= top_k <= PARO_MOE_MAX_K (with ids given it

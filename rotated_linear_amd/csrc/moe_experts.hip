@@ -282,7 +282,7 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
       if (c.a_fragments) {
         _Float16* const to = static_cast<_Float16*>(c.a) + row + fragment_place(n);
         *to = static_cast<_Float16>(v);
-        if (count <= kTwoParts) to[size_t(c.M) * c.top_k * c.F] = __builtin_bit_cast(_Float16, rest16(v, static_cast<_Float16>(v)));
+        to[size_t(c.M) * c.top_k * c.F] = __builtin_bit_cast(_Float16, rest16(v, static_cast<_Float16>(v)));
       } else
         static_cast<float*>(c.a)[row + n] = v;
     }
@@ -305,15 +305,17 @@ struct DownArgs {
 // A workgroup has T times 16 columns of y and its share of the items, an item being four groups of a unit: the items in
 // order are cut into splits * W equal runs, one for each wave. A wave keeps sums of its own for every token in LDS, to
 // which it adds an expert's products times the tokens' weights where it leaves the expert. R groups are in flight.
-// a is float16, but a unit of up to 8 tokens has 8 rows of the matrix products to spare: there they take what a's rounding
-// took away, at no cost in loads or products (error of y, float16, one token, 8 of 64 experts 1024 -> 2048: 3.2e-4 -> 2.1e-4 of
-// y, of which its own rounding is 2.1e-4; the fuller units' a is off by 2^-12 of each value).
+// a is in two float16 parts (one would leave an error as large as y's own rounding, 3.2e-4 of a float16 y instead of
+// 2.1e-4). A unit of up to 8 tokens has 8 rows of the matrix products to spare: they take the lower parts, at no cost in
+// loads or products. A fuller unit, which only calls of more tokens have (PARTS = 2), loads them besides and takes them
+// through products of their own (64 tokens, 8 of 64 experts, 4096 -> 1408: 48 -> 56 us). Those loads come in front of the
+// group's others: the waits count as if they were not there, and so wait for no weights that are asked for later.
 //
 // What bounds it is what a CU takes in, some 38 KB a microsecond here (weights from HBM and a from the L2 cache; more
 // groups in flight change nothing): a group of 16 rows of a is four times the bytes of 16 columns' weights, so more
 // columns to a workgroup cost less, as long as there is a workgroup for each CU.
-template <int W, int T, int R, bool ONCE>
-__global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const DownArgs args) {
+template <int W, int T, int R, int PARTS, bool ONCE>
+__global__ __launch_bounds__(64 * W, T == 4 || (T == 2 && PARTS == 2) ? 2 : 4) void down_kernel(const DownArgs args) {
   static_assert(R == 2 || R == 4, "a group's slot is fixed");
   extern __shared__ __attribute__((aligned(16))) char smem[];  // float [W][M][16 T], then the tables
   const MoeCall& c = args.c;
@@ -333,16 +335,18 @@ __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const Down
   uint32_t wo = nl * 64 + h * 16, so = 0, ao = 0;  // this lane's part of a group of 16 rows, its scale and zero, its row of a
   f4 acc[T] = {};
   uint4 w[R][T];
-  Rows a[R];
+  Rows a[R][PARTS];
   uint32_t scale[T], zero[T], sz[T][4];
   // the item that is loaded next: its unit, four groups and addresses; and the one that is used next
   int lu = begin / Q, lq = begin - lu * Q, uu = lu, uq = lq, left = end - begin;
+  bool lfull = false, ufull = false;  // their units have more than kTwoParts tokens
   const char *wp = nullptr, *sp = nullptr, *zp = nullptr;
   auto aim = [&]() {  // (no global access: the wait counts stay exact)
     const MoeUnit k = unit[lu];
-    const bool both = k.count <= kTwoParts;
-    const int r = min(both ? nl % kTwoParts : nl, k.count - 1);
-    ao = (uint32_t(slot[k.first + r].pair) + (both && nl >= kTwoParts ? pairs : 0)) * uint32_t(c.F) * 2 + h * (c.a_fragments ? 16 : 64);
+    const int count = __builtin_amdgcn_readfirstlane(k.count);
+    lfull = PARTS == 2 && count > kTwoParts;
+    const int r = min(lfull ? nl : nl % kTwoParts, count - 1);
+    ao = (uint32_t(slot[k.first + r].pair) + (!lfull && nl >= kTwoParts ? pairs : 0)) * uint32_t(c.F) * 2 + h * (c.a_fragments ? 16 : 64);
     const size_t row = size_t(__builtin_amdgcn_readfirstlane(k.expert)) * c.D + tile * 16 * T;
     wp = reinterpret_cast<const char*>(c.dn_qw) + row * (c.F / 2);
     sp = reinterpret_cast<const char*>(c.dn_sc) + row * G * 2;
@@ -362,12 +366,14 @@ __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const Down
       for (int t = 0; t < T; ++t) load_scales(scale[t], zero[t], sp + size_t(t) * 32 * G, zp + size_t(t) * 32 * G, so);
     }
     const uint32_t g = min(4 * lq + p, G - 1);
+    if (PARTS == 2 && lfull) load_rows(a[q][PARTS - 1], c.a_down + (size_t(pairs) * c.F + g * PARO_GROUP), ao, c.a_fragments ? 64 : 16);
 #pragma unroll
     for (int t = 0; t < T; ++t) w[q][t] = load_weights<ONCE>(wp + size_t(t) * 8 * c.F + g * 1024, wo);
-    load_rows(a[q], c.a_down + g * PARO_GROUP, ao, c.a_fragments ? 64 : 16);
+    load_rows(a[q][0], c.a_down + g * PARO_GROUP, ao, c.a_fragments ? 64 : 16);
   };
   if (begin < end) {
     aim();
+    ufull = lfull;
 #pragma unroll
     for (int q = 0; q < R; ++q) load(q, q);
     for (int n = end - begin; n > 0; --n) {
@@ -378,11 +384,19 @@ __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const Down
 #pragma unroll
           for (int t = 0; t < T; ++t) spread4(scale[t] | zero[t] << 16, sz[t]);
         }
-        if (p == 0 || 4 * uq + p < G) {  // uniform
+        if (p == 0 || 4 * uq + p < G) {  // uniform, as full is
+          if (PARTS == 2 && ufull) {
 #pragma unroll
-          for (int t = 0; t < T; ++t) {
-            group_product(w[p % R][t], sz[t][p], &a[p % R], acc[t]);
-            settled(acc[t]);
+            for (int t = 0; t < T; ++t) {
+              group_product<PARTS>(w[p % R][t], sz[t][p], a[p % R], acc[t]);
+              settled(acc[t]);
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+              group_product(w[p % R][t], sz[t][p], a[p % R], acc[t]);
+              settled(acc[t]);
+            }
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -392,7 +406,7 @@ __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const Down
       __builtin_amdgcn_sched_barrier(0);
       if (++uq == Q || n == 1) {
         const MoeUnit k = unit[uu];
-        if (k.count <= kTwoParts) {  // lanes 32..63 have the lower parts' sums
+        if (!ufull) {  // lanes 32..63 have the lower parts' sums
 #pragma unroll
           for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -415,6 +429,7 @@ __global__ __launch_bounds__(64 * W, T == 4 ? 2 : 4) void down_kernel(const Down
         for (int t = 0; t < T; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
         uq = 0;
         ++uu;
+        if (PARTS == 2 && n > 1) ufull = __builtin_amdgcn_readfirstlane(unit[uu].count) > kTwoParts;
       }
     }
   }
@@ -535,10 +550,11 @@ hipError_t launch_moe_down(const MoeCall& c, hipStream_t st) {
     return hipGetLastError();
   };
   const bool once = reached(c.M, c.E, c.top_k) * c.F * c.D / 2 >= kOnceDown;  // (so much is cut into wide columns, nearly always)
-  if (hipError_t e = p.tiles == 1   ? go(down_kernel<W, 1, 4, false>)
-                     : p.tiles == 2 ? go(down_kernel<W, 2, 2, false>)
-                     : once         ? go(down_kernel<W, 4, 2, true>)
-                                    : go(down_kernel<W, 4, 2, false>))
+  const bool few = c.M <= kTwoParts;
+  if (hipError_t e = p.tiles == 1   ? few ? go(down_kernel<W, 1, 4, 1, false>) : go(down_kernel<W, 1, 2, 2, false>)
+                     : p.tiles == 2 ? few ? go(down_kernel<W, 2, 2, 1, false>) : go(down_kernel<W, 2, 2, 2, false>)
+                     : once         ? few ? go(down_kernel<W, 4, 2, 1, true>) : go(down_kernel<W, 4, 2, 2, true>)
+                                    : few ? go(down_kernel<W, 4, 2, 1, false>) : go(down_kernel<W, 4, 2, 2, false>))
     return e;
   if (p.splits > 1) {
     const int total = c.M * c.D;

@@ -20,7 +20,8 @@ struct MoeTables {
   MoeUnit* unit;
   MoeSlot* slot;
 };
-// The rows of a matrix product are 16: a unit of up to 8 tokens has room for both parts of its rows of a.
+// The rows of a matrix product are 16: a unit of up to 8 tokens has room for both parts of its rows of a, and a call of
+// up to 8 tokens has no other units.
 constexpr int kTwoParts = 8;
 int moe_units_max(int M, int E, int top_k);
 
@@ -30,7 +31,7 @@ struct MoeCall {
   bool x_parts;  // a transform's rows: 8-channel words as [0,4,1,5,2,6,3,7], and [M][D] more, what their rounding took away
   bool a_fragments;     // a is float16 in the order of fragments; else, with a transform behind it, float32 as it is, and
                         // a_down float16 in the nibble order. Behind float16 rows [M top_k][F] of a as many more, what
-                        // their rounding took away, where a unit has few tokens (kTwoParts)
+                        // their rounding took away
   const uint8_t* gu_qw;
   const uint16_t* gu_sc;
   const uint16_t* gu_zr;
