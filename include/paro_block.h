@@ -102,16 +102,19 @@ typedef struct {
  * paro_moe_w4a16 -- the experts of a few tokens, ids and weights given:
  *     y[m] = sum over j of weights[m][j] * down_e(a),  e = ids[m][j],
  *     a = silu(gate_e x'[m]) * (up_e x'[m]),
- * each product as in paro_w4a16_linear (products of float16 values exact, float32 sums). a is rounded to two
- * float16 parts, which leave 2^-22 of it, or 2^-25 where that is more; past float16's range it is an infinity. y is
- * rounded once to ydtype (PARO_F16 or PARO_F32). An id outside 0..E-1 takes no expert (its weight is not read into the sum): a hole in a padded batch,
- * or an expert on another GPU; a token without experts has y = 0. An id that a token names twice counts twice.
+ * each product as in paro_w4a16_linear (products of float16 values exact, float32 sums). a is rounded to two float16
+ * parts times a power of two by the norm |x[m]| of the token's row. They leave 2^-22 of it, or 2^-38 |x[m]|^2 where that
+ * is more; past 2^11 |x[m]|^2, where no a gets if the norms of gate's and up's rows multiply to less than 2^11, it may be
+ * an infinity. y is rounded once to ydtype (PARO_F16 or PARO_F32). An id outside 0..E-1 takes no expert (its weight is not
+ * read into the sum): a hole in a padded batch, or an expert on another GPU; a token without experts has y = 0. An id that
+ * a token names twice counts twice.
  * x float16 [M][D]; ids int32 [M][top_k], weights float32 [M][top_k], 1 <= top_k <= PARO_MOE_MAX_K (with ids given it
  * may pass E); gate_up [E][2 F][D] (gate rows, then up rows), down [E][D][F]. With rot_x (D channels), x' is the
- * transform of x in float32 (as two float16 parts), else x; with rot_a (F channels), a is the transform of silu(gate) * up,
- * in float32 until its rounding. Both are shared by all experts, whose weights are packed with them. D and F as D in
- * paro.h. A row of x with a NaN or an infinity reaches no other row of y; an expert that no token names is not read. How
- * many tokens share an expert may change the last bits of a token's row. ws holds at least
+ * transform of x in float32, rounded to two such parts (which leave 2^-22 of it, or 2^-35 |x[m]|; past 2^15 |x[m]| it may
+ * be an infinity), else x; with rot_a (F channels), a is the transform of silu(gate) * up, in float32 until its rounding.
+ * Both are shared by all experts, whose weights are packed with them. D and F as D in paro.h. A row of x with a NaN or an
+ * infinity reaches no other row of y; an expert that no token names is not read. How many tokens share an expert may
+ * change the last bits of the float32 sums. ws holds at least
  * paro_moe_workspace_bytes(M, D, F, E, top_k) bytes (else PARO_EWORKSPACE).
  */
 size_t paro_moe_workspace_bytes(int M, int D, int F, int E, int top_k);

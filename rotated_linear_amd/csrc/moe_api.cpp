@@ -14,7 +14,7 @@ bool good_sizes(int M, int E, int top_k, bool routed) {
 
 // A workspace's sections, each at a multiple of 256 bytes.
 struct Layout {
-  size_t logits, x, a, a_rotated, part, units, unit, slot, total;
+  size_t logits, x, a, a_rotated, part, units, unit, slot, power, total;
 };
 Layout layout(int M, int D, int F, int E, int top_k) {
   Layout l;
@@ -34,6 +34,7 @@ Layout layout(int M, int D, int F, int E, int top_k) {
   l.units = take(4);
   l.unit = take(size_t(moe_units_max(M, E, top_k)) * sizeof(MoeUnit));
   l.slot = take(pairs * sizeof(MoeSlot));
+  l.power = take(size_t(M) * 4);
   l.total = at;
   return l;
 }
@@ -101,21 +102,23 @@ paro_status experts(int M, int D, int F, int E, int top_k, const void* x, const 
   c.a_fragments = rot_a == nullptr;
   c.part = reinterpret_cast<float*>(base + l.part);
   c.t = MoeTables{reinterpret_cast<int*>(base + l.units), reinterpret_cast<MoeUnit*>(base + l.unit), reinterpret_cast<MoeSlot*>(base + l.slot)};
+  int* const power = reinterpret_cast<int*>(base + l.power);
+  c.power = power;
   c.y = y;
   c.ydtype = ydtype;
   const hipStream_t st = as_stream(stream);
   hipError_t e = hipSuccess;
   if (r) {
     const MoeRoute route{M, D, E, top_k, c.x, r->router, r->dtype == PARO_F32, r->scoring == PARO_MOE_SIGMOID, r->renormalize != 0,
-                         reinterpret_cast<double*>(base + l.logits), ids, weights};
+                         reinterpret_cast<double*>(base + l.logits), ids, weights, power};
     e = launch_moe_logits(route, st);
     if (e == hipSuccess) e = launch_moe_select(route, &c.t, st);
   } else {
-    e = launch_moe_group(M, E, top_k, ids, weights, c.t, st);
+    e = launch_moe_group(M, D, E, top_k, c.x, ids, weights, c.t, power, st);
   }
   if (e == hipSuccess && rot_x) {
     uint16_t* const xr = reinterpret_cast<uint16_t*>(base + l.x);
-    e = launch_rotate_parts(rx, M, c.x, xr, st);
+    e = launch_rotate_parts(rx, M, c.x, xr, RowPower{power, 1, 0, 1}, st);
     c.x = xr;
     c.x_parts = true;
   }
@@ -123,7 +126,7 @@ paro_status experts(int M, int D, int F, int E, int top_k, const void* x, const 
   if (e == hipSuccess && rot_a) {
     // (every row there may be: those of pairs without an expert hold what they held, and no product reads them)
     uint16_t* const ar = reinterpret_cast<uint16_t*>(base + l.a_rotated);
-    e = launch_rotate_f32_parts(ra, M * top_k, static_cast<const float*>(c.a), ar, st);
+    e = launch_rotate_f32_parts(ra, M * top_k, static_cast<const float*>(c.a), ar, RowPower{power, top_k, kLiftA, 2}, st);
     c.a_down = ar;
   }
   if (e == hipSuccess) e = launch_moe_down(c, st);
@@ -153,7 +156,7 @@ paro_status paro_moe_route(int M, int D, int E, int top_k, const void* x, const 
   const Span ins[] = {{x, size_t(M) * D * 2}, {router, router_bytes(r, D, E)}};
   if (any_overlap(outs, ins)) return PARO_EINVAL;
   const MoeRoute route{M, D, E, top_k, static_cast<const uint16_t*>(x), router, router_dtype == PARO_F32, scoring == PARO_MOE_SIGMOID,
-                       renormalize != 0, static_cast<double*>(ws), ids, weights};
+                       renormalize != 0, static_cast<double*>(ws), ids, weights, nullptr};
   const hipStream_t st = as_stream(stream);
   hipError_t e = launch_moe_logits(route, st);
   if (e == hipSuccess) e = launch_moe_select(route, nullptr, st);

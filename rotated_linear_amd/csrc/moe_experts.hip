@@ -21,21 +21,25 @@ struct Rows {
 };
 
 // sum[row of x][row of w] += the group's products. sz: the scale and, in the upper half, the zero of the lane's row.
-// PARTS: a[0] and a[PARTS - 1] are the rows' upper and lower parts, else there is a[0] alone.
+// PARTS = 2: a[0] and a[1] are the rows' upper and lower parts, else there is a[0] alone.
 template <int PARTS = 1>
 __device__ inline void group_product(const uint4& w, uint32_t sz, const Rows* a, f4& sum) {
   const _Float16 z = __builtin_bit_cast(_Float16, uint16_t(sz >> 16));
   const _Float16 zl = -(static_cast<_Float16>(1024.0f) + z), zh = -(static_cast<_Float16>(64.0f) + z);
   const h2 zlo = {zl, zl}, zhi = {zh, zh};
   const uint32_t wv[4] = {w.x, w.y, w.z, w.w};
-  f4 g = {0.f, 0.f, 0.f, 0.f};
+  f4 g = {0.f, 0.f, 0.f, 0.f}, low = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const h8 b = dequant_word(wv[k], zlo, zhi, 0x000F000Fu, 0x00F000F0u, 0x64006400u);
     g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0].v[k], b, g, 0, 0, 0);
-    if constexpr (PARTS == 2) g = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1].v[k], b, g, 0, 0, 0);
+    if constexpr (PARTS == 2) low = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1].v[k], b, low, 0, 0, 0);
   }
   const float s = static_cast<float>(__builtin_bit_cast(_Float16, uint16_t(sz)));
+  if constexpr (PARTS == 2) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) g[i] = __builtin_fmaf(kRestDown, low[i], g[i]);
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) sum[i] = __builtin_fmaf(s, g[i], sum[i]);
 }
@@ -111,7 +115,8 @@ __device__ inline int fragment_place(int n) {
 // in registers (GW = 0: any number, w, w + W, ..., read again for each tile). Weights come straight into a ring of
 // registers, R groups ahead, from tile to tile without a break: a tile's gate rows, then its up rows. Every kPark
 // tiles, and where the unit ends, the waves' sums meet in LDS.
-// PARTS = 2: the tokens' rows come from a transform, in two float16 parts, and take twice the registers and products.
+// PARTS = 2: the tokens' rows come from a transform, in two float16 parts, and take twice the registers and products (with
+// sums of their own, group by group, for the lower parts).
 // How many waves, and so how many groups to each, is a matter of registers: 16 waves on a CU leave each 128.
 constexpr int kPark = 4;
 template <int W, int GW, int PARTS, bool ONCE>
@@ -194,6 +199,7 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
   Rows a[GW ? GW : 2][PARTS];
   int unit = begin / per_unit, tile = begin - unit * per_unit, first = 0, count = 0;
   uint32_t xo = 0;
+  uint32_t mine = 0;  // of the token whose results this thread makes: its pair, and its row's power in the upper half
   // a group of the unit's tokens; past the last one zeros, so that its products are
   auto rows = [&](int q, int i) {
 #pragma unroll
@@ -213,6 +219,8 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
     first = __builtin_amdgcn_readfirstlane(c.t.unit[unit].first);
     count = __builtin_amdgcn_readfirstlane(c.t.unit[unit].count);
     xo = uint32_t(c.t.slot[first + min(nl, count - 1)].token) * uint32_t(c.D) * 2 + h * 64;
+    const MoeSlot s = c.t.slot[first + min(tid >> 4 & 15, count - 1)];
+    mine = s.pair | uint32_t(c.power[s.token]) << 16;
     if constexpr (GW > 0) {
 #pragma unroll
       for (int i = 0; i < GW; ++i) rows(i, i);
@@ -267,6 +275,7 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
     ++parked;
     if (parked < kPark && tile < per_unit && t < end) continue;
     __syncthreads();
+    static_assert(64 * W % 256 == 0, "a thread has one token");
     for (int o = tid; o < parked * 256; o += 64 * W) {
       const int col = o & 15, m = o >> 4 & 15, j = o >> 8, l = (m >> 2) * 16 + col, i = m & 3;
       if (m >= count) continue;
@@ -276,10 +285,16 @@ __global__ __launch_bounds__(64 * W, 4) void gate_up_kernel(const MoeCall c) {
         gate += red[j][0][v][l][i];
         upv += red[j][1][v][l][i];
       }
-      const float v = gate / (1.0f + expf(-gate)) * upv;
-      const size_t row = size_t(c.t.slot[first + m].pair) * c.F;
+      const int power = int(mine) >> 16;
+      if constexpr (PARTS == 2) {
+        gate *= power2(power);
+        upv *= power2(power);
+      }
+      float v = gate / (1.0f + expf(-gate)) * upv;
+      const size_t row = size_t(mine & 0xFFFFu) * c.F;
       const int n = (tile - parked + j) * 16 + col;
       if (c.a_fragments) {
+        v *= power2(kLiftA - 2 * power);
         _Float16* const to = static_cast<_Float16*>(c.a) + row + fragment_place(n);
         *to = static_cast<_Float16>(v);
         to[size_t(c.M) * c.top_k * c.F] = __builtin_bit_cast(_Float16, rest16(v, static_cast<_Float16>(v)));
@@ -317,7 +332,7 @@ struct DownArgs {
 template <int W, int T, int R, int PARTS, bool ONCE>
 __global__ __launch_bounds__(64 * W, T == 4 || (T == 2 && PARTS == 2) ? 2 : 4) void down_kernel(const DownArgs args) {
   static_assert(R == 2 || R == 4, "a group's slot is fixed");
-  extern __shared__ __attribute__((aligned(16))) char smem[];  // float [W][M][16 T], then the tables
+  extern __shared__ __attribute__((aligned(16))) char smem[];  // float [W][M][16 T], then the tables, then float [M]
   const MoeCall& c = args.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), nl = lane & 15, h = lane >> 4;
   const int pairs = c.M * c.top_k, tile = blockIdx.x / args.splits, split = blockIdx.x - tile * args.splits;
@@ -326,6 +341,8 @@ __global__ __launch_bounds__(64 * W, T == 4 || (T == 2 && PARTS == 2) ? 2 : 4) v
   MoeSlot* const slot = reinterpret_cast<MoeSlot*>(all + W * c.M * 16 * T);
   MoeUnit* const unit = reinterpret_cast<MoeUnit*>(slot + pairs);
   const int units = *c.t.units;
+  float* const undo = reinterpret_cast<float*>(unit + units);  // [M]: what takes a's power of two off again
+  for (int i = tid; i < c.M; i += 64 * W) undo[i] = power2(2 * c.power[i] - kLiftA);
   for (int i = tid; i < pairs; i += 64 * W) slot[i] = c.t.slot[i];  // (those past the last one are not used)
   for (int i = tid; i < units; i += 64 * W) unit[i] = c.t.unit[i];
   for (int i = lane; i < c.M * 16 * T; i += 64) sums[i] = 0;
@@ -410,7 +427,7 @@ __global__ __launch_bounds__(64 * W, T == 4 || (T == 2 && PARTS == 2) ? 2 : 4) v
 #pragma unroll
           for (int t = 0; t < T; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] += __shfl_xor(acc[t][i], 32);
+            for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(kRestDown, __shfl_xor(acc[t][i], 32), acc[t][i]);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -418,10 +435,11 @@ __global__ __launch_bounds__(64 * W, T == 4 || (T == 2 && PARTS == 2) ? 2 : 4) v
           if (r < k.count) {
             // (an expert has a token once: no two lanes meet)
             const MoeSlot o = slot[k.first + r];
+            const float by = undo[o.token];
 #pragma unroll
             for (int t = 0; t < T; ++t) {
               float& v = sums[(o.token * T + t) * 16 + nl];
-              v = __builtin_fmaf(o.weight, acc[t][i], v);
+              v = __builtin_fmaf(o.weight, acc[t][i] * by, v);
             }
           }
         }
@@ -487,7 +505,7 @@ hipError_t launch_gate_up(const MoeCall& c, hipStream_t st) {
 
 constexpr int kDownWaves = 8;
 constexpr size_t down_lds(int T, int M, int units, int pairs) {
-  return size_t(kDownWaves) * T * M * 64 + sizeof(MoeSlot) * pairs + sizeof(MoeUnit) * units;
+  return size_t(kDownWaves) * T * M * 64 + sizeof(MoeSlot) * pairs + sizeof(MoeUnit) * units + 4 * M;
 }
 static_assert(down_lds(4, PARO_MOE_MAX_M, PARO_MOE_MAX_E + PARO_MOE_MAX_M, PARO_MOE_MAX_M * PARO_MOE_MAX_K) <= 160 * 1024, "a CU's LDS");
 

@@ -58,13 +58,43 @@ __device__ inline double traded_sum(double a, double b) {
   return __builtin_bit_cast(double, lo) + __builtin_bit_cast(double, hi);
 }
 
-// A workgroup has MT tokens and ET experts; its threads take 8 channels at a time.
+// The power of a row of x (moe_internal.h), by all threads of a workgroup: 2^power is over its norm and at most twice it;
+// 0 for a row of zeros, and for one that has no finite norm.
+__device__ inline void row_power(const uint16_t* x, int D, int* power) {
+  __shared__ double part[kWaves];
+  const int tid = threadIdx.x;
+  double v = 0;
+  for (int c = tid; c < D / 8; c += 64 * kWaves) {
+    const h8 w = *reinterpret_cast<const h8*>(x + c * 8);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v = __builtin_fma(double(float(w[k])), double(float(w[k])), v);
+  }
+  v = wave_sum(v);
+  if ((tid & 63) == 0) part[tid >> 6] = v;
+  __syncthreads();
+  if (tid == 0) {
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) v += part[i];
+    const int e = int(__builtin_bit_cast(uint64_t, v) >> 52);  // (exact squares: no subnormal sums)
+    *power = e == 0 || e == 2047 ? 0 : ((e - 1023) >> 1) + 1;
+  }
+}
+
+// A workgroup has MT tokens and ET experts; its threads take 8 channels at a time. With r.power there are MT more to each
+// row of the grid, for the powers of its tokens.
 template <bool F32, int MT, int ET>
 __global__ __launch_bounds__(64 * kWaves) void logits_kernel(const MoeRoute r) {
   constexpr int V = MT * ET;
   __shared__ double part[kWaves][V];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int e0 = blockIdx.x * ET, m0 = blockIdx.y * MT;
+  const int tiles = (r.E + ET - 1) / ET;
+  if (int(blockIdx.x) >= tiles) {
+    const int m = m0 + blockIdx.x - tiles;
+    if (m < r.M) row_power(r.x + size_t(m) * r.D, r.D, r.power + m);
+    return;
+  }
   double acc[V] = {};
   for (int c = tid; c < r.D / 8; c += 64 * kWaves) {
     float w[ET][8];
@@ -249,8 +279,14 @@ __global__ __launch_bounds__(kOneGroup) void select_one_kernel(const MoeRoute r,
   }
 }
 
-__global__ __launch_bounds__(PARO_MOE_MAX_E) void group_kernel(int M, int E, int top_k, const int32_t* given_ids,
-                                                               const float* given_weights, const MoeTables t) {
+// One workgroup makes the tables; with more, each of the others has the power of a row of x.
+static_assert(PARO_MOE_MAX_E == 64 * kWaves, "row_power's threads");
+__global__ __launch_bounds__(PARO_MOE_MAX_E) void group_kernel(int M, int D, int E, int top_k, const uint16_t* x, const int32_t* given_ids,
+                                                               const float* given_weights, const MoeTables t, int* power) {
+  if (blockIdx.x > 0) {
+    row_power(x + size_t(blockIdx.x - 1) * D, D, power + blockIdx.x - 1);
+    return;
+  }
   __shared__ TableWork work;
   __shared__ int ids[kMaxM * kMaxK];
   __shared__ float weights[kMaxM * kMaxK];
@@ -281,7 +317,7 @@ __global__ __launch_bounds__(PARO_MOE_MAX_E) void group_kernel(int M, int E, int
 
 template <int MT, int ET>
 hipError_t launch_logits(const MoeRoute& r, hipStream_t st) {
-  const dim3 grid(unsigned((r.E + ET - 1) / ET), unsigned((r.M + MT - 1) / MT));
+  const dim3 grid(unsigned((r.E + ET - 1) / ET + (r.power ? MT : 0)), unsigned((r.M + MT - 1) / MT));
   if (r.router_f32)
     hipLaunchKernelGGL((logits_kernel<true, MT, ET>), grid, dim3(64 * kWaves), 0, st, r);
   else
@@ -312,11 +348,12 @@ hipError_t launch_moe_select(const MoeRoute& r, const MoeTables* t, hipStream_t 
     return hipGetLastError();
   };
   if (hipError_t e = r.E <= 64 ? go(select_kernel<16>) : r.E <= 256 ? go(select_kernel<4>) : go(select_kernel<2>)) return e;
-  return t ? launch_moe_group(r.M, r.E, r.top_k, r.ids, r.weights, *t, st) : hipSuccess;
+  return t ? launch_moe_group(r.M, r.D, r.E, r.top_k, nullptr, r.ids, r.weights, *t, nullptr, st) : hipSuccess;
 }
 
-hipError_t launch_moe_group(int M, int E, int top_k, const int32_t* ids, const float* weights, const MoeTables& t, hipStream_t st) {
-  hipLaunchKernelGGL(group_kernel, dim3(1), dim3(PARO_MOE_MAX_E), 0, st, M, E, top_k, ids, weights, t);
+hipError_t launch_moe_group(int M, int D, int E, int top_k, const uint16_t* x, const int32_t* ids, const float* weights, const MoeTables& t,
+                            int* power, hipStream_t st) {
+  hipLaunchKernelGGL(group_kernel, dim3(x ? 1 + M : 1), dim3(PARO_MOE_MAX_E), 0, st, M, D, E, top_k, x, ids, weights, t, power);
   return hipGetLastError();
 }
 

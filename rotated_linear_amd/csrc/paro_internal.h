@@ -144,10 +144,15 @@ hipError_t launch_pack(const DevRot& R, int N, const uint16_t* W, uint8_t* qweig
 // nibble_order: write each 8-channel word as [0,4,1,5,2,6,3,7] (the decode kernel's A order).
 hipError_t launch_rotate(const DevRot& R, int M, const uint16_t* x, uint16_t* xout, bool nibble_order,
                          hipStream_t st);
-// For few rows, in the nibble order: float16 rows [M][D], and behind them [M][D] what their rounding took away.
-hipError_t launch_rotate_parts(const DevRot& R, int M, const uint16_t* x, uint16_t* xout, hipStream_t st);
+// Row m of a transform's output is multiplied by 2^(add - times * power[m / per]).
+struct RowPower {
+  const int* power;
+  int per, add, times;
+};
+// For few rows, in the nibble order and in two float16 parts (w4_device.h): [M][D], and behind them [M][D] the lower parts.
+hipError_t launch_rotate_parts(const DevRot& R, int M, const uint16_t* x, uint16_t* xout, const RowPower& p, hipStream_t st);
 // The same from float32 rows.
-hipError_t launch_rotate_f32_parts(const DevRot& R, int M, const float* x, uint16_t* xout, hipStream_t st);
+hipError_t launch_rotate_f32_parts(const DevRot& R, int M, const float* x, uint16_t* xout, const RowPower& p, hipStream_t st);
 // Several transforms of the same D (each with its own descriptor, x and output) in as few
 // launches as the GPU holds at once (up to kRotMaxJobs per launch).
 constexpr int kRotMaxJobs = 16;

@@ -60,6 +60,7 @@ struct RotJobs {
   int K[kRotMaxJobs];
   int blk0[kRotMaxJobs + 1];
   int n, D;
+  RowPower power;  // of outputs in two parts
 };
 
 // Two adjacent channels as they are read.
@@ -121,7 +122,10 @@ __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
   // formed there and not kept live (or spilled) across the stages.
   using Pair = ChannelPair<F32>;
   typename Pair::T hv[PPT][R];
+  int power[LO ? R : 1];  // (asked for with the rows: it is not waited for behind them)
   auto load_rows = [&](int b) {
+#pragma unroll
+    for (int r = 0; r < (LO ? R : 0); ++r) power[r] = J.power.power[min(b * R + r, M - 1) / J.power.per];
     const int tl = fresh_tid();
     uintptr_t xb = reinterpret_cast<uintptr_t>(x);
     asm volatile("" : "+s"(xb));
@@ -167,6 +171,9 @@ __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
   for (;;) {
     const int next = blk + int(gridDim.x);
     const bool more = next < nblk;  // uniform
+    float by[LO ? R : 1];
+#pragma unroll
+    for (int r = 0; r < (LO ? R : 0); ++r) by[r] = power2(J.power.add - J.power.times * power[r]);
     if (more) load_rows(next);
     if (K > 0) ring_run<R>(ring, lds, K, P, tid, recs);  // ends with a barrier
 
@@ -184,7 +191,11 @@ __global__ __launch_bounds__(NT) void rotate_rows_kernel(const RotJobs J) {
       const V va = sw ? w2 : w1, vb = sw ? w1 : w2;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float fa = vec_at<R>(va, r) * isa[u], fb = vec_at<R>(vb, r) * isc[u];
+        float fa = vec_at<R>(va, r) * isa[u], fb = vec_at<R>(vb, r) * isc[u];
+        if constexpr (LO) {
+          fa *= by[r];
+          fb *= by[r];
+        }
         const _Float16 ha = static_cast<_Float16>(fa), hb = static_cast<_Float16>(fb);
         ov[u][r] = __builtin_bit_cast(uint16_t, ha) | uint32_t(__builtin_bit_cast(uint16_t, hb)) << 16;
         if constexpr (LO) ol[u][r] = rest16(fa, ha) | uint32_t(rest16(fb, hb)) << 16;
@@ -333,22 +344,22 @@ hipError_t launch_rotate(const DevRot& R, int M, const uint16_t* x, uint16_t* xo
   return launch_jobs(&job, 1, rows_per_block(R.D, M), nibble_order, st);
 }
 
-hipError_t launch_rotate_parts(const DevRot& R, int M, const uint16_t* x, uint16_t* xout, hipStream_t st) {
+hipError_t launch_rotate_parts(const DevRot& R, int M, const uint16_t* x, uint16_t* xout, const RowPower& p, hipStream_t st) {
   if (R.D / 2 > 8 * 1024) return hipErrorInvalidValue;
   const RotateJob job{&R, M, x, xout};
-  const RotJobs J = table(&job, 1, 1);
+  RotJobs J = table(&job, 1, 1);
+  J.power = p;
   return launch_ppt<1, true, false, true>(J, -J.blk0[1], st);
 }
 
 // (Blocks of two rows hold twice the registers of float32 rows: only where a thread has few pairs.)
-hipError_t launch_rotate_f32_parts(const DevRot& R, int M, const float* x, uint16_t* xout, hipStream_t st) {
+hipError_t launch_rotate_f32_parts(const DevRot& R, int M, const float* x, uint16_t* xout, const RowPower& p, hipStream_t st) {
   if (R.D / 2 > 8 * 1024) return hipErrorInvalidValue;
   const RotateJob job{&R, M, reinterpret_cast<const uint16_t*>(x), xout};
-  if (R.D > 4096 || M <= kCUs) {
-    const RotJobs J = table(&job, 1, 1);
-    return launch_ppt<1, true, true, true>(J, -J.blk0[1], st);
-  }
-  const RotJobs J = table(&job, 1, 2);
+  const bool two = R.D <= 4096 && M > kCUs;
+  RotJobs J = table(&job, 1, two ? 2 : 1);
+  J.power = p;
+  if (!two) return launch_ppt<1, true, true, true>(J, -J.blk0[1], st);
   if (R.D <= 1024) return launch_exact<512, 2, 1, 4, true, true, true>(J, -J.blk0[1], st);
   if (R.D <= 2048) return launch_exact<512, 2, 2, 4, true, true, true>(J, -J.blk0[1], st);
   return launch_exact<512, 2, 4, 2, true, true, true>(J, -J.blk0[1], st);

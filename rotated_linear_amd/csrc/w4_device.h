@@ -5,11 +5,16 @@
 
 namespace paro {
 
-// What the rounding of v to h takes away, as float16 (0 where v has no number, and where h has none, past 65504).
+// Float32 values in two float16 parts. The lower part is what the rounding of v to h takes away times 2^11, which makes it
+// as large as v at most: it has its 11 bits as long as h has its own. The two leave 2^-22 of v, or 2^-36 where that is more
+// (under 2^-14). (The lower part is 0 where v has no number, and where h has none, past 65504.)
+constexpr float kRestUp = 0x1p11f, kRestDown = 0x1p-11f;
 __device__ inline uint16_t rest16(float v, _Float16 h) {
-  const float d = v - static_cast<float>(h);
+  const float d = (v - static_cast<float>(h)) * kRestUp;
   return __builtin_bit_cast(uint16_t, static_cast<_Float16>(fabsf(d) < 65504.0f ? d : 0.0f));
 }
+// 2^e, -126 <= e <= 127.
+__device__ inline float power2(int e) { return __builtin_bit_cast(float, (e + 127) << 23); }
 
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));

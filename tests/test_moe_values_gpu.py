@@ -48,3 +48,67 @@ def test_digits_of_the_rows_between_the_products(M, E, k, K):
     want, _ = B.experts(np.asarray(x64, np.float64), ids, w.astype(np.float64), gw, dw, between)
     y = rl.paro_moe_w4a16(x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), gu, dn, *rots, out_dtype=torch.float32)
     assert relative(y, want) <= EXACT
+
+
+@pytest.mark.parametrize("M,E,k", [(1, 2, 2), (8, 3, 2), (40, 3, 2)])
+@pytest.mark.parametrize("K", [0, 2])
+def test_rows_of_every_scale(M, E, k, K):
+    """Rows from 2^-14 to 2^13 side by side, so that the rows between the products run from 2^-30 to 2^27: each
+    keeps its digits."""
+    D, F = 256, 384
+    C.log(f"scales M={M} E={E} k={k} K={K}")
+    r = np.random.default_rng([M, E, k, K, 1])
+    gu, gw = pack(r, E, 2 * F, D)
+    dn, dw = pack(r, E, D, F)
+    rots, between = (None, None), None
+    if K:
+        Lx, La = W.custom_linear(51, 1, D, 16, K), W.custom_linear(52, 1, F, 16, K)
+        rots = [rl.paro_rotation_prepare(L.pairs, L.theta, L.scale) for L in (Lx, La)]
+
+        def between(a):
+            return O.transform_activations(a, La.pairs, La.theta, La.scale)
+
+    ids, w = choose(r, M, E, k)
+    for powers in ([-14], [-8], [8], [13], [-14, -3, 13, 6]):
+        x64 = r.normal(0, 1, (M, D)).clip(-3.9, 3.9) * np.exp2(np.resize(powers, M))[:, None]
+        x64[0, 7] = 3.9 * 2.0 ** powers[0]
+        x = torch.from_numpy(x64.astype(np.float16)).cuda()
+        x64 = x.cpu().numpy().astype(np.float64)
+        assert np.isfinite(x64).all()
+        if K:
+            x64 = np.asarray(O.transform_activations(x64.astype(np.float16), Lx.pairs, Lx.theta, Lx.scale), np.float64)
+        want, _ = B.experts(x64, ids, w.astype(np.float64), gw, dw, between)
+        y = rl.paro_moe_w4a16(x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), gu, dn, *rots, out_dtype=torch.float32)
+        for m in range(M):
+            assert relative(y[m], want[m]) <= EXACT, (powers, m)
+
+
+def test_transformed_rows_past_the_range_of_float16():
+    D, F, E = 256, 384, 2
+    r = np.random.default_rng(12)
+    gu, gw = pack(r, E, 2 * F, D)
+    dn, dw = pack(r, E, D, F)
+    L = W.custom_linear(51, 1, D, 16, 2)
+    rot = rl.paro_rotation_prepare(L.pairs, L.theta, L.scale)
+    v = r.normal(0, 1, (3, D))
+    v[1, np.argmin(L.scale)] = 2.0 ** 17
+    x = O.untransform_activations(v, L.pairs, L.theta, L.scale).astype(np.float16)
+    x64 = np.asarray(O.transform_activations(x, L.pairs, L.theta, L.scale), np.float64)
+    assert np.isfinite(x).all() and np.abs(x64).max() > 65504
+    ids, w = choose(r, 3, E, 2)
+    want, _ = B.experts(x64, ids, w.astype(np.float64), gw, dw)
+    y = rl.paro_moe_w4a16(torch.from_numpy(x).cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), gu, dn, rot, out_dtype=torch.float32)
+    for m in range(3):
+        assert relative(y[m], want[m]) <= EXACT
+
+
+def test_rows_of_zeros():
+    r = np.random.default_rng(8)
+    M, D, F, E = 12, 256, 384, 2
+    gu, _ = pack(r, E, 2 * F, D)
+    dn, _ = pack(r, E, D, F)
+    x, _ = tokens(r, M, D)
+    ids, w = choose(r, M, E, 1)
+    x[5] = 0
+    y = rl.paro_moe_w4a16(x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), gu, dn)
+    assert not y[5].any() and bool((y[[m for m in range(M) if m != 5]] != 0).any(1).all())
