@@ -252,11 +252,11 @@ hipError_t launch_rows(const RotJobs& J, int grid, hipStream_t st) {
   return hipGetLastError();
 }
 
-// PD: ring depth.
-template <int NT, int R, int PPT, int PD, bool PERM, bool F32, bool LO>
+// PD: ring depth where the pairs divide evenly over the threads (EXACT), PDN otherwise (the range checks take registers).
+template <int NT, int R, int PPT, int PD, bool PERM, bool F32, bool LO, int PDN = PD>
 hipError_t launch_exact(const RotJobs& J, int grid, hipStream_t st) {
   if (J.D / 2 == PPT * NT) return launch_rows<NT, R, PPT, PD, true, PERM, F32, LO>(J, grid, st);
-  return launch_rows<NT, R, PPT, PD, false, PERM, F32, LO>(J, grid, st);
+  return launch_rows<NT, R, PPT, PDN, false, PERM, F32, LO>(J, grid, st);
 }
 
 // Threads, pairs per thread per stage (PPT) and ring depth by row width (the ring is shallower
@@ -276,10 +276,14 @@ hipError_t launch_ppt(const RotJobs& J, int grid, hipStream_t st) {
   // 46.6 -> 40.8 us (2 rows). With 2 or 4 rows the record ring is one stage deep: at 1024
   // threads a deeper ring spills, which was slower still (2048 x 8960: 58.7 us).
   // Past 14336 channels 8 pairs per thread would spill at 1024 threads: 512 threads, 16 pairs each.
+  // Outputs in two parts (LO) of 7 pairs a thread: a ring of two stages spills up to 112 bytes a thread where the range
+  // checks are, and one of one stage nothing (an expert layer of 64 tokens, 2 of 4 experts, 1024 -> 13312, K = 2: 106 us
+  // with two, 98 with one; 13312 -> 1024 197 and 192). At 14336 exactly two spill 16 bytes at most and are ahead (8 tokens,
+  // K = 8, 1024 -> 14336: 59.0 and 60.0 us; 14336 -> 1024 80.5 and 82.5).
   if constexpr (R == 1) {
     if (P <= 4608) return launch_exact<1024, R, 5, 2, PERM, F32, LO>(J, grid, st);
     if (P <= 6144) return launch_exact<1024, R, 6, 2, PERM, F32, LO>(J, grid, st);
-    if (P <= 7168) return launch_exact<1024, R, 7, 2, PERM, F32, LO>(J, grid, st);
+    if (P <= 7168) return launch_exact<1024, R, 7, 2, PERM, F32, LO, (LO ? 1 : 2)>(J, grid, st);
     return launch_exact<512, R, 16, 1, PERM, F32, LO>(J, grid, st);
   } else if constexpr (R == 2) {
     if (P <= 4608) return launch_exact<1024, R, 5, 2, PERM, F32, LO>(J, grid, st);
