@@ -112,3 +112,47 @@ def test_rows_of_zeros():
     x[5] = 0
     y = rl.paro_moe_w4a16(x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), gu, dn)
     assert not y[5].any() and bool((y[[m for m in range(M) if m != 5]] != 0).any(1).all())
+
+
+# A transform's kernel is one of nine by the row's width, each for widths that its threads divide and for others.
+WIDTHS = [640, 1024, 1152, 2048, 2176, 3200, 4096, 4224, 6144, 6272, 10240, 10368, 12288, 12416, 14336, 14464, 16384]
+
+
+def transformed(seed, width, K):
+    """(the library's transform, the oracle's function)"""
+    r = np.random.default_rng([seed, width, K])
+    pairs = np.stack([r.permutation(width).reshape(-1, 2) for _ in range(K)]).astype(np.int32) if K else np.zeros((0, width // 2, 2), np.int32)
+    theta = r.uniform(-np.pi, np.pi, (K, width // 2)).astype(np.float32)
+    scale = np.exp(r.normal(0, 0.3, width)).astype(np.float32)
+    return rl.paro_rotation_prepare(pairs, theta, scale), lambda v: np.asarray(O.transform_activations(v, pairs, theta, scale), np.float64)
+
+
+def experts_against_the_oracle(seed, M, D, F, E, k, K_x, K_a):
+    """K_x, K_a: stages of the transforms, None for no transform."""
+    r = np.random.default_rng([seed, M, D, F, E, k])
+    gu, gw = pack(r, E, 2 * F, D)
+    dn, dw = pack(r, E, D, F)
+    x, x64 = tokens(r, M, D)
+    rot_x, turn_x = (None, lambda v: v) if K_x is None else transformed(1, D, K_x)
+    rot_a, turn_a = (None, None) if K_a is None else transformed(2, F, K_a)
+    ids, w = choose(r, M, E, k)
+    want, _ = B.experts(turn_x(x64), ids, w.astype(np.float64), gw, dw, turn_a)
+    y = rl.paro_moe_w4a16(x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), gu, dn, rot_x, rot_a, out_dtype=torch.float32)
+    # (sums of more products are sums of sums: of 128 in a group, of the groups of a wave, of up to 16 waves; a stage of a
+    # transform costs some U of an element. EXACT leaves room for both)
+    assert relative(y, want) <= EXACT
+
+
+@pytest.mark.parametrize("K", [0, 1, 3])
+@pytest.mark.parametrize("width", WIDTHS)
+def test_transforms_of_every_width(width, K):
+    C.log(f"transforms of {width}, K={K}")
+    experts_against_the_oracle(21, 3, width, 128, 2, 1, K, None)
+    experts_against_the_oracle(22, 3, 128, width, 2, 1, None, K)
+
+
+@pytest.mark.parametrize("width", [640, 1024, 1152, 2048, 2176, 4096])
+def test_transforms_of_many_rows(width):
+    """More rows between the products than the GPU has CUs: two rows to a workgroup."""
+    C.log(f"transforms of many rows of {width}")
+    experts_against_the_oracle(23, 64, 128, width, 5, 5, 2, 2)
