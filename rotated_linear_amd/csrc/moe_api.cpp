@@ -182,6 +182,13 @@ paro_status paro_moe_layer_w4a16(int M, int D, int F, int E, int top_k, const vo
   return experts(M, D, F, E, top_k, x, &r, ids, weights, rot_x, rot_a, gate_up, down, y, ydtype, ws, ws_bytes, stream);
 }
 
+void paro_internal_moe_gate_up_plan(int M, int D, int F, int E, int top_k, int parts, int* waves, int* groups, int* once) {
+  const MoeGateUpPlan p = moe_gate_up_plan(M, D, F, E, top_k, parts);
+  *waves = p.waves;
+  *groups = p.groups;
+  *once = p.once;
+}
+
 void paro_internal_moe_down_plan(int M, int D, int F, int E, int top_k, int* tiles, int* splits) {
   const MoeDownPlan p = moe_down_plan(M, D, F, E, top_k);
   *tiles = p.tiles;

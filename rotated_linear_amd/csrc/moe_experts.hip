@@ -482,24 +482,40 @@ __global__ __launch_bounds__(256) void sum_kernel(const float* part, int splits,
   }
 }
 
-// The experts that a call reaches, where each choice of a token is as good as any other.
+// The experts that a call reaches, where each choice of a token is as good as any other, and the units that those have.
 double reached(int M, int E, int top_k) { return E * (1.0 - std::pow(1.0 - std::min(1.0, double(top_k) / E), M)); }
+double expected_units(int M, int E, int top_k) {
+  if (M <= 16) return reached(M, E, top_k);
+  if (top_k >= E) return E * ((M + 15) / 16);
+  const double p = double(top_k) / E;
+  double sum = 0, chance = std::pow(1.0 - p, M);  // of an expert's having c tokens
+  for (int c = 0; c <= M; ++c) {
+    sum += chance * ((c + 15) / 16);
+    chance *= p / (1.0 - p) * (M - c) / (c + 1);
+  }
+  return E * sum;
+}
 
 // From so many bytes of the reached experts' weights on they are loaded past the caches, and leave those to what is read
 // again. A layer with both products' loads in the caches, gate and up's past them, both: 4 tokens, 2 of 8 experts, 4096 ->
 // 14336 106, 103 and 100 us; 64 tokens, 8 of 64, 4096 -> 1408 143, 141 and 135; 13 tokens, 4 of 60, 1536 -> 1408 65, 62 and 65
 // (82 and 41 MB); one token, 8 of 64, 2048 -> 1024 22.0, 23.0 and 23.1 (18 and 9 MB, which were still in the caches).
+// Where experts have 16 tokens and more, most have several units, which read the same weights, and the caches keep them: 64
+// tokens, 2 of 4 experts, 4096 -> 14336 (32 tokens to an expert) 242 us past the caches, 222 through them; 32 tokens (16 to
+// an expert) 138 and 134; 24 tokens, 1 of 2 (12) 71 and 75; 64 tokens, 8 of 64, 4096 -> 1408 (8) 146 and 151.
 constexpr double kOnceGateUp = 32e6, kOnceDown = 128e6;
+bool weights_once(int M, int D, int F, int E, int top_k, double rows, double least) {  // rows: of weights, half a byte a channel
+  return M * top_k < 16 * E && reached(M, E, top_k) * rows / 2 * F * D >= least;
+}
 
 // Workgroups: as many as the GPU holds at once (16 waves on a CU), and no more than there can be tiles.
-template <int W, int GW, int PARTS = 1>
-hipError_t launch_gate_up(const MoeCall& c, hipStream_t st) {
+template <int W, int GW, int PARTS>
+hipError_t launch_gate_up(const MoeCall& c, bool once, hipStream_t st) {
   const long tiles = long(moe_units_max(c.M, c.E, c.top_k)) * (c.F / 16);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(std::min<long>(tiles, long(kCUs) * (16 / W)))), dim3(64 * W), 0, st, c);
     return hipGetLastError();
   };
-  const bool once = reached(c.M, c.E, c.top_k) * c.F * c.D >= kOnceGateUp;  // (two rows of half a byte)
   return once ? go(gate_up_kernel<W, GW, PARTS, true>) : go(gate_up_kernel<W, GW, PARTS, false>);
 }
 
@@ -514,13 +530,13 @@ static_assert(down_lds(4, PARO_MOE_MAX_M, PARO_MOE_MAX_E + PARO_MOE_MAX_M, PARO_
 int moe_units_max(int M, int E, int top_k) { return std::min(E, M * top_k) + M * top_k / 16; }
 
 // 16, 32 or 64 columns to a workgroup, and how many workgroups share them, by an estimate in microseconds: a CU's time for
-// an item (four groups of an expert's rows), fitted to ten calls of 1 to 64 tokens at 27 cuts each, and the kernel that adds
+// an item (four groups of a unit's rows), fitted to ten calls of 1 to 64 tokens at 27 cuts each, and the kernel that adds
 // the parts. The shares are those that fill the GPU once, or one. Measured, a layer with 16 columns to a workgroup and no shares, with 32, 64 and
 // as many shares as fill the GPU: 4 tokens, 2 of 8 experts, 4096 -> 14336 112, 107 and 106 us; 8 tokens, 4 of 16, 4096 ->
 // 2048 48, 48 and 47; 64 tokens, 8 of 64, 4096 -> 1408 174, 150 and 142; one token, 8 of 64, 2048 -> 1024 21.5, 21.2 and 22.9.
 MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {
   constexpr double kItem[3] = {0.28, 0.39, 0.62}, kSum = 4.0;
-  const double items = reached(M, E, top_k) * ((F / PARO_GROUP + 3) / 4);
+  const double items = expected_units(M, E, top_k) * ((F / PARO_GROUP + 3) / 4);
   MoeDownPlan best{1, 1};
   double least = 1e30;
   for (int i = 0; i < 3; ++i) {
@@ -538,23 +554,41 @@ MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {
   return best;
 }
 
+// Waves, and groups of channels to each (0: any number), by the groups of a row and by the registers that the tokens' rows
+// take: twice as many in two parts. (There, eight waves for 5 to 8 groups: half as many workgroups load the tokens; against
+// four of two groups each, a layer of 50 tokens, 2 of 6 experts, 896 -> 2688 43 us against 47, of 64, 4 of 60, 1024 -> 1408
+// 69 against 67.)
+MoeGateUpPlan moe_gate_up_plan(int M, int D, int F, int E, int top_k, int parts) {
+  const int G = D / PARO_GROUP;
+  const bool once = weights_once(M, D, F, E, top_k, 2, kOnceGateUp);
+  if (parts == 2) {
+    if (G > 32) return {16, 0, once};
+    return G <= 4 ? MoeGateUpPlan{4, 1, once} : G <= 8 ? MoeGateUpPlan{8, 1, once} : G <= 16 ? MoeGateUpPlan{8, 2, once} : MoeGateUpPlan{16, 2, once};
+  }
+  if (G > 64) return {16, 0, once};
+  const int waves = G <= 16 ? 4 : G <= 32 ? 8 : 16;
+  return {waves, std::max((G + waves - 1) / waves, waves > 4 ? 3 : 1), once};
+}
+
 hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st) {
-  const int G = c.D / PARO_GROUP;
-  if (c.x_parts) {  // twice the registers for a group of the tokens' rows
-    // (eight waves for 5 to 8 groups: half as many workgroups load the tokens; against four of two groups each, a layer of 50
-    // tokens, 2 of 6 experts, 896 -> 2688 43 us against 47, of 64, 4 of 60, 1024 -> 1408 69 against 67)
-    if (G <= 8) return G <= 4 ? launch_gate_up<4, 1, 2>(c, st) : launch_gate_up<8, 1, 2>(c, st);
-    if (G <= 32) return G <= 16 ? launch_gate_up<8, 2, 2>(c, st) : launch_gate_up<16, 2, 2>(c, st);
-    return launch_gate_up<16, 0, 2>(c, st);
+  const MoeGateUpPlan p = moe_gate_up_plan(c.M, c.D, c.F, c.E, c.top_k, c.x_parts ? 2 : 1);
+  const auto is = [&](int waves, int groups) { return p.waves == waves && p.groups == groups; };
+  if (c.x_parts) {
+    if (is(4, 1)) return launch_gate_up<4, 1, 2>(c, p.once, st);
+    if (is(8, 1)) return launch_gate_up<8, 1, 2>(c, p.once, st);
+    if (is(8, 2)) return launch_gate_up<8, 2, 2>(c, p.once, st);
+    if (is(16, 2)) return launch_gate_up<16, 2, 2>(c, p.once, st);
+    return launch_gate_up<16, 0, 2>(c, p.once, st);
   }
-  if (G <= 16) {
-    if (G <= 4) return launch_gate_up<4, 1>(c, st);
-    if (G <= 8) return launch_gate_up<4, 2>(c, st);
-    return G <= 12 ? launch_gate_up<4, 3>(c, st) : launch_gate_up<4, 4>(c, st);
-  }
-  if (G <= 32) return G <= 24 ? launch_gate_up<8, 3>(c, st) : launch_gate_up<8, 4>(c, st);
-  if (G <= 64) return G <= 48 ? launch_gate_up<16, 3>(c, st) : launch_gate_up<16, 4>(c, st);
-  return launch_gate_up<16, 0>(c, st);
+  if (is(4, 1)) return launch_gate_up<4, 1, 1>(c, p.once, st);
+  if (is(4, 2)) return launch_gate_up<4, 2, 1>(c, p.once, st);
+  if (is(4, 3)) return launch_gate_up<4, 3, 1>(c, p.once, st);
+  if (is(4, 4)) return launch_gate_up<4, 4, 1>(c, p.once, st);
+  if (is(8, 3)) return launch_gate_up<8, 3, 1>(c, p.once, st);
+  if (is(8, 4)) return launch_gate_up<8, 4, 1>(c, p.once, st);
+  if (is(16, 3)) return launch_gate_up<16, 3, 1>(c, p.once, st);
+  if (is(16, 4)) return launch_gate_up<16, 4, 1>(c, p.once, st);
+  return launch_gate_up<16, 0, 1>(c, p.once, st);
 }
 
 hipError_t launch_moe_down(const MoeCall& c, hipStream_t st) {
@@ -567,7 +601,7 @@ hipError_t launch_moe_down(const MoeCall& c, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(c.D / 16 / p.tiles * p.splits)), dim3(64 * W), lds, st, a);
     return hipGetLastError();
   };
-  const bool once = reached(c.M, c.E, c.top_k) * c.F * c.D / 2 >= kOnceDown;  // (so much is cut into wide columns, nearly always)
+  const bool once = weights_once(c.M, c.D, c.F, c.E, c.top_k, 1, kOnceDown);  // (so much is cut into wide columns, nearly always)
   const bool few = c.M <= kTwoParts;
   if (hipError_t e = p.tiles == 1   ? few ? go(down_kernel<W, 1, 4, 1, false>) : go(down_kernel<W, 1, 2, 2, false>)
                      : p.tiles == 2 ? few ? go(down_kernel<W, 2, 2, 1, false>) : go(down_kernel<W, 2, 2, 2, false>)

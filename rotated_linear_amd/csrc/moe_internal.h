@@ -71,6 +71,11 @@ hipError_t launch_moe_select(const MoeRoute& r, const MoeTables* t, hipStream_t 
 // The tables from given ids and weights, and where x is not nullptr the rows' powers.
 hipError_t launch_moe_group(int M, int D, int E, int top_k, const uint16_t* x, const int32_t* ids, const float* weights, const MoeTables& t,
                             int* power, hipStream_t st);
+struct MoeGateUpPlan {
+  int waves, groups;  // of a workgroup, and of a wave (0: any number)
+  bool once;          // weights past the caches
+};
+MoeGateUpPlan moe_gate_up_plan(int M, int D, int F, int E, int top_k, int parts);  // parts: of x'
 hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st);
 struct MoeDownPlan {
   int tiles, splits;  // 16-column tiles of a workgroup, and the workgroups that share them
@@ -80,5 +85,6 @@ hipError_t launch_moe_down(const MoeCall& c, hipStream_t st);
 
 }  // namespace paro
 
-// For tests, and in no header of the library: how a call's down product is cut.
+// For tests, and in no header of the library: the kernel of a call's gate and up product, and how its down product is cut.
+extern "C" void paro_internal_moe_gate_up_plan(int M, int D, int F, int E, int top_k, int parts, int* waves, int* groups, int* once);
 extern "C" void paro_internal_moe_down_plan(int M, int D, int F, int E, int top_k, int* tiles, int* splits);
