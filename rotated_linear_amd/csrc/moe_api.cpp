@@ -195,4 +195,11 @@ void paro_internal_moe_down_plan(int M, int D, int F, int E, int top_k, int* til
   *splits = p.splits;
 }
 
+void paro_internal_moe_down_kernel(int M, int D, int F, int E, int top_k, int* tiles, int* few, int* once) {
+  const MoeDownPlan p = moe_down_plan(M, D, F, E, top_k);
+  *tiles = p.tiles;
+  *few = p.few;
+  *once = p.once;
+}
+
 }  // extern "C"

@@ -537,7 +537,7 @@ int moe_units_max(int M, int E, int top_k) { return std::min(E, M * top_k) + M *
 MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {
   constexpr double kItem[3] = {0.28, 0.39, 0.62}, kSum = 4.0;
   const double items = expected_units(M, E, top_k) * ((F / PARO_GROUP + 3) / 4);
-  MoeDownPlan best{1, 1};
+  MoeDownPlan best{};
   double least = 1e30;
   for (int i = 0; i < 3; ++i) {
     const int columns = D / 16 >> i, rounds = (columns + kCUs - 1) / kCUs;
@@ -545,12 +545,13 @@ MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {
     auto take = [&](int s, double us) {
       if (us < least) {
         least = us;
-        best = MoeDownPlan{1 << i, s};
+        best = MoeDownPlan{1 << i, s, M <= kTwoParts, false};
       }
     };
     take(1, rounds * items * kItem[i]);
     if (shares > 1) take(shares, items / shares * kItem[i] + kSum);
   }
+  best.once = best.tiles == 4 && weights_once(M, D, F, E, top_k, 1, kOnceDown);  // (so much has wide columns, nearly always)
   return best;
 }
 
@@ -601,12 +602,10 @@ hipError_t launch_moe_down(const MoeCall& c, hipStream_t st) {
     hipLaunchKernelGGL(kernel, dim3(unsigned(c.D / 16 / p.tiles * p.splits)), dim3(64 * W), lds, st, a);
     return hipGetLastError();
   };
-  const bool once = weights_once(c.M, c.D, c.F, c.E, c.top_k, 1, kOnceDown);  // (so much is cut into wide columns, nearly always)
-  const bool few = c.M <= kTwoParts;
-  if (hipError_t e = p.tiles == 1   ? few ? go(down_kernel<W, 1, 4, 1, false>) : go(down_kernel<W, 1, 2, 2, false>)
-                     : p.tiles == 2 ? few ? go(down_kernel<W, 2, 2, 1, false>) : go(down_kernel<W, 2, 2, 2, false>)
-                     : once         ? few ? go(down_kernel<W, 4, 2, 1, true>) : go(down_kernel<W, 4, 2, 2, true>)
-                                    : few ? go(down_kernel<W, 4, 2, 1, false>) : go(down_kernel<W, 4, 2, 2, false>))
+  if (hipError_t e = p.tiles == 1   ? p.few ? go(down_kernel<W, 1, 4, 1, false>) : go(down_kernel<W, 1, 2, 2, false>)
+                     : p.tiles == 2 ? p.few ? go(down_kernel<W, 2, 2, 1, false>) : go(down_kernel<W, 2, 2, 2, false>)
+                     : p.once       ? p.few ? go(down_kernel<W, 4, 2, 1, true>) : go(down_kernel<W, 4, 2, 2, true>)
+                                    : p.few ? go(down_kernel<W, 4, 2, 1, false>) : go(down_kernel<W, 4, 2, 2, false>))
     return e;
   if (p.splits > 1) {
     const int total = c.M * c.D;

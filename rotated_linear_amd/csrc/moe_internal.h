@@ -79,6 +79,8 @@ MoeGateUpPlan moe_gate_up_plan(int M, int D, int F, int E, int top_k, int parts)
 hipError_t launch_moe_gate_up(const MoeCall& c, hipStream_t st);
 struct MoeDownPlan {
   int tiles, splits;  // 16-column tiles of a workgroup, and the workgroups that share them
+  bool few;           // no unit has more than kTwoParts tokens
+  bool once;          // weights past the caches
 };
 MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k);
 hipError_t launch_moe_down(const MoeCall& c, hipStream_t st);
@@ -88,3 +90,4 @@ hipError_t launch_moe_down(const MoeCall& c, hipStream_t st);
 // For tests, and in no header of the library: the kernel of a call's gate and up product, and how its down product is cut.
 extern "C" void paro_internal_moe_gate_up_plan(int M, int D, int F, int E, int top_k, int parts, int* waves, int* groups, int* once);
 extern "C" void paro_internal_moe_down_plan(int M, int D, int F, int E, int top_k, int* tiles, int* splits);
+extern "C" void paro_internal_moe_down_kernel(int M, int D, int F, int E, int top_k, int* tiles, int* few, int* once);

@@ -3,9 +3,11 @@ import ctypes
 
 import pytest
 
-from tests.test_moe_gpu import down_plan
+from tests.test_moe_gpu import LARGE, SIZES, down_plan, test_rotated_experts as _rotated
+from tests.test_moe_values_gpu import MORE, WIDTHS
 
 rl = pytest.importorskip("rotated_linear_amd")
+ROTATED = next(m.args[1] for m in _rotated.pytestmark if m.name == "parametrize")
 
 
 def gate_up_plan(*size, parts=1):
@@ -35,3 +37,22 @@ def test_a_row_fits_its_waves(parts):
         waves, each, _ = gate_up_plan(4, 128 * groups, 256, 8, 2, parts=parts)
         assert waves in (4, 8, 16) and (each == 0 or (waves * each >= groups and parts * each <= 4))
         assert each or groups > 64 // parts
+
+
+def down_kernel(*size):
+    """(16-column tiles of a workgroup, whether no expert can have more than 8 tokens, whether weights go past the caches)"""
+    out = [ctypes.c_int() for _ in range(3)]
+    rl.lib().paro_internal_moe_down_kernel(*size, *map(ctypes.byref, out))
+    return tuple(v.value for v in out)
+
+
+def test_the_gpu_tests_reach_every_kernel():
+    calls = [(*s, 1) for s in SIZES + MORE] + [(*s[:5], 2 if s[5] else 1) for s in LARGE]
+    calls += [(*s[:5], 2) for s in ROTATED] + [(3, w, 128, 2, 1, 2) for w in WIDTHS] + [(3, 128, w, 2, 1, 1) for w in WIDTHS]
+    gate_up = {(parts, *gate_up_plan(*size, parts=parts)) for *size, parts in calls}
+    plain = (4, 1), (4, 2), (4, 3), (4, 4), (8, 3), (8, 4), (16, 3), (16, 4), (16, 0)
+    behind = (4, 1), (8, 1), (8, 2), (16, 2), (16, 0)
+    assert gate_up == {(parts, *plan, once) for parts, plans in ((1, plain), (2, behind)) for plan in plans for once in (0, 1)}
+    down = {(*down_kernel(*size), down_plan(*size)[1] > 1) for *size, _ in calls}
+    assert down >= {(tiles, few, 0, shared) for tiles in (1, 2, 4) for few in (0, 1) for shared in (False, True)}
+    assert {d[:3] for d in down if d[2]} == {(4, 0, 1), (4, 1, 1)}

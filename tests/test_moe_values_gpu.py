@@ -6,7 +6,7 @@ import oracle as O
 import workloads as W
 from oracle import block_oracle as B
 from tests import gpu_common as C
-from tests.test_moe_gpu import choose, pack, tokens
+from tests.test_moe_gpu import choose, pack, test_large_experts as large_experts, tokens
 
 pytestmark = pytest.mark.gpu
 
@@ -112,6 +112,14 @@ def test_rows_of_zeros():
     x[5] = 0
     y = rl.paro_moe_w4a16(x, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), gu, dn)
     assert not y[5].any() and bool((y[[m for m in range(M) if m != 5]] != 0).any(1).all())
+
+
+MORE = [(7, 4096, 256, 9, 2), (8, 4096, 8192, 8, 8)]  # M, D, F, E, top_k: kernels that no other test's sizes reach
+
+
+@pytest.mark.parametrize("M,D,F,E,k", MORE)
+def test_more_sizes(M, D, F, E, k):
+    large_experts(M, D, F, E, k, 0)
 
 
 # A transform's kernel is one of nine by the row's width, each for widths that its threads divide and for others.
