@@ -497,13 +497,15 @@ double expected_units(int M, int E, int top_k) {
 }
 
 // From so many bytes of the reached experts' weights on they are loaded past the caches, and leave those to what is read
-// again. A layer with both products' loads in the caches, gate and up's past them, both: 4 tokens, 2 of 8 experts, 4096 ->
-// 14336 106, 103 and 100 us; 64 tokens, 8 of 64, 4096 -> 1408 143, 141 and 135; 13 tokens, 4 of 60, 1536 -> 1408 65, 62 and 65
-// (82 and 41 MB); one token, 8 of 64, 2048 -> 1024 22.0, 23.0 and 23.1 (18 and 9 MB, which were still in the caches).
+// again. Three sets of weights in turn, a layer with its loads in the caches and past them. Gate and up: 30 MB (8 tokens, 4 of 16 experts, 2048 -> 1024) 30.1
+// and 30.7 us; 46 MB (4, 2 of 8, 4096 -> 2048) 31.9 and 32.6; 60 MB (8, 4 of 16, 2048 -> 2048) 39.9 and 39.0; 132 MB (32, 4 of
+// 32, 4096 -> 1024) 66.2 and 60.2; 265 MB (32, 4 of 32, 4096 -> 2048) 106.4 and 100.0. Down: 21 to 92 MB within 1 % either way,
+// 41 MB (13, 4 of 60, 1536 -> 1408, behind transforms) 62 and 65; 132 MB (32, 4 of 32, 4096 -> 2048) 106.4 and 104.1; 160 MB (4,
+// 2 of 8, 4096 -> 14336) 103 and 100.
 // Where experts have 16 tokens and more, most have several units, which read the same weights, and the caches keep them: 64
 // tokens, 2 of 4 experts, 4096 -> 14336 (32 tokens to an expert) 242 us past the caches, 222 through them; 32 tokens (16 to
 // an expert) 138 and 134; 24 tokens, 1 of 2 (12) 71 and 75; 64 tokens, 8 of 64, 4096 -> 1408 (8) 146 and 151.
-constexpr double kOnceGateUp = 32e6, kOnceDown = 128e6;
+constexpr double kOnceGateUp = 48e6, kOnceDown = 128e6;
 bool weights_once(int M, int D, int F, int E, int top_k, double rows, double least) {  // rows: of weights, half a byte a channel
   return M * top_k < 16 * E && reached(M, E, top_k) * rows / 2 * F * D >= least;
 }
