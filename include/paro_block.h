@@ -114,8 +114,8 @@ typedef struct {
  * be an infinity), else x; with rot_a (F channels), a is the transform of silu(gate) * up, in float32 until its rounding.
  * Both are shared by all experts, whose weights are packed with them. D and F as D in paro.h. A row of x with a NaN or an
  * infinity reaches no other row of y; an expert that no token names is not read. How many tokens share an expert may
- * change the last bits of the float32 sums. ws holds at least
- * paro_moe_workspace_bytes(M, D, F, E, top_k) bytes (else PARO_EWORKSPACE).
+ * change the last bits of the float32 sums. ws holds at least paro_moe_workspace_bytes(M, D, F, E, top_k) bytes (else
+ * PARO_EWORKSPACE), which are enough with transforms and without.
  */
 size_t paro_moe_workspace_bytes(int M, int D, int F, int E, int top_k);
 paro_status paro_moe_w4a16(int M, int D, int F, int E, int top_k, const void* x, const int32_t* ids, const float* weights,

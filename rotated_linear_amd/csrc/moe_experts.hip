@@ -1,8 +1,9 @@
 // The experts' products of a mixture-of-experts layer for a few tokens, on INT4 weights: gate and up with their
 // activation, then down with the sum over a token's experts. Bound by the weights' way from HBM where the experts are
-// large, and by launches where they are not. Measured (in a trace; a copy runs at 4.95 TB/s), gate and up, then down: 4
-// tokens, 2 of 8 experts, 4096 -> 14336 53 us (6.4 TB/s) and 38 us (4.5); 64 tokens, 8 of 64, 4096 -> 1408 74 (5.3) and
-// 48 (4.0); 32 tokens, 4 of 16, 4096 -> 2048 31 (4.6) and 22 (3.2); one token, 8 of 64, 2048 -> 1024 7.7 and 7.7.
+// large, and by launches where they are not. Measured (in a trace; a copy runs at 4.95 TB/s, reading alone at 5.95), gate and
+// up, then down: 4 tokens, 2 of 8 experts, 5 of them reached, 4096 -> 14336 53 us (5.9 TB/s) and 38 us (4.1); 64 tokens, 8
+// of 64, 4096 -> 1408 74 (5.3) and 57 (3.4); 32 tokens, 4 of 16, 4096 -> 2048 30 (4.6) and 21.5 (3.2); one token, 8 of 64,
+// 2048 -> 1024 7.9 and 7.7.
 #include <algorithm>
 #include <cmath>
 
@@ -323,12 +324,12 @@ struct DownArgs {
 // a is in two float16 parts (one would leave an error as large as y's own rounding, 3.2e-4 of a float16 y instead of
 // 2.1e-4). A unit of up to 8 tokens has 8 rows of the matrix products to spare: they take the lower parts, at no cost in
 // loads or products. A fuller unit, which only calls of more tokens have (PARTS = 2), loads them besides and takes them
-// through products of their own (64 tokens, 8 of 64 experts, 4096 -> 1408: 48 -> 56 us). Those loads come in front of the
+// through products of their own (64 tokens, 8 of 64 experts, 4096 -> 1408: 57 us, 48 without). Those loads come in front of the
 // group's others: the waits count as if they were not there, and so wait for no weights that are asked for later.
 //
 // What bounds it is what a CU takes in, some 38 KB a microsecond here (weights from HBM and a from the L2 cache; more
-// groups in flight change nothing): a group of 16 rows of a is four times the bytes of 16 columns' weights, so more
-// columns to a workgroup cost less, as long as there is a workgroup for each CU.
+// groups in flight change nothing): a group of 16 rows of a, or of 8 in two parts, is four times the bytes of 16 columns'
+// weights, so more columns to a workgroup cost less, as long as there is a workgroup for each CU.
 template <int W, int T, int R, int PARTS, bool ONCE>
 __global__ __launch_bounds__(64 * W, T == 4 || (T == 2 && PARTS == 2) ? 2 : 4) void down_kernel(const DownArgs args) {
   static_assert(R == 2 || R == 4, "a group's slot is fixed");
@@ -497,11 +498,11 @@ double expected_units(int M, int E, int top_k) {
 }
 
 // From so many bytes of the reached experts' weights on they are loaded past the caches, and leave those to what is read
-// again. Three sets of weights in turn, a layer with its loads in the caches and past them. Gate and up: 30 MB (8 tokens, 4 of 16 experts, 2048 -> 1024) 30.1
-// and 30.7 us; 46 MB (4, 2 of 8, 4096 -> 2048) 31.9 and 32.6; 60 MB (8, 4 of 16, 2048 -> 2048) 39.9 and 39.0; 132 MB (32, 4 of
-// 32, 4096 -> 1024) 66.2 and 60.2; 265 MB (32, 4 of 32, 4096 -> 2048) 106.4 and 100.0. Down: 21 to 92 MB within 1 % either way,
-// 41 MB (13, 4 of 60, 1536 -> 1408, behind transforms) 62 and 65; 132 MB (32, 4 of 32, 4096 -> 2048) 106.4 and 104.1; 160 MB (4,
-// 2 of 8, 4096 -> 14336) 103 and 100.
+// again. Three sets of weights in turn, a layer with its loads in the caches and past them. Gate and up: 30 MB (8 tokens, 4
+// of 16 experts, 2048 -> 1024) 30.1 and 30.7 us; 46 MB (4, 2 of 8, 4096 -> 2048) 31.9 and 32.6; 60 MB (8, 4 of 16, 2048 ->
+// 2048) 39.9 and 39.0; 132 MB (32, 4 of 32, 4096 -> 1024) 66.2 and 60.2; 265 MB (32, 4 of 32, 4096 -> 2048) 106.4 and 100.0.
+// Down: 21 to 92 MB within 1 % either way, 41 MB (13, 4 of 60, 1536 -> 1408, behind transforms) 62 and 65; 132 MB (32, 4 of
+// 32, 4096 -> 2048) 106.4 and 104.1; 160 MB (4, 2 of 8, 4096 -> 14336) 103 and 100.
 // Where experts have 16 tokens and more, most have several units, which read the same weights, and the caches keep them: 64
 // tokens, 2 of 4 experts, 4096 -> 14336 (32 tokens to an expert) 242 us past the caches, 222 through them; 32 tokens (16 to
 // an expert) 138 and 134; 24 tokens, 1 of 2 (12) 71 and 75; 64 tokens, 8 of 64, 4096 -> 1408 (8) 146 and 151.
@@ -533,7 +534,7 @@ int moe_units_max(int M, int E, int top_k) { return std::min(E, M * top_k) + M *
 
 // 16, 32 or 64 columns to a workgroup, and how many workgroups share them, by an estimate in microseconds: a CU's time for
 // an item (four groups of a unit's rows), fitted to ten calls of 1 to 64 tokens at 27 cuts each, and the kernel that adds
-// the parts. The shares are those that fill the GPU once, or one. Measured, a layer with 16 columns to a workgroup and no shares, with 32, 64 and
+// the parts. The shares are those that fill the GPU once, or one. Measured (with one part of a), a layer with 16 columns to a workgroup and no shares, with 32, 64 and
 // as many shares as fill the GPU: 4 tokens, 2 of 8 experts, 4096 -> 14336 112, 107 and 106 us; 8 tokens, 4 of 16, 4096 ->
 // 2048 48, 48 and 47; 64 tokens, 8 of 64, 4096 -> 1408 174, 150 and 142; one token, 8 of 64, 2048 -> 1024 21.5, 21.2 and 22.9.
 MoeDownPlan moe_down_plan(int M, int D, int F, int E, int top_k) {

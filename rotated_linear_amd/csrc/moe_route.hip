@@ -1,8 +1,9 @@
 // The router of a mixture-of-experts layer: logits, then the experts of each token with their weights.
 //
 // Logits are float64 sums of products that are exact in it: which expert a token takes hangs on the order of two
-// logits, and a float32 sum turns close ones round. Bound by launches: one token, 64 experts, 2048 channels 2.5 us, choice
-// and tables 4.9; 64 tokens, 64 experts, 4096 channels 5.8, choice 4.6, tables 4.7.
+// logits, and a float32 sum turns close ones round. Bound by latency: one token, 64 experts, 2048 channels 2.5 us, little more
+// than a launch, choice and tables 4.8, the round trips to LDS of one workgroup; 64 tokens, 64 experts, 4096 channels 5.8,
+// choice 4.6, tables 4.7.
 #include <algorithm>
 
 #include "moe_tables.h"

@@ -247,7 +247,7 @@ __device__ inline void store_tile(const GemmArgs& a, const Place& p, const i32x4
 // The same for a call with an epilogue. The residual is read as the lanes hold their sums, four columns of a row each, a
 // piece ahead of the one that is worked on. With one tile for each CU this code runs once, from a cold instruction cache,
 // so that its length counts (4096 x 14336 -> 4096 with a residual: 234 us with the pieces unrolled, 223 with the
-// activations in the way, 204 so, the plain product 197; 64 x 4096 -> 14336 with GELU 13.4 us, plain 12.6; 1021 x 1536 ->
+// activations in the way, 200 to 207 so, the plain product 197; 64 x 4096 -> 14336 with GELU 13.4 us, plain 12.6; 1021 x 1536 ->
 // 1537 with a float32 residual 13.2, plain 10.2): one copy of it serves all pieces, whose sums are first moved to registers of their own, and
 // ACT, with an activation, is another. bias: of the wave's column `lane`.
 template <class T, int DT, bool ACT>
